@@ -202,11 +202,11 @@ def own_run(s):
 
     case, op = s["case"], s["case"]["op"]
     if op == "logp":
-        logp, lse, _ = objectives.iso_token_logp(s["logits"], s["labels"], temperature=case["temperature"])
+        logp, norm, _ = objectives.iso_token_logp(s["logits"], s["labels"], temperature=case["temperature"])
         if not case["grad"]:
             return {"logp": logp}
         return {"logp": logp, "dlogits": objectives.iso_token_logp_backward(
-            s["grad"], s["logits"], s["labels"], lse, temperature=case["temperature"])}
+            s["grad"], s["logits"], s["labels"], norm, temperature=case["temperature"])}
     if op == "policy":
         r = objectives.iso_policy_loss(
             s["logits"], s["labels"], s["old"], s["advantages"], s["ref"], clip_low=s["low"], clip_high=s["high"],
