@@ -18,6 +18,10 @@ Entry points (same names as the C ABI):
 * :func:`isotonic` -- differentiable convenience op (autograd), which also
   accepts host tensors (copied to the GPU and back); :func:`isotonic_ragged`,
   its counterpart for a ragged batch.
+
+:mod:`.soft_rank` holds the differentiable soft rank, :mod:`.objectives` the
+training objectives (token log-probabilities, policy, preference and balance
+losses).
 """
 from __future__ import annotations
 
@@ -43,7 +47,10 @@ EXPORTS = ("iso_version", "iso_status_string", "iso_fit_workspace_bytes", "iso_f
            "iso_fit_copy_control_workspace_bytes", "iso_fit_copy_control",
            "iso_fit_f64", "iso_backward_f64", "iso_backward_w_f64", "iso_fit_ragged_f64",
            "iso_profile_enable", "iso_profile_read", "iso_bridge_stats_mode",
-           "iso_bridge_stats_read")
+           "iso_bridge_stats_read", "iso_token_logp", "iso_token_logp_backward",
+           "iso_policy_loss_workspace_bytes", "iso_policy_loss",
+           "iso_preference_loss_workspace_bytes", "iso_preference_loss",
+           "iso_balance_loss_workspace_bytes", "iso_balance_loss", "iso_balance_loss_backward")
 
 _lib = None
 _lock = threading.Lock()
@@ -104,6 +111,25 @@ def load_library(path: str | None = None):
         lib.iso_bridge_stats_mode.restype = ci
         lib.iso_bridge_stats_read.argtypes = [ctypes.POINTER(ctypes.c_uint64)]
         lib.iso_bridge_stats_read.restype = ci
+        cf = ctypes.c_float
+        scores = [vp, ci, i64, i64, i64]   # logits, dtype, rows, n, stride
+        lib.iso_token_logp.argtypes = scores + [vp, cf, vp, vp, vp, vp]
+        lib.iso_token_logp_backward.argtypes = scores + [vp, cf, vp, vp, cf, vp, ci, vp, i64, vp]
+        lib.iso_policy_loss_workspace_bytes.argtypes = [i64]
+        lib.iso_policy_loss.argtypes = (scores + [vp, cf, vp, vp, vp, vp] + [cf] * 4 + [vp] * 6
+                                        + [i64, vp, sz, vp, vp])
+        lib.iso_preference_loss_workspace_bytes.argtypes = [i64, i64]
+        lib.iso_preference_loss.argtypes = (scores + [vp, vp, i64, vp, ci, cf, cf, ci, cf]
+                                            + [vp] * 7 + [i64, vp, sz, vp, vp, vp])
+        lib.iso_balance_loss_workspace_bytes.argtypes = [i64, i64]
+        lib.iso_balance_loss.argtypes = scores + [ci, vp, ci] + [vp] * 6 + [sz, vp]
+        lib.iso_balance_loss_backward.argtypes = (scores + [ci, vp, ci] + [vp] * 5
+                                                  + [cf, vp, vp, i64, vp])
+        for name in ("policy", "preference", "balance"):
+            getattr(lib, f"iso_{name}_loss_workspace_bytes").restype = sz
+            getattr(lib, f"iso_{name}_loss").restype = ci
+        for name in ("iso_token_logp", "iso_token_logp_backward", "iso_balance_loss_backward"):
+            getattr(lib, name).restype = ci
         _lib = lib
         return lib
 

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libiso.so")
 SOURCES = ("iso_api.cu", "iso_rows.cu", "iso_rows_f64.cu", "iso_long.cu", "iso_long_f64.cu",
-           "iso_backward.cu", "iso_noalloc.cu", "iso_ragged.cu")
+           "iso_backward.cu", "iso_noalloc.cu", "iso_ragged.cu",
+           "obj_api.cu", "obj_scores.cu", "obj_balance.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-Xptxas", "-warn-spills"]

@@ -1,0 +1,442 @@
+"""Training objectives over rows of scores, each with its gradient.
+
+What a model trained on ranks and preferences needs beside the fit: rewards
+calibrated by :func:`iso_fit`, or their :func:`soft_rank.soft_rank`, enter a
+policy or preference loss over the log-probabilities of a model's tokens, and a
+router of experts adds its balance loss.  With ``x`` a row's scores (logits),
+``l`` its label and ``T`` the temperature,
+
+    lp = x[l] / T - log sum_j exp(x[j] / T),   d lp / d x[j] = ([j == l] - p[j]) / T.
+
+Explicit calls (same names and arguments as the C ABI of ``include/iso.h``,
+which states the formulas, the masks and the errors in full):
+
+* :func:`iso_token_logp`, :func:`iso_token_logp_backward`
+* :func:`iso_policy_loss` -- loss and gradient in one call
+* :func:`iso_preference_loss` -- loss and gradient in one call
+* :func:`iso_balance_loss`, :func:`iso_balance_loss_backward`
+
+Differentiable in the scores (autograd): :func:`token_logp`, :func:`policy_loss`,
+:func:`preference_loss`, :func:`balance_loss`.
+
+Scores are float32, bfloat16 or float16 CUDA tensors, ``[rows, n]`` or ``[n]``,
+contiguous within a row (rows may be strided); gradients have their type.
+Labels are int64, and a negative one marks a row that takes no part.  Calls
+run on ``stream`` (default: the current one); what they allocate belongs to it.
+"""
+from __future__ import annotations
+
+import contextlib
+from collections import namedtuple
+
+from . import ISO_OK, IsoError, _check_dev, _torch, load_library
+
+MAX_EXPERTS = 1024   # ISO_MAX_EXPERTS
+MAX_TOP_K = 32       # ISO_MAX_TOP_K
+ISO_ROW_BAD_LABEL = 8
+KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
+
+PolicyLoss = namedtuple("PolicyLoss", "loss stats logp norm coef dlogits row_status")
+PreferenceLoss = namedtuple("PreferenceLoss",
+                            "loss margins seq_logp logp norm coef dlogits row_status pair_status")
+BalanceLoss = namedtuple("BalanceLoss", "loss counts experts gates live mask renormalize")
+
+_dtypes = None
+
+
+def _scores(t, name="logits"):
+    """(dtype code, rows, n, row stride) of a tensor of scores."""
+    global _dtypes
+    torch = _torch()
+    if _dtypes is None:
+        _dtypes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _dtypes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16")
+    if t.dim() == 2:
+        (rows, n), (stride, inner) = t.shape, t.stride()
+    elif t.dim() == 1:
+        rows, n, stride, inner = 1, t.shape[0], t.shape[0], t.stride(0)
+    else:
+        raise ValueError(f"{name} must be [n] or [rows, n]")
+    if n < 1:
+        raise ValueError(f"{name} must have at least one score a row")
+    if inner != 1 and n > 1:
+        raise ValueError(f"{name} must be contiguous within a row")
+    return code, rows, n, stride
+
+
+def _check(t, name, dtype, shape, device):
+    _check_dev(t, name, dtype)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+def _check_out(t, shape, like):
+    """A caller's gradient buffer: (dtype code checked) its row stride."""
+    code, rows, n, stride = _scores(t, "out")
+    if t.dtype != like.dtype or t.shape != shape or t.device != like.device:
+        raise ValueError("out must have the logits' shape, type and device")
+    if rows > 1 and stride < n:
+        raise ValueError("out's rows must not overlap")
+    return stride
+
+
+def _like(t, rows, n, stride):
+    """A gradient's buffer beside the scores t, with their row stride where rows are only
+    padded: its rows are then aligned as theirs."""
+    torch = _torch()
+    if n <= stride <= n + max(64, n >> 3) and t.dim() == 2:
+        return torch.empty_strided((rows, n), (stride, 1), dtype=t.dtype, device=t.device), stride
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device), n
+
+
+@contextlib.contextmanager
+def _entered(device, stream):
+    torch = _torch()
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def _call(name, *args):
+    st = getattr(load_library(), name)(*args)
+    if st != ISO_OK:
+        raise IsoError(st, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(nbytes, workspace, device):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
+    _check_dev(workspace, "workspace", torch.uint8)
+    return workspace, workspace.numel()
+
+
+def _labels(labels, logits, device):
+    _check(labels, "labels", _torch().int64, logits.shape[:-1], device)
+
+
+def iso_token_logp(logits, labels, *, temperature: float = 1.0, stream=None):
+    """The labels' log-probabilities.  Returns ``(logp, norm, row_status)``: float32 of the
+    labels' shape; the rows' largest score and sum of exponentials ``[rows, 2]`` for the
+    backward; int32 ``[rows]``."""
+    torch = _torch()
+    code, rows, n, stride = _scores(logits)
+    dev = logits.device
+    _labels(labels, logits, dev)
+    with _entered(dev, stream) as st:
+        logp = torch.empty(labels.shape, dtype=torch.float32, device=dev)
+        norm = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+        status = torch.empty(rows, dtype=torch.int32, device=dev)
+        _call("iso_token_logp", logits.data_ptr(), code, rows, n, stride, labels.data_ptr(),
+              temperature, logp.data_ptr(), norm.data_ptr(), status.data_ptr(), st)
+    return logp, norm, status
+
+
+def iso_token_logp_backward(grad_logp, logits, labels, norm, *, temperature: float = 1.0,
+                            grad_scale: float = 1.0, grad_scale_dev=None,
+                            changed_only: bool = False, out=None, stream=None):
+    """The gradient of ``grad_scale * grad_scale_dev * sum(grad_logp * logp)`` in the logits.
+    ``norm`` is the forward's.  With ``changed_only`` and ``out`` given, nothing is written
+    when the device scalar ``grad_scale_dev`` is 1."""
+    torch = _torch()
+    code, rows, n, stride = _scores(logits)
+    dev = logits.device
+    _labels(labels, logits, dev)
+    _check(grad_logp, "grad_logp", torch.float32, labels.shape, dev)
+    _check(norm, "norm", torch.float32, (rows, 2), dev)
+    if grad_scale_dev is not None:
+        _check(grad_scale_dev, "grad_scale_dev", torch.float32, torch.Size(()), dev)
+    if changed_only and out is None:
+        raise ValueError("changed_only needs out")
+    with _entered(dev, stream) as st:
+        if out is None:
+            out, out_stride = _like(logits, rows, n, stride)
+        else:
+            out_stride = _check_out(out, logits.shape, logits)
+        _call("iso_token_logp_backward", logits.data_ptr(), code, rows, n, stride,
+              labels.data_ptr(), temperature, norm.data_ptr(), grad_logp.data_ptr(), grad_scale,
+              _ptr(grad_scale_dev), int(changed_only), out.data_ptr(), out_stride, st)
+    return out
+
+
+def iso_policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights=None, *,
+                    clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                    temperature: float = 1.0, grad_scale: float = 1.0, want_grad: bool = True,
+                    out=None, workspace=None, stream=None):
+    """Clipped policy loss with a KL term, and its gradient in the logits, in one pass over
+    them.  Returns a :class:`PolicyLoss`: ``loss`` (scalar), ``stats`` (``[3]``: policy term,
+    KL term, share of clipped rows), ``logp``, ``norm``, ``coef`` (the loss's derivative in
+    ``logp``), ``dlogits`` (None without ``want_grad``; times ``grad_scale``), ``row_status``."""
+    torch = _torch()
+    code, rows, n, stride = _scores(logits)
+    dev, f32 = logits.device, torch.float32
+    _labels(labels, logits, dev)
+    shape = labels.shape
+    _check(old_logp, "old_logp", f32, shape, dev)
+    _check(advantages, "advantages", f32, shape, dev)
+    if ref_logp is not None:
+        _check(ref_logp, "ref_logp", f32, shape, dev)
+    if weights is not None:
+        _check(weights, "weights", f32, shape, dev)
+    lib = load_library()
+    with _entered(dev, stream) as st:
+        ws, ws_bytes = _workspace(lib.iso_policy_loss_workspace_bytes(rows), workspace, dev)
+        loss = torch.empty((), dtype=f32, device=dev)
+        stats = torch.empty(3, dtype=f32, device=dev)
+        logp = torch.empty(shape, dtype=f32, device=dev)
+        norm = torch.empty((rows, 2), dtype=f32, device=dev)
+        coef = torch.empty(shape, dtype=f32, device=dev)
+        status = torch.empty(rows, dtype=torch.int32, device=dev)
+        out_stride = n
+        if out is not None:
+            out_stride = _check_out(out, logits.shape, logits)
+        elif want_grad:
+            out, out_stride = _like(logits, rows, n, stride)
+        _call("iso_policy_loss", logits.data_ptr(), code, rows, n, stride, labels.data_ptr(),
+              temperature, old_logp.data_ptr(), advantages.data_ptr(), _ptr(ref_logp),
+              _ptr(weights), clip_low, clip_high, kl_coef, grad_scale, loss.data_ptr(),
+              stats.data_ptr(), logp.data_ptr(), norm.data_ptr(), coef.data_ptr(), _ptr(out),
+              out_stride, ws.data_ptr(), ws_bytes, status.data_ptr(), st)
+    return PolicyLoss(loss, stats, logp, norm, coef, out, status)
+
+
+def iso_preference_loss(logits, labels, offsets, ref_logp=None, *, kind: str = "sigmoid",
+                        beta: float = 0.1, label_smoothing: float = 0.0, average: bool = False,
+                        grad_scale: float = 1.0, want_grad: bool = True, out=None,
+                        workspace=None, stream=None):
+    """Preference loss over pairs of token sequences laid end to end, and its gradient in the
+    logits.  ``offsets``: int64 CUDA tensor of ``2 * pairs + 1`` entries (not read by the
+    host); sequence ``2q`` is pair q's chosen one, ``2q + 1`` its rejected one.  ``kind``:
+    "sigmoid", "hinge" or "squared".  Returns a :class:`PreferenceLoss`."""
+    torch = _torch()
+    code, rows, n, stride = _scores(logits)
+    dev, f32 = logits.device, torch.float32
+    _labels(labels, logits, dev)
+    _check_dev(offsets, "offsets", torch.int64)
+    if offsets.dim() != 1 or offsets.numel() % 2 != 1 or offsets.device != dev:
+        raise ValueError("offsets must hold 2 * pairs + 1 entries, beside the logits")
+    if kind not in KINDS:
+        raise ValueError(f"kind must be one of {sorted(KINDS)}")
+    if ref_logp is not None:
+        _check(ref_logp, "ref_logp", f32, labels.shape, dev)
+    pairs = offsets.numel() // 2
+    lib = load_library()
+    with _entered(dev, stream) as st:
+        ws, ws_bytes = _workspace(lib.iso_preference_loss_workspace_bytes(rows, pairs), workspace, dev)
+        loss = torch.empty((), dtype=f32, device=dev)
+        margins = torch.empty(pairs, dtype=f32, device=dev)
+        seq_logp = torch.empty(2 * pairs, dtype=f32, device=dev)
+        logp = torch.empty(labels.shape, dtype=f32, device=dev)
+        norm = torch.empty((rows, 2), dtype=f32, device=dev)
+        coef = torch.empty(labels.shape, dtype=f32, device=dev)
+        status = torch.empty(rows, dtype=torch.int32, device=dev)
+        pair_status = torch.empty(pairs, dtype=torch.int32, device=dev)
+        out_stride = n
+        if out is not None:
+            out_stride = _check_out(out, logits.shape, logits)
+        elif want_grad:
+            out, out_stride = _like(logits, rows, n, stride)
+        _call("iso_preference_loss", logits.data_ptr(), code, rows, n, stride, labels.data_ptr(),
+              offsets.data_ptr(), pairs, _ptr(ref_logp), KINDS[kind], beta, label_smoothing,
+              int(bool(average)), grad_scale, loss.data_ptr(), margins.data_ptr(),
+              seq_logp.data_ptr(), logp.data_ptr(), norm.data_ptr(), coef.data_ptr(), _ptr(out),
+              out_stride, ws.data_ptr(), ws_bytes, status.data_ptr(), pair_status.data_ptr(), st)
+    return PreferenceLoss(loss, margins, seq_logp, logp, norm, coef, out, status, pair_status)
+
+
+def _router(logits, top_k, mask):
+    code, tokens, experts, stride = _scores(logits)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [tokens, experts]")
+    if experts > MAX_EXPERTS or not 1 <= top_k <= min(experts, MAX_TOP_K):
+        raise ValueError(f"at most {MAX_EXPERTS} experts, and 1 <= top_k <= min(experts, {MAX_TOP_K})")
+    if mask is not None:
+        torch = _torch()
+        if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
+            mask = mask.view(torch.uint8)
+        _check(mask, "mask", torch.uint8, logits.shape[:1], logits.device)
+    return code, tokens, experts, stride, mask
+
+
+def iso_balance_loss(logits, top_k: int, mask=None, *, renormalize: bool = False, workspace=None,
+                     stream=None):
+    """A router's choice of ``top_k`` experts for each row of ``logits`` ``[tokens, experts]``,
+    its balance loss and the tokens of each expert.  ``mask``: bool or uint8 ``[tokens]``, false
+    where a token takes no part.  Returns a :class:`BalanceLoss`: ``loss`` (scalar), ``counts``
+    (int64 ``[experts]``), ``experts`` (int32 ``[tokens, top_k]``, -1 where none), ``gates``
+    (float32), ``live`` (int64 scalar: the tokens that take part), ``mask``, ``renormalize``."""
+    torch = _torch()
+    code, tokens, experts, stride, mask = _router(logits, top_k, mask)
+    dev = logits.device
+    lib = load_library()
+    with _entered(dev, stream) as st:
+        ws, ws_bytes = _workspace(lib.iso_balance_loss_workspace_bytes(tokens, experts), workspace, dev)
+        loss = torch.empty((), dtype=torch.float32, device=dev)
+        counts = torch.empty(experts, dtype=torch.int64, device=dev)
+        chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
+        gates = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+        live = torch.empty((), dtype=torch.int64, device=dev)
+        _call("iso_balance_loss", logits.data_ptr(), code, tokens, experts, stride, top_k,
+              _ptr(mask), int(bool(renormalize)), loss.data_ptr(), counts.data_ptr(),
+              chosen.data_ptr(), gates.data_ptr(), live.data_ptr(), ws.data_ptr(), ws_bytes, st)
+    return BalanceLoss(loss, counts, chosen, gates, live, mask, bool(renormalize))
+
+
+def iso_balance_loss_backward(logits, result, *, grad_loss: float = 1.0, grad_loss_dev=None,
+                              grad_gates=None, out=None, stream=None):
+    """The gradient of ``grad_loss * grad_loss_dev * loss + sum(grad_gates * gates)`` in the
+    logits, ``result`` being :func:`iso_balance_loss`'s for them."""
+    torch = _torch()
+    shape = result.experts.shape
+    code, tokens, experts, stride, mask = _router(logits, shape[1], result.mask)
+    dev = logits.device
+    _check(result.experts, "experts", torch.int32, (tokens, shape[1]), dev)
+    _check(result.gates, "gates", torch.float32, shape, dev)
+    _check(result.counts, "counts", torch.int64, (experts,), dev)
+    _check(result.live, "live", torch.int64, torch.Size(()), dev)
+    if grad_gates is not None:
+        _check(grad_gates, "grad_gates", torch.float32, shape, dev)
+    if grad_loss_dev is not None:
+        _check(grad_loss_dev, "grad_loss_dev", torch.float32, torch.Size(()), dev)
+    with _entered(dev, stream) as st:
+        if out is None:
+            out, out_stride = _like(logits, tokens, experts, stride)
+        else:
+            out_stride = _check_out(out, logits.shape, logits)
+        _call("iso_balance_loss_backward", logits.data_ptr(), code, tokens, experts, stride,
+              shape[1], _ptr(mask), int(result.renormalize), result.counts.data_ptr(),
+              result.experts.data_ptr(), result.gates.data_ptr(), result.live.data_ptr(),
+              _ptr(grad_gates), grad_loss, _ptr(grad_loss_dev), out.data_ptr(), out_stride, st)
+    return out
+
+
+def _make():
+    torch = _torch()
+
+    class _TokenLogp(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, labels, temperature):
+            logp, norm, _ = iso_token_logp(logits, labels, temperature=temperature)
+            ctx.save_for_backward(logits, labels, norm)
+            ctx.temperature = temperature
+            return logp
+
+        @staticmethod
+        def backward(ctx, g):
+            logits, labels, norm = ctx.saved_tensors
+            return iso_token_logp_backward(g.contiguous(), logits, labels, norm,
+                                           temperature=ctx.temperature), None, None
+
+    def hand_over(ctx, g):
+        # The forward left the gradient for an upstream gradient of 1.  It is handed out once
+        # (rewritten when g is not 1); a further backward through the same graph forms it anew.
+        logits, labels, norm, coef = ctx.saved_tensors
+        held, ctx.dlogits = ctx.dlogits, None
+        return iso_token_logp_backward(coef, logits, labels, norm, temperature=ctx.temperature,
+                                       grad_scale_dev=g.contiguous(),
+                                       changed_only=held is not None, out=held)
+
+    class _PolicyLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, labels, old_logp, advantages, ref_logp, weights, options):
+            r = iso_policy_loss(logits, labels, old_logp, advantages, ref_logp, weights,
+                                want_grad=ctx.needs_input_grad[0], **options)
+            ctx.save_for_backward(logits, labels, r.norm, r.coef)
+            ctx.temperature, ctx.dlogits = options["temperature"], r.dlogits
+            ctx.mark_non_differentiable(r.stats, r.logp)
+            return r.loss, r.stats, r.logp
+
+        @staticmethod
+        def backward(ctx, g, *_):
+            return (hand_over(ctx, g),) + (None,) * 6
+
+    class _PreferenceLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, labels, offsets, ref_logp, options):
+            r = iso_preference_loss(logits, labels, offsets, ref_logp,
+                                    want_grad=ctx.needs_input_grad[0], **options)
+            ctx.save_for_backward(logits, labels, r.norm, r.coef)
+            ctx.temperature, ctx.dlogits = 1.0, r.dlogits
+            ctx.mark_non_differentiable(r.margins, r.seq_logp)
+            return r.loss, r.margins, r.seq_logp
+
+        @staticmethod
+        def backward(ctx, g, *_):
+            return (hand_over(ctx, g),) + (None,) * 4
+
+    class _BalanceLoss(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, top_k, mask, renormalize):
+            ctx.set_materialize_grads(False)
+            r = iso_balance_loss(logits, top_k, mask, renormalize=renormalize)
+            ctx.save_for_backward(logits, r.counts, r.experts, r.gates, r.live, r.mask)
+            ctx.renormalize = renormalize
+            ctx.mark_non_differentiable(r.counts, r.experts)
+            return r.loss, r.gates, r.counts, r.experts
+
+        @staticmethod
+        def backward(ctx, g_loss, g_gates, *_):
+            logits, counts, experts, gates, live, mask = ctx.saved_tensors
+            if g_loss is None and g_gates is None:
+                return (None,) * 4
+            r = BalanceLoss(None, counts, experts, gates, live, mask, ctx.renormalize)
+            return iso_balance_loss_backward(
+                logits, r, grad_loss=0.0 if g_loss is None else 1.0,
+                grad_loss_dev=None if g_loss is None else g_loss.contiguous(),
+                grad_gates=None if g_gates is None else g_gates.contiguous()), None, None, None
+
+    return {"token": _TokenLogp, "policy": _PolicyLoss, "preference": _PreferenceLoss,
+            "balance": _BalanceLoss}
+
+
+_Fn = None
+
+
+def _fn(name):
+    global _Fn
+    if _Fn is None:
+        _Fn = _make()
+    return _Fn[name]
+
+
+def token_logp(logits, labels, temperature: float = 1.0):
+    """Differentiable log-probabilities of the labels (0 where a label is negative)."""
+    return _fn("token").apply(logits, labels, float(temperature))
+
+
+def policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights=None, *,
+                clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                temperature: float = 1.0):
+    """Differentiable clipped policy loss; returns ``(loss, stats, logp)``, of which only the
+    loss carries a gradient (to the logits)."""
+    options = {"clip_low": float(clip_low), "clip_high": float(clip_high),
+               "kl_coef": float(kl_coef), "temperature": float(temperature)}
+    return _fn("policy").apply(logits, labels, old_logp, advantages, ref_logp, weights, options)
+
+
+def preference_loss(logits, labels, offsets, ref_logp=None, *, kind: str = "sigmoid",
+                    beta: float = 0.1, label_smoothing: float = 0.0, average: bool = False):
+    """Differentiable preference loss over pairs of sequences; returns ``(loss, margins,
+    seq_logp)``, of which only the loss carries a gradient (to the logits)."""
+    options = {"kind": kind, "beta": float(beta), "label_smoothing": float(label_smoothing),
+               "average": bool(average)}
+    return _fn("preference").apply(logits, labels, offsets, ref_logp, options)
+
+
+def balance_loss(logits, top_k: int, mask=None, renormalize: bool = False):
+    """Differentiable router: returns ``(loss, gates, counts, experts)``; the loss and the
+    gates carry gradients to the logits."""
+    return _fn("balance").apply(logits, int(top_k), mask, bool(renormalize))

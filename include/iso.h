@@ -1,5 +1,7 @@
 /*
- * iso.h -- C ABI of the GB300 (sm_103a) isotonic-regression library libiso.so.
+ * iso.h -- C ABI of the GB300 (sm_103a) isotonic-regression library libiso.so,
+ * and of the training objectives beside it (token log-probabilities, policy,
+ * preference and balance losses; see "Training objectives" below).
  *
  * The operation ("Merge Hulls Without Copying Vertices: GPU Isotonic Regression",
  * Section 2.1, eq. (1)): for every row y_1..y_n with weights w_i > 0, the unique
@@ -292,6 +294,182 @@ iso_status iso_backward_w_f64(const double *grad, const uint8_t *blocks, const d
  */
 iso_status iso_backward_noalloc(const float *grad, const uint8_t *blocks, const float *w,
                                 int64_t rows, int64_t n, float *out, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Training objectives over rows of scores.
+ *
+ * What a model trained on ranks and preferences needs beside the fit: rewards
+ * that iso_fit calibrates, or their soft ranks, enter a policy or a preference
+ * loss over the log-probabilities of a model's tokens; a router of experts
+ * adds its balance loss.  With x [rows, n] a row's scores (logits), T > 0 the
+ * temperature and l_r the row's label,
+ *
+ *   lp_r = x[r, l_r] / T - log sum_j exp(x[r, j] / T)
+ *   d lp_r / d x[r, j] = ([j == l_r] - p[r, j]) / T,
+ *   p[r, j] = exp(x[r, j] / T) / sum_i exp(x[r, i] / T).
+ *
+ * Conventions, beside those at the top of this file:
+ *  - Scores and their gradients are float32, bfloat16 or float16 (`dtype`);
+ *    everything else is float32 unless said otherwise.  Sums and softmax
+ *    statistics are float32 within a row and float64 across rows; a gradient
+ *    is rounded once, to the scores' type.  Results do not depend on timing:
+ *    the same call gives the same bits.
+ *  - Row r of the scores starts at element r * stride, of the gradient at
+ *    r * out_stride (strides in elements; the gradient's at least n).  1 <= n <=
+ *    2^31 - 1, 0 <= rows <= 2^31 - 1, rows * stride <= 2^40.  Element alignment is enough.
+ *  - labels [rows] int64: a negative label marks a row that takes no part; its
+ *    scores (and its other inputs) are not used, its log-probability is 0 and
+ *    its gradient 0.  A label >= n is an error in the data: the row's
+ *    log-probability is NaN and its row_status has ISO_ROW_BAD_LABEL.
+ *  - A score of -inf is a closed entry of probability 0.  The type's lowest
+ *    value is an ordinary, very small score.  A row with a NaN or +inf, or
+ *    with nothing but -inf, has no probabilities: its log-probability and
+ *    gradient are NaN and its row_status has ISO_ROW_BAD_Y.
+ *  - norm [rows, 2]: the row's largest score and sum_j exp((x[r, j] - largest) / T),
+ *    from which the backward forms p without another pass.
+ * ------------------------------------------------------------------------ */
+typedef enum { ISO_F32 = 0, ISO_BF16 = 1, ISO_F16 = 2 } iso_dtype;
+#define ISO_ROW_BAD_LABEL 8u /* the row's label is not below n                   */
+
+/*
+ * iso_token_logp -- the labels' log-probabilities.
+ *
+ *  logp       [rows], written: lp_r, or 0 for a row without a label.
+ *  norm       [rows, 2], written.
+ *  row_status [rows] uint32, written, or NULL.
+ */
+iso_status iso_token_logp(const void *logits, int dtype, int64_t rows, int64_t n, int64_t stride,
+                          const int64_t *labels, float temperature, float *logp, float *norm,
+                          uint32_t *row_status, void *stream);
+
+/*
+ * iso_token_logp_backward -- dlogits[r, j] = g_r / T ([j == l_r] - p[r, j]) with
+ * g_r = grad_logp[r] * grad_scale * (*grad_scale_dev).
+ *
+ *  norm            what the forward wrote for the same logits and temperature.
+ *  grad_logp       [rows].
+ *  grad_scale_dev  one float on the device, or NULL for 1.
+ *  changed_only    0 or 1.  1: when *grad_scale_dev is 1, nothing is written
+ *                  (dlogits already holds the gradient for a scale of 1, as
+ *                  iso_policy_loss and iso_preference_loss leave it).
+ */
+iso_status iso_token_logp_backward(const void *logits, int dtype, int64_t rows, int64_t n,
+                                   int64_t stride, const int64_t *labels, float temperature,
+                                   const float *norm, const float *grad_logp, float grad_scale,
+                                   const float *grad_scale_dev, int changed_only, void *dlogits,
+                                   int64_t out_stride, void *stream);
+
+/*
+ * iso_policy_loss -- clipped policy loss with a KL term to a reference, and its
+ * gradient in the scores.  Over the labelled rows, with q_r = exp(lp_r - old_logp[r])
+ * and d_r = ref_logp[r] - lp_r,
+ *
+ *   policy_r = max(-A_r q_r, -A_r clip(q_r, 1 - clip_low, 1 + clip_high))
+ *   kl_r     = exp(d_r) - 1 - d_r
+ *   loss     = sum_r w_r (policy_r + kl_coef kl_r)
+ *
+ *  old_logp, advantages  [rows]: log-probabilities when the labels were drawn; A.
+ *  ref_logp   [rows], or NULL: no KL term (kl_coef is then not used).
+ *  weights    [rows]: w, or NULL: 1 / (number of labelled rows).
+ *  clip_low, clip_high   0 <= clip_low <= 1, 0 <= clip_high.
+ *  grad_scale multiplies the gradient only (loss scaling).
+ *  loss       one float, written (0 when no row has a label).
+ *  stats      three floats, written: sum w policy, sum w kl, sum of w over the
+ *             rows whose policy term the clip holds (their policy gradient is 0).
+ *  logp, norm [rows], [rows, 2], written.
+ *  coef       [rows], written: d loss / d lp_r (without grad_scale).
+ *  dlogits    [rows, n] of dtype, written, or NULL: not wanted.
+ *  workspace  iso_policy_loss_workspace_bytes(rows) bytes, 256-byte aligned.
+ */
+size_t iso_policy_loss_workspace_bytes(int64_t rows);
+iso_status iso_policy_loss(const void *logits, int dtype, int64_t rows, int64_t n, int64_t stride,
+                           const int64_t *labels, float temperature, const float *old_logp,
+                           const float *advantages, const float *ref_logp, const float *weights,
+                           float clip_low, float clip_high, float kl_coef, float grad_scale,
+                           float *loss, float *stats, float *logp, float *norm, float *coef,
+                           void *dlogits, int64_t out_stride, void *workspace,
+                           size_t workspace_bytes, uint32_t *row_status, void *stream);
+
+/*
+ * iso_preference_loss -- preference loss over pairs of token sequences, and its
+ * gradient in the scores.  Sequence s holds rows offsets[s] .. offsets[s+1]-1;
+ * pair q's chosen sequence is 2q, its rejected one 2q + 1.  With S_s the sum (or,
+ * average != 0, the mean) of lp over s's labelled rows and R_s the same of ref_logp,
+ *
+ *   h_q = (S_2q - R_2q) - (S_2q+1 - R_2q+1),   z_q = beta h_q
+ *   sigmoid: -(1 - label_smoothing) log sigmoid(z) - label_smoothing log sigmoid(-z)
+ *   hinge:   max(0, 1 - z)
+ *   squared: (h - 1 / (2 beta))^2
+ *   loss = mean over the pairs.
+ *
+ *  offsets    [2 pairs + 1] int64, not read by the host.  A pair with offsets
+ *             out of order or out of [0, rows] gets ISO_ROW_BAD_SHAPE in
+ *             pair_status, and NaN; rows of no sequence get a gradient of 0.
+ *  ref_logp   [rows], or NULL: R = 0.
+ *  loss       one float, written (0 for no pairs).
+ *  margins    [pairs], written: z.       seq_logp [2 pairs], written: S.
+ *  logp, norm, coef   [rows], [rows, 2], [rows], written; coef = d loss / d lp_r.
+ *  dlogits    [rows, n], written, or NULL.
+ *  workspace  iso_preference_loss_workspace_bytes(rows, pairs) bytes, 256-byte aligned.
+ *  row_status, pair_status  [rows], [pairs] uint32, written, or NULL.
+ */
+#define ISO_PREFERENCE_SIGMOID 0
+#define ISO_PREFERENCE_HINGE 1
+#define ISO_PREFERENCE_SQUARED 2
+size_t iso_preference_loss_workspace_bytes(int64_t rows, int64_t pairs);
+iso_status iso_preference_loss(const void *logits, int dtype, int64_t rows, int64_t n,
+                               int64_t stride, const int64_t *labels, const int64_t *offsets,
+                               int64_t pairs, const float *ref_logp, int kind, float beta,
+                               float label_smoothing, int average, float grad_scale, float *loss,
+                               float *margins, float *seq_logp, float *logp, float *norm,
+                               float *coef, void *dlogits, int64_t out_stride, void *workspace,
+                               size_t workspace_bytes, uint32_t *row_status,
+                               uint32_t *pair_status, void *stream);
+
+/*
+ * iso_balance_loss -- a router's choice of top_k experts for each token, its
+ * balance loss and the tokens of each expert.  With p the softmax of a token's
+ * scores, T the live tokens and n_e the tokens that chose e,
+ *
+ *   loss = experts / (top_k T^2) sum_e n_e sum_t p[t, e]     (1 when even)
+ *
+ *  logits     [tokens, experts] of dtype, row t at element t * stride;
+ *             1 <= experts <= ISO_MAX_EXPERTS.
+ *  top_k      1 <= top_k <= min(experts, ISO_MAX_TOP_K).
+ *  mask       [tokens] uint8, or NULL: 0 marks a token that takes no part.  A
+ *             token with nothing but -inf takes no part either.
+ *  renormalize  0: gates are p at the chosen experts; 1: divided by their sum.
+ *  loss       one float, written (0 for no live token).
+ *  counts     [experts] int64, written: n.
+ *  chosen     [tokens, top_k] int32, written: the experts by decreasing score,
+ *             equal scores by increasing index; -1 where no open expert is left (a
+ *             score of -inf or NaN is never chosen) or the token takes no part.
+ *  gates      [tokens, top_k] float32, written: 0 where chosen is -1.
+ *  live       one int64, written: T.
+ *  workspace  iso_balance_loss_workspace_bytes(tokens, experts) bytes, 256-byte aligned.
+ *
+ * iso_balance_loss_backward -- the gradient of grad_loss * (*grad_loss_dev) * loss
+ * + sum grad_gates * gates in the scores (the counts carry none).
+ *
+ *  counts, chosen, gates, live   as the forward wrote them.
+ *  grad_gates    [tokens, top_k], or NULL: 0.
+ *  grad_loss_dev one float on the device, or NULL for 1.
+ *  dlogits       [tokens, experts] of dtype, row t at t * out_stride, written.
+ */
+#define ISO_MAX_EXPERTS 1024
+#define ISO_MAX_TOP_K 32
+size_t iso_balance_loss_workspace_bytes(int64_t tokens, int64_t experts);
+iso_status iso_balance_loss(const void *logits, int dtype, int64_t tokens, int64_t experts,
+                            int64_t stride, int top_k, const uint8_t *mask, int renormalize,
+                            float *loss, int64_t *counts, int32_t *chosen, float *gates,
+                            int64_t *live, void *workspace, size_t workspace_bytes, void *stream);
+iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t tokens,
+                                     int64_t experts, int64_t stride, int top_k,
+                                     const uint8_t *mask, int renormalize, const int64_t *counts,
+                                     const int32_t *chosen, const float *gates,
+                                     const int64_t *live, const float *grad_gates,
+                                     float grad_loss, const float *grad_loss_dev, void *dlogits,
+                                     int64_t out_stride, void *stream);
 
 /*
  * Optional per-kernel timing for benchmarks (not part of the fit).
