@@ -66,9 +66,9 @@ balance_tokens_kernel(RouterArgs a, Balance b, int32_t* __restrict__ chosen,
             }
 #pragma unroll
             for (int i = 0; i < EPL; ++i) soft_raise(st, v[i], kLog2e);
-            const float r = soft_ref(st.m);
+            const SoftRef ref(st.m, kLog2e);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) st.s += ex2((v[i] - r) * kLog2e);
+            for (int i = 0; i < EPL; ++i) st.s += ref.exp(v[i]);
             st = soft_warp(st, kLog2e);
         }
         if (!on || (st.m == -INFINITY && st.s == 0.f)) {
@@ -80,10 +80,11 @@ balance_tokens_kernel(RouterArgs a, Balance b, int32_t* __restrict__ chosen,
         }
         ++tokens;
         const float inv = 1.f / st.s;
+        const SoftRef ref(st.m, kLog2e);
         uint32_t key[EPL];
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            psum[i] += ex2((v[i] - st.m) * kLog2e) * inv;
+            psum[i] += ref.exp(v[i]) * inv;
             key[i] = choice_key(v[i]);
         }
         int mine = -1;
@@ -104,7 +105,7 @@ balance_tokens_kernel(RouterArgs a, Balance b, int32_t* __restrict__ chosen,
             for (int i = 0; i < EPL; ++i)
                 if (at == lane + 32 * i) {
                     key[i] = 0u;
-                    g = ex2((v[i] - st.m) * kLog2e);
+                    g = ref.exp(v[i]);
                     atomicAdd(&sh_n[at], 1u);
                 }
             g = __shfl_sync(~0u, g, at & 31);
@@ -185,9 +186,9 @@ balance_backward_kernel(RouterArgs a, const int64_t* __restrict__ counts,
             }
 #pragma unroll
             for (int i = 0; i < EPL; ++i) soft_raise(st, v[i], kLog2e);
-            const float r = soft_ref(st.m);
+            const SoftRef ref(st.m, kLog2e);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) st.s += ex2((v[i] - r) * kLog2e);
+            for (int i = 0; i < EPL; ++i) st.s += ref.exp(v[i]);
             st = soft_warp(st, kLog2e);
         }
         T* o = out + t * out_stride;
@@ -223,9 +224,10 @@ balance_backward_kernel(RouterArgs a, const int64_t* __restrict__ counts,
             }
         float dot = 0.f;
         const float inv = 1.f / st.s;
+        const SoftRef ref(st.m, kLog2e);
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
-            v[i] = ex2((v[i] - st.m) * kLog2e) * inv;
+            v[i] = ref.exp(v[i]) * inv;
             dot += v[i] * (a.renormalize ? u[i] : u[i] + extra[i]);
         }
 #pragma unroll

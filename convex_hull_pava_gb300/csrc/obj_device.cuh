@@ -1,5 +1,5 @@
-// Device helpers of the training objectives: element types, the running
-// maximum and sum of a softmax, and their reductions.
+// Device helpers of the training objectives: words of scores, the softmax's reference and
+// running state, and their reductions.
 #pragma once
 
 #include <cstdint>
@@ -9,6 +9,7 @@
 namespace isodev {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 // 2^v by the hardware's instruction: relative error about 2^-22, results under
 // 2^-126 become 0 (a probability that small adds nothing to a float32 sum).
@@ -26,57 +27,211 @@ template <> __device__ __forceinline__ float from_f32<float>(float v) { return v
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
 
-// A softmax's running state: the largest score m seen so far and the sum s of
-// exp2((x - m) a), a = log2(e) / temperature.  Differences are formed before
-// the scaling, so that the type's lowest value minus itself is 0 and not an
-// overflow.  A state that has seen nothing, or only -inf, is (-inf, 0); a NaN
-// or +inf among the scores leaves NaN in s.
-struct SoftState {
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 two(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t two(float2 v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(two(a)), "l"(two(b)), "l"(two(c)));
+    return two(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(two(a)), "l"(two(b)));
+    return two(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(two(a)), "l"(two(b)));
+    return two(d);
+}
+
+// A word: 16 bytes of scores.
+template <class T>
+struct Word {
+    static constexpr int N = 16 / (int)sizeof(T);
+};
+
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[2], float) {
+    v[0] = {__uint_as_float(w.x), __uint_as_float(w.y)};
+    v[1] = {__uint_as_float(w.z), __uint_as_float(w.w)};
+}
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[4], __nv_bfloat16) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = {__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)};
+}
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[4], __half) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+}
+__device__ __forceinline__ uint4 pack(const float2 (&v)[2], float) {
+    return {__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y)};
+}
+__device__ __forceinline__ uint4 pack(const float2 (&v)[4], __nv_bfloat16) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[i].x, v[i].y);
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return {u[0], u[1], u[2], u[3]};
+}
+__device__ __forceinline__ uint4 pack(const float2 (&v)[4], __half) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(v[i].x, v[i].y);
+        u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return {u[0], u[1], u[2], u[3]};
+}
+
+// A word of closed entries.
+__device__ __forceinline__ uint4 word_closed(float) { return {0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u}; }
+__device__ __forceinline__ uint4 word_closed(__nv_bfloat16) { return {0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u}; }
+__device__ __forceinline__ uint4 word_closed(__half) { return {0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u, 0xfc00fc00u}; }
+
+// The largest score of a word (NaN are passed over, as by fmaxf).
+__device__ __forceinline__ float word_max(const uint4& w, float) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)),
+                 fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+template <class H2>
+__device__ __forceinline__ H2 word_max2(const uint4& w) {
+    const H2* h = reinterpret_cast<const H2*>(&w);
+    return __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+}
+__device__ __forceinline__ float word_max(const uint4& w, __nv_bfloat16) {
+    const __nv_bfloat162 m = word_max2<__nv_bfloat162>(w);
+    return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float word_max(const uint4& w, __half) {
+    const __half2 m = word_max2<__half2>(w);
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+// Loads and stores of what this call touches once.
+__device__ __forceinline__ void store_streaming(void* p, const uint4& w) {
+    asm volatile("st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+}
+__device__ __forceinline__ uint4 load_streaming(const void* p) {
+    uint4 w;
+    asm volatile("ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(p));
+    return w;
+}
+
+// 16 bytes from global memory into shared memory, behind the caller's back.
+__device__ __forceinline__ void copy_async(void* shared, const void* global) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(shared)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// Every thread of the cluster arrives and waits: shared-memory writes before it, in any of its
+// CTAs, are seen after it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// What scores are taken against in a softmax, a = log2(e) / temperature: exp2(x a - c), with c the
+// float32 product of the largest score m and a.  The one fused operation rounds the difference
+// only, and c's own rounding is the same in every term, in the sum and in the label's, so that it
+// cancels.  Where the product would leave float32's range or come near (a row of the type's lowest
+// value is a softmax as any other) the difference is formed first: exp2((x - m) a).  With nothing
+// but -inf seen, m counts as 0: every -inf then adds 0, and a NaN still shows.
+struct SoftRef {
+    float m, c, a;
+    bool far;
+    __device__ __forceinline__ SoftRef(float top, float scale) {
+        m = top == -INFINITY ? 0.f : top;
+        a = scale;
+        c = __fmul_rn(m, a);
+        far = !(fabsf(c) < 1e30f);
+    }
+    // The exponent of a score.
+    __device__ __forceinline__ float of(float x) const { return far ? (x - m) * a : fmaf(x, a, -c); }
+    __device__ __forceinline__ float exp(float x) const { return ex2(of(x)); }
+    // What turns a sum that was taken against the score `top` into one against this.
+    __device__ __forceinline__ float factor(float top) const {
+        if (top == -INFINITY) return 0.f;
+        return ex2(far ? (top - m) * a : __fmul_rn(top, a) - c);
+    }
+};
+
+// A softmax's running state: the largest score m seen so far and the sum s of the exponentials
+// against it.  A state that has seen nothing, or only -inf, is (-inf, 0); a NaN or +inf among the
+// scores leaves NaN in s.
+struct alignas(8) SoftState {
     float m, s;
 };
 
 __device__ __forceinline__ SoftState soft_empty() { return {-INFINITY, 0.f}; }
 
-// The reference that scores are taken against: with only -inf seen, 0 (every
-// -inf then adds 0, and a NaN still shows).
-__device__ __forceinline__ float soft_ref(float m) { return m == -INFINITY ? 0.f : m; }
-
-// Raises the state's maximum to at least mc.
-__device__ __forceinline__ void soft_raise(SoftState& st, float mc, float a) {
-    if (mc > st.m) {
-        st.s *= ex2((st.m - mc) * a);
-        st.m = mc;
+// Raises the state's maximum to at least `top`.
+__device__ __forceinline__ void soft_raise(SoftState& st, float top, float a) {
+    if (top > st.m) {
+        st.s *= SoftRef(top, a).factor(st.m);
+        st.m = top;
     }
 }
 
-__device__ __forceinline__ SoftState soft_merge(SoftState p, SoftState q, float a) {
-    const float m = fmaxf(p.m, q.m), r = soft_ref(m);
-    // each product rounded by itself: the same bits whichever of the two comes first
-    return {m, __fadd_rn(__fmul_rn(p.s, ex2((p.m - r) * a)), __fmul_rn(q.s, ex2((q.m - r) * a)))};
-}
-
-__device__ __forceinline__ SoftState soft_warp(SoftState st, float a) {
+// The exponentials of a word's scores, in pairs; FAR is ref.far.
+template <class T, bool FAR>
+__device__ __forceinline__ void word_exp(const uint4& w, const SoftRef& ref, float2 (&v)[Word<T>::N / 2]) {
+    unpack(w, v, T());
+    const float2 a2{ref.a, ref.a};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        SoftState q{__shfl_xor_sync(~0u, st.m, o), __shfl_xor_sync(~0u, st.s, o)};
-        st = soft_merge(st, q, a);
+    for (int i = 0; i < Word<T>::N / 2; ++i) {
+        v[i] = FAR ? mul2(add2(v[i], {-ref.m, -ref.m}), a2) : fma2(v[i], a2, {-ref.c, -ref.c});
+        v[i] = {ex2(v[i].x), ex2(v[i].y)};
     }
-    return st;
 }
 
-// Over a CTA of NT threads; `sh` holds NT / 32 states.  Every thread gets the
-// result; ends with the CTA in step, so that `sh` may be used again.
-template <int NT>
-__device__ __forceinline__ SoftState soft_cta(SoftState st, float a, SoftState* sh) {
-    st = soft_warp(st, a);
-    if (NT == 32) return st;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) sh[warp] = st;
-    __syncthreads();
-    st = lane < NT / 32 ? sh[lane] : soft_empty();
-    st = soft_warp(st, a);
-    __syncthreads();
-    return st;
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float warp_add(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    return v;
+}
+
+// Over a warp: the maximum first, then one rescaling of each lane's sum.  Every lane gets the
+// same bits.
+__device__ __forceinline__ SoftState soft_warp(SoftState st, float a) {
+    const float m = warp_max(st.m);
+    return {m, warp_add(st.s * SoftRef(m, a).factor(st.m))};
+}
+
+// Writes a state to the same place of another CTA of the cluster.
+__device__ __forceinline__ void store_remote(SoftState* place, int cta, SoftState st) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(place)), "r"(cta));
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(st.m), "f"(st.s) : "memory");
 }
 
 __device__ __forceinline__ double warp_sum(double v) {

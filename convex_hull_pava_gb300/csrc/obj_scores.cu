@@ -10,14 +10,16 @@
 // log-probability and its gradient are 0.
 #include "obj_internal.h"
 #include "obj_device.cuh"
+#include "iso_internal.h"
 
 #include <algorithm>
+#include <type_traits>
+#define MINB 3
 
 namespace isodev {
 
 namespace {
 
-constexpr int kRowThreads = 256;
 
 inline __host__ __device__ size_t align256o(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -28,10 +30,9 @@ struct PolicyRow {
     float coef, pg, kl, cut;
 };
 
-__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, int64_t r, float logp) {
-    const float w = p.weights ? p.weights[r] : *p.inv_count;
-    const float adv = p.advantages[r];
-    const float ratio = expf(logp - p.old_logp[r]);
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, float logp, float old,
+                                                float adv, float ref, float w) {
+    const float ratio = expf(logp - old);
     const float free = -adv * ratio;
     const float held = -adv * fminf(fmaxf(ratio, p.low), p.high);
     const bool cut = held > free;
@@ -42,93 +43,372 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, int64_t r, 
     q.kl = 0.f;
     if (p.ref_logp) {
         // exp(d) - 1 - d without its cancellation at small d
-        const float d = p.ref_logp[r] - logp, e = expm1f(d);
+        const float d = ref - logp, e = expm1f(d);
         q.kl = w * (e - d);
         q.coef -= p.kl_coef * w * e;
     }
     return q;
 }
 
+// The gradient of a row: h exp(...) throughout, and g more at the label.
+template <class T>
+struct RowGrad {
+    float g, h;
+    SoftRef ref;
+    template <bool FAR>
+    __device__ __forceinline__ uint4 word(const uint4& w) const {
+        float2 v[Word<T>::N / 2];
+        word_exp<T, FAR>(w, ref, v);
+#pragma unroll
+        for (int i = 0; i < Word<T>::N / 2; ++i) v[i] = mul2(v[i], {h, h});
+        return pack(v, T());
+    }
+    __device__ __forceinline__ T one(float x, bool label) const {
+        return from_f32<T>(h * ref.exp(x) + (label ? g : 0.f));
+    }
+};
+
 __device__ __forceinline__ uint32_t norm_status(SoftState st) {
     return isfinite(st.m) && isfinite(st.s) ? 0u : ISO_ROW_BAD_Y;
 }
 
 // What is asked of a row's scores.
-enum class Ask { kLogp, kPolicy, kBackward };
+enum class Ask { kLogp, kPolicy };
 
-// One CTA per row: a pass for the norm (kLogp, kPolicy) and a pass for the gradient.
-template <class T, Ask ASK>
-__global__ void __launch_bounds__(kRowThreads)
-score_rows_kernel(ScoreRows sc, PolicyArgs p, float* __restrict__ logp, float* __restrict__ norm,
-                  float* __restrict__ coef, float grad_scale, const float* grad_scale_dev,
-                  int changed_only, T* __restrict__ out, int64_t out_stride,
-                  uint32_t* __restrict__ row_status) {
-    __shared__ SoftState sh[kRowThreads / 32];
-    __shared__ float sh_coef;
+struct RowOuts {
+    float *logp, *norm, *coef;
+    void* out;
+    int64_t out_stride;
+    int out_words;  // the gradient's rows are aligned as the scores' rows: words can be stored
+    uint32_t* status;
+};
+
+// A row as words of 16 bytes between at most 2 (N - 1) single scores (N a word), of which a CTA
+// of a cluster takes an equal share.
+template <class T>
+struct RowShape {
+    int head, words, tail;  // single scores before the words, words, single scores after
+    int first, count;       // this CTA's words
+    // ctas: a power of two of which `shift` is the exponent, or any number with shift < 0
+    __device__ __forceinline__ RowShape(const T* x, int n, int rank, int ctas, int shift = -1) {
+        constexpr int N = Word<T>::N;
+        const int at = (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (N - 1);
+        head = min(n, (N - at) & (N - 1));
+        words = (n - head) / N;
+        tail = n - head - words * N;
+        const int share = shift < 0 ? (words + ctas - 1) / ctas : (words + ctas - 1) >> shift;
+        first = min(words, rank * share);
+        count = min(words, first + share) - first;
+    }
+    // The thread of a team that has the label's word, or -1.
+    __device__ __forceinline__ int owner(int64_t label, int team) const {
+        const int64_t j = label - head - (int64_t)first * Word<T>::N;
+        return j >= 0 && j < (int64_t)count * Word<T>::N ? (int)(j / Word<T>::N) % team : -1;
+    }
+    // The single score that lane e of the row's first warp takes, or -1.
+    __device__ __forceinline__ int edge(int n, int e) const {
+        return e < head ? e : e < head + tail ? n - tail + (e - head) : -1;
+    }
+};
+
+// A word of a gradient, whole or score by score.
+template <class T>
+__device__ __forceinline__ void store_word(T* at, const uint4& w, bool whole) {
+    if (whole) {
+        store_streaming(at, w);
+    } else {
+        const T* v = reinterpret_cast<const T*>(&w);
+#pragma unroll
+        for (int i = 0; i < Word<T>::N; ++i) at[i] = v[i];
+    }
+}
+
+// What a team has of its next row before that row's turn; the scores' words are on their way to
+// shared memory.
+struct RowAhead {
+    int64_t label;
+    float at_label, edge, old, adv, ref, w;
+};
+
+// Teams of TEAM threads (a warp; a CTA; the CTAs of a cluster) take the rows in turn.  Each thread
+// copies its words of the next row (up to K) to a place of its own in shared memory while it works
+// on the current one, which it holds in registers from the maximum to the gradient: the scores are
+// read once.  A thread reads only what it has copied, so the one thing that a team shares is the
+// row's (maximum, sum); the warps of a cluster write theirs to every CTA and meet once a row.
+// LONG: rows longer than the team's registers are read twice, the second time from L2.
+template <class T, Ask ASK, int NT, int TEAM, int K, bool LONG>
+__global__ void __launch_bounds__(NT, NT * K >= 4096 ? 2 : NT == 128 ? 6 : 3)
+score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
+    constexpr int N = Word<T>::N, W = NT / 32;
+    extern __shared__ uint4 ahead_words[];
+    __shared__ SoftState part[2][TEAM == 32 ? 1 : 8 * W];
+    const int ctas = TEAM == 32 ? 1 : (int)cluster_size(), rank = TEAM == 32 ? 0 : (int)cluster_rank();
+    const int shift = 31 - __clz(ctas);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tt = TEAM == 32 ? lane : threadIdx.x;
+    const int64_t teams = TEAM == 32 ? (int64_t)gridDim.x * W : gridDim.x >> shift;
+    int64_t r = TEAM == 32 ? (int64_t)blockIdx.x * W + warp : blockIdx.x >> shift;
+    uint4* mine = ahead_words + (TEAM == 32 ? warp * 32 * K : 0) + tt;
     const float a = kLog2e * sc.inv_t;
     const int n = sc.n;
-    if (ASK == Ask::kBackward && grad_scale_dev) {
+    const bool edges = rank == 0 && tt < 32;
+    const T* const base = static_cast<const T*>(sc.x);
+
+    auto start = [&](int64_t row, int64_t label) {
+        RowAhead h;
+        h.label = label;
+        h.at_label = h.edge = h.old = h.adv = h.ref = h.w = 0.f;
+        if (label >= 0) {
+            const T* x = base + row * sc.stride;
+            const RowShape<T> s(x, n, rank, ctas, shift);
+            if (!LONG) {
+                const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first + tt;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (tt + k * TEAM < s.count) copy_async(mine + k * TEAM, src + k * TEAM);
+            }
+            h.at_label = label < n ? to_f32(x[label]) : NAN;
+            const int e = edges ? s.edge(n, tt) : -1;
+            h.edge = e >= 0 ? to_f32(x[e]) : -INFINITY;
+            if (ASK == Ask::kPolicy) {
+                h.old = p.old_logp[row];
+                h.adv = p.advantages[row];
+                if (p.ref_logp) h.ref = p.ref_logp[row];
+                if (p.weights) h.w = p.weights[row];
+            }
+        }
+        copy_async_commit();
+        return h;
+    };
+
+    if (r >= sc.rows) return;
+    int64_t label_next = r + teams < sc.rows ? sc.labels[r + teams] : -1;
+    RowAhead cur = start(r, sc.labels[r]), next;
+    const float inv_count = ASK == Ask::kPolicy && !p.weights ? *p.inv_count : 0.f;
+    for (int turn = 0; r < sc.rows; r += teams, cur = next) {
+        const int64_t after = r + 2 * teams;
+        const int64_t label_after = after < sc.rows ? sc.labels[after] : -1;
+        const T* x = base + r * sc.stride;
+        const RowShape<T> s(x, n, rank, ctas, shift);
+        const int rounds = (s.count + TEAM - 1) / TEAM;  // the same in all threads, as is what depends on it
+        T* out = static_cast<T*>(o.out) + r * o.out_stride;
+        uint4 w[K];
+        float top = -INFINITY;
+        if (cur.label >= 0) {
+            copy_async_wait_all();
+            top = cur.edge;
+            if (!LONG) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (k < rounds) {
+                        w[k] = mine[k * TEAM];
+                        if (tt + k * TEAM >= s.count) w[k] = word_closed(T());
+                        top = fmaxf(top, word_max(w[k], T()));
+                    }
+            }
+        }
+        next = start(r + teams, label_next);
+        label_next = label_after;
+        if (cur.label < 0) {
+            if (rank == 0 && tt == 0) {
+                o.logp[r] = 0.f;
+                o.norm[2 * r] = 0.f;
+                o.norm[2 * r + 1] = 1.f;
+                if (o.coef) o.coef[r] = 0.f;
+                if (o.status) o.status[r] = 0u;
+                if (ASK == Ask::kPolicy)
+                    for (int i = 0; i < 3; ++i) p.terms[i * sc.rows + r] = 0.f;
+            }
+            if (ASK == Ask::kPolicy && o.out) {
+                if (o.out_words) {
+                    uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
+                    for (int j = tt; j < s.count; j += TEAM) store_streaming(dst + j, uint4{0, 0, 0, 0});
+                    const int e = edges ? s.edge(n, tt) : -1;
+                    if (e >= 0) out[e] = from_f32<T>(0.f);
+                } else {
+                    for (int j = rank * TEAM + tt; j < n; j += ctas * TEAM) out[j] = from_f32<T>(0.f);
+                }
+            }
+            continue;
+        }
+
+        // the warp's sum, against the warp's maximum
+        SoftState st;
+        float2 sum{0.f, 0.f};
+        if (!LONG) {
+            st.m = warp_max(top);
+            const SoftRef ref(st.m, a);
+            auto add = [&](auto far) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (k < rounds) {
+                        float2 v[N / 2];
+                        word_exp<T, decltype(far)::value>(w[k], ref, v);
+#pragma unroll
+                        for (int i = 0; i < N / 2; ++i) sum = add2(sum, v[i]);
+                    }
+            };
+            ref.far ? add(std::true_type()) : add(std::false_type());
+            st.s = warp_add((edges ? ref.exp(cur.edge) : 0.f) + sum.x + sum.y);
+        } else {
+            const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
+            st.m = cur.edge;
+            st.s = edges ? SoftRef(st.m, a).exp(cur.edge) : 0.f;
+            for (int j = tt; j < s.count; j += K * TEAM) {
+                float m = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < K; ++k) w[k] = j + k * TEAM < s.count ? src[j + k * TEAM] : word_closed(T());
+#pragma unroll
+                for (int k = 0; k < K; ++k) m = fmaxf(m, word_max(w[k], T()));
+                soft_raise(st, m, a);
+                const SoftRef ref(st.m, a);
+                sum = {0.f, 0.f};
+                auto add = [&](auto far) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        float2 v[N / 2];
+                        word_exp<T, decltype(far)::value>(w[k], ref, v);
+#pragma unroll
+                        for (int i = 0; i < N / 2; ++i) sum = add2(sum, v[i]);
+                    }
+                };
+                ref.far ? add(std::true_type()) : add(std::false_type());
+                st.s += sum.x + sum.y;
+            }
+            st = soft_warp(st, a);
+        }
+        if (TEAM != 32) {
+            // Two sets of places in turn: a CTA that writes to one again has been through the
+            // meeting in between, for which every thread had read the first.
+            SoftState* slot = part[turn++ & 1];
+            if (ctas == 1) {
+                if (lane == 0) slot[warp] = st;
+                __syncthreads();
+            } else {
+                if (lane < ctas) store_remote(&slot[rank * W + warp], lane, st);
+                __syncwarp();
+                cluster_sync();
+            }
+            constexpr int P = 8 * W / 32;
+            SoftState q[P];
+            float m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                q[i] = lane + 32 * i < ctas * W ? slot[lane + 32 * i] : soft_empty();
+                m = fmaxf(m, q[i].m);
+            }
+            st.m = warp_max(m);
+            const SoftRef ref(st.m, a);
+            float t = 0.f;
+#pragma unroll
+            for (int i = 0; i < P; ++i) t += q[i].s * ref.factor(q[i].m);
+            st.s = warp_add(t);
+        }
+
+        const SoftRef ref(st.m, a);
+        const float lp = ref.of(cur.at_label) * kLn2 - logf(st.s);
+        PolicyRow q{};
+        if (ASK == Ask::kPolicy)
+            q = policy_row(p, lp, cur.old, cur.adv, cur.ref, p.weights ? cur.w : inv_count);
+        if (rank == 0 && tt == 0) {
+            o.logp[r] = lp;
+            o.norm[2 * r] = st.m;
+            o.norm[2 * r + 1] = st.s;
+            if (o.coef) o.coef[r] = q.coef;
+            if (o.status) o.status[r] = norm_status(st) | (cur.label >= n ? ISO_ROW_BAD_LABEL : 0u);
+            if (ASK == Ask::kPolicy) {
+                p.terms[r] = q.pg;
+                p.terms[sc.rows + r] = q.kl;
+                p.terms[2 * sc.rows + r] = q.cut;
+            }
+        }
+        if (ASK == Ask::kLogp || !o.out) continue;
+
+        const float g = q.coef * p.grad_scale * sc.inv_t;
+        const RowGrad<T> grad{g, -g / st.s, ref};
+        if (!LONG && o.out_words) {
+            uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first + tt;
+            auto give = [&](auto far) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (k < rounds) {
+                        const uint4 d = grad.template word<decltype(far)::value>(w[k]);
+                        if (tt + k * TEAM < s.count) store_streaming(dst + k * TEAM, d);
+                    }
+            };
+            ref.far ? give(std::true_type()) : give(std::false_type());
+        } else {
+            // read again: the row is long, or its gradient lies at other places within 16 bytes
+            const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
+            T* dst = out + s.head + (int64_t)s.first * N;
+            for (int j = tt; j < s.count; j += TEAM) {
+                const uint4 word = src[j];
+                store_word(dst + (int64_t)j * N, ref.far ? grad.template word<true>(word) : grad.template word<false>(word), o.out_words);
+            }
+        }
+        const int e = edges ? s.edge(n, tt) : -1;
+        if (e >= 0) out[e] = grad.one(cur.edge, e == cur.label);
+        // the label's score again, by the thread that has just written its word
+        if (s.owner(cur.label, TEAM) == tt) out[cur.label] = grad.one(cur.at_label, true);
+    }
+    copy_async_wait_all();
+}
+
+// out = g (onehot - p) with g from the rows' coefficients: a CTA takes K words a thread of one
+// row, from the last row to the first (the forward has read them in order, so that the last
+// ones are in L2).
+template <class T, int NT, int K>
+__global__ void __launch_bounds__(NT)
+score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float* __restrict__ coef,
+                      float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o,
+                      int parts) {
+    constexpr int N = Word<T>::N;
+    if (grad_scale_dev) {
         const float g = *grad_scale_dev;
         if (changed_only && g == 1.f) return;
         grad_scale *= g;
     }
-    for (int64_t r = blockIdx.x; r < sc.rows; r += gridDim.x) {
-        const T* __restrict__ x = static_cast<const T*>(sc.x) + r * sc.stride;
+    const float a = kLog2e * sc.inv_t;
+    const int n = sc.n, tt = threadIdx.x;
+    for (int64_t unit = blockIdx.x; unit < sc.rows * parts; unit += gridDim.x) {
+        const int64_t r = sc.rows - 1 - unit / parts;
+        const int part = (int)(unit % parts);
+        const T* x = static_cast<const T*>(sc.x) + r * sc.stride;
+        T* out = static_cast<T*>(o.out) + r * o.out_stride;
+        const RowShape<T> s(x, n, part, parts);
         const int64_t label = sc.labels[r];
+        const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
+        uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
+        const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
         if (label < 0) {
-            if (ASK != Ask::kBackward && threadIdx.x == 0) {
-                logp[r] = 0.f;
-                norm[2 * r] = 0.f;
-                norm[2 * r + 1] = 1.f;
-                if (coef) coef[r] = 0.f;
-                if (row_status) row_status[r] = 0u;
-                if (ASK == Ask::kPolicy)
-                    for (int i = 0; i < 3; ++i) p.terms[i * sc.rows + r] = 0.f;
+            if (o.out_words) {
+                for (int j = tt; j < s.count; j += NT) store_streaming(dst + j, uint4{0, 0, 0, 0});
+            } else {
+                for (int j = tt; j < s.count * N; j += NT) out[s.head + (int64_t)s.first * N + j] = from_f32<T>(0.f);
             }
-            if (out)
-                for (int j = threadIdx.x; j < n; j += kRowThreads) out[r * out_stride + j] = from_f32<T>(0.f);
+            if (e >= 0) out[e] = from_f32<T>(0.f);
             continue;
         }
-        SoftState st;
-        if (ASK != Ask::kBackward) {
-            st = soft_empty();
-            for (int j = threadIdx.x; j < n; j += kRowThreads) {
-                const float v = to_f32(x[j]);
-                soft_raise(st, v, a);
-                st.s += ex2((v - soft_ref(st.m)) * a);
-            }
-            st = soft_cta<kRowThreads>(st, a, sh);
-            if (threadIdx.x == 0) {
-                const bool bad = label >= n;
-                const float lp = bad ? NAN : (to_f32(x[label]) - st.m) * sc.inv_t - logf(st.s);
-                logp[r] = lp;
-                norm[2 * r] = st.m;
-                norm[2 * r + 1] = st.s;
-                if (row_status) row_status[r] = norm_status(st) | (bad ? ISO_ROW_BAD_LABEL : 0u);
-                if (ASK == Ask::kPolicy) {
-                    const PolicyRow q = policy_row(p, r, lp);
-                    p.terms[r] = q.pg;
-                    p.terms[sc.rows + r] = q.kl;
-                    p.terms[2 * sc.rows + r] = q.cut;
-                    coef[r] = q.coef;
-                    sh_coef = q.coef;
-                } else if (coef) {
-                    coef[r] = 0.f;
+        const float edge = e >= 0 ? to_f32(x[e]) : 0.f;
+        const float m = norm[2 * r], sum = norm[2 * r + 1];
+        const float g = coef[r] * grad_scale * sc.inv_t;
+        const RowGrad<T> grad{g, -g / sum, SoftRef(m, a)};
+        const bool owner = s.owner(label, NT) == tt;
+        const float at_label = owner ? to_f32(x[label]) : 0.f;
+        for (int j = tt; j < s.count; j += K * NT) {
+            uint4 w[K];
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (j + k * NT < s.count) w[k] = load_streaming(src + j + k * NT);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+                if (j + k * NT < s.count) {
+                    const uint4 d = grad.ref.far ? grad.template word<true>(w[k]) : grad.template word<false>(w[k]);
+                    store_word(out + s.head + (int64_t)(s.first + j + k * NT) * N, d, o.out_words);
                 }
-            }
-            if (ASK == Ask::kLogp || !out) continue;
-            __syncthreads();
-        } else {
-            st = {norm[2 * r], norm[2 * r + 1]};
         }
-        const float g = (ASK == Ask::kBackward ? coef[r] : sh_coef) * grad_scale * sc.inv_t;
-        const float h = -g / st.s;
-        for (int j = threadIdx.x; j < n; j += kRowThreads) {
-            float d = h * ex2((to_f32(x[j]) - st.m) * a);
-            if (j == label) d += g;
-            out[r * out_stride + j] = from_f32<T>(d);
-        }
-        __syncthreads();  // sh_coef is read before the next row writes it
+        if (e >= 0) out[e] = grad.one(edge, e == label);
+        if (owner) out[label] = grad.one(at_label, true);
     }
 }
 
@@ -238,41 +518,104 @@ preference_finish_kernel(const float* __restrict__ each, int64_t pairs, float* _
     if (threadIdx.x == 0) *loss = pairs > 0 ? (float)(c / (double)pairs) : 0.f;
 }
 
-template <class T, Ask ASK>
-cudaError_t run_rows(const ScoreRows& s, const PolicyArgs& p, float* logp, float* norm, float* coef,
-                     float grad_scale, const float* grad_scale_dev, int changed_only, void* out,
-                     int64_t out_stride, uint32_t* row_status, cudaStream_t st) {
-    if (s.rows == 0) return cudaSuccess;
-    score_rows_kernel<T, ASK><<<row_grid(s.rows), kRowThreads, 0, st>>>(
-        s, p, logp, norm, coef, grad_scale, grad_scale_dev, changed_only, static_cast<T*>(out),
-        out_stride, row_status);
-    return cudaGetLastError();
+template <class T, Ask ASK, int NT, int TEAM, int K, bool LONG>
+cudaError_t launch_rows(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, int ctas, cudaStream_t st) {
+    auto* kernel = score_rows_kernel<T, ASK, NT, TEAM, K, LONG>;
+    constexpr size_t shared = LONG ? 0 : (size_t)NT * K * 16;
+    cudaLaunchConfig_t c{};
+    c.blockDim = dim3(NT);
+    c.dynamicSmemBytes = shared;
+    c.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = ctas;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = TEAM == 32 ? 0 : 1;
+    // the clusters of this size that the GPU holds at once (a cluster's CTAs share a group of SMs,
+    // so that they are fewer than its SMs alone would take); asked once
+    static int held[64][4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int& fit = held[dev][ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3];
+    if (fit == 0) {
+        if (shared > 48 * 1024 &&
+            (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared)) != cudaSuccess)
+            return e;
+        int n = 0;
+        c.gridDim = dim3((unsigned)(device_sms() * ctas));
+        if (ctas == 1) {
+            if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NT, shared)) != cudaSuccess) return e;
+            n *= device_sms();
+        } else if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &c)) != cudaSuccess) {
+            return e;
+        }
+        fit = std::max(1, n);
+    }
+    const int64_t wanted = TEAM == 32 ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows;
+    c.gridDim = dim3((unsigned)(std::min<int64_t>(wanted, fit) * ctas));
+    return cudaLaunchKernelEx(&c, kernel, s, p, o);
 }
 
-template <Ask ASK, class... A>
-cudaError_t by_type(int dtype, A... args) {
+// By a row's bytes: a warp holds up to 4 KB, a CTA 16, 32 or 64 KB and a cluster up to 8 times that;
+// longer rows are read twice.
+template <class T, Ask ASK>
+cudaError_t run_rows(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, cudaStream_t st) {
+    if (s.rows == 0) return cudaSuccess;
+    const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
+    if (words <= 32 * 8) return launch_rows<T, ASK, 256, 32, 8, false>(s, p, o, 1, st);
+    if (words > 8 * 256 * 16) return launch_rows<T, ASK, 256, 256, 8, true>(s, p, o, 8, st);
+    int ctas = 1;
+    while (words > (int64_t)ctas * 256 * 16) ctas *= 2;
+    // few rows: more CTAs for each, down to a word a thread
+    while (ctas < 8 && s.rows * ctas < device_sms() && words > (int64_t)ctas * 256) ctas *= 2;
+    if (words <= ctas * 128 * 8) return launch_rows<T, ASK, 128, 128, 8, false>(s, p, o, ctas, st);
+    if (words <= ctas * 256 * 8) return launch_rows<T, ASK, 256, 256, 8, false>(s, p, o, ctas, st);
+    return launch_rows<T, ASK, 256, 256, 16, false>(s, p, o, ctas, st);
+}
+
+template <class F>
+cudaError_t by_type(int dtype, F f) {
     switch (dtype) {
-        case ISO_F32: return run_rows<float, ASK>(args...);
-        case ISO_BF16: return run_rows<__nv_bfloat16, ASK>(args...);
-        default: return run_rows<__half, ASK>(args...);
+        case ISO_F32: return f(float{});
+        case ISO_BF16: return f(__nv_bfloat16{});
+        default: return f(__half{});
     }
+}
+
+// Whether the gradient's rows start at the same place within 16 bytes as the scores' rows.
+inline int words_agree(const ScoreRows& s, const void* out, int64_t out_stride, int dtype) {
+    const int64_t size = dtype == ISO_F32 ? 4 : 2;
+    const uintptr_t off = reinterpret_cast<uintptr_t>(s.x) ^ reinterpret_cast<uintptr_t>(out);
+    return (off & 15u) == 0 && (s.rows <= 1 || ((s.stride - out_stride) * size) % 16 == 0);
 }
 
 }  // namespace
 
 cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, float* zero_coef,
                        uint32_t* row_status, cudaStream_t st) {
-    return by_type<Ask::kLogp>(dtype, s, PolicyArgs{}, logp, norm, zero_coef, 1.f,
-                               (const float*)nullptr, 0, (void*)nullptr, (int64_t)0, row_status, st);
+    const RowOuts o{logp, norm, zero_coef, nullptr, 0, 0, row_status};
+    return by_type(dtype, [&](auto t) {
+        return run_rows<decltype(t), Ask::kLogp>(s, PolicyArgs{}, o, st);
+    });
 }
 
 cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,
                                 float grad_scale, const float* grad_scale_dev, int changed_only,
                                 void* out, int64_t out_stride, cudaStream_t st) {
-    return by_type<Ask::kBackward>(dtype, s, PolicyArgs{}, (float*)nullptr,
-                                   const_cast<float*>(norm), const_cast<float*>(coef), grad_scale,
-                                   grad_scale_dev, changed_only, out, out_stride,
-                                   (uint32_t*)nullptr, st);
+    if (s.rows == 0) return cudaSuccess;
+    const RowOuts o{nullptr, nullptr, nullptr, out, out_stride, words_agree(s, out, out_stride, dtype), nullptr};
+    return by_type(dtype, [&](auto t) {
+        using T = decltype(t);
+        constexpr int NT = 256, K = 4;
+        const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
+        const int parts = (int)std::max<int64_t>(1, (words + NT * K - 1) / (NT * K));
+        score_backward_kernel<T, NT, K><<<(unsigned)std::min<int64_t>(s.rows * parts, 1 << 30), NT, 0, st>>>(
+            s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, parts);
+        return cudaGetLastError();
+    });
 }
 
 size_t policy_workspace(int64_t rows) { return 256 + align256o((size_t)rows * 12); }
@@ -289,8 +632,8 @@ cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& args, f
         count_labels_kernel<<<1, 1024, 0, st>>>(s.labels, s.rows, inv);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    e = by_type<Ask::kPolicy>(dtype, s, p, p.logp, p.norm, p.coef, p.grad_scale,
-                              (const float*)nullptr, 0, out, out_stride, row_status, st);
+    const RowOuts o{p.logp, p.norm, p.coef, out, out_stride, out ? words_agree(s, out, out_stride, dtype) : 0, row_status};
+    e = by_type(dtype, [&](auto t) { return run_rows<decltype(t), Ask::kPolicy>(s, p, o, st); });
     if (e != cudaSuccess) return e;
     policy_finish_kernel<<<1, 1024, 0, st>>>(p.terms, s.rows, p.kl_coef, loss, stats);
     return cudaGetLastError();
