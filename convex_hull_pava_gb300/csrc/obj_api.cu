@@ -44,7 +44,7 @@ iso_status iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t n
     if (rows == 0) return ISO_OK;
     if (!logits || !labels || !logp || !norm) return ISO_ERR_INVALID_ARG;
     return from_cuda(isodev::token_logp(dtype, score_rows(logits, rows, n, stride, labels, temperature),
-                                        logp, norm, nullptr, row_status,
+                                        logp, norm, nullptr, nullptr, row_status,
                                         static_cast<cudaStream_t>(stream)));
 }
 
@@ -95,9 +95,10 @@ iso_status iso_policy_loss(const void* logits, int dtype, int64_t rows, int64_t 
     p.logp = logp;
     p.norm = norm;
     p.coef = coef;
+    p.loss = loss;
+    p.stats = stats;
     return from_cuda(isodev::policy_loss(
-        dtype, score_rows(logits, rows, n, stride, labels, temperature), p, loss, stats, dlogits,
-        out_stride, workspace, row_status, static_cast<cudaStream_t>(stream)));
+        dtype, score_rows(logits, rows, n, stride, labels, temperature), p, dlogits, out_stride, workspace, row_status, static_cast<cudaStream_t>(stream)));
 }
 
 size_t iso_preference_loss_workspace_bytes(int64_t rows, int64_t pairs) {
@@ -126,7 +127,7 @@ iso_status iso_preference_loss(const void* logits, int dtype, int64_t rows, int6
     if (!workspace_ok(workspace, workspace_bytes, isodev::preference_workspace(rows, pairs)))
         return ISO_ERR_WORKSPACE;
     isodev::PreferenceArgs p{offsets, pairs,   ref_logp, kind,        average, beta,
-                             label_smoothing, loss,    margins,  seq_logp,    pair_status, nullptr};
+                             label_smoothing, loss,    margins,  seq_logp,    pair_status, nullptr, nullptr};
     return from_cuda(isodev::preference_loss(
         dtype, score_rows(logits, rows, n, stride, labels, 1.f), p, logp, norm, coef, grad_scale,
         dlogits, out_stride, workspace, row_status, static_cast<cudaStream_t>(stream)));

@@ -135,6 +135,8 @@ __device__ __forceinline__ void copy_async(void* shared, const void* global) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(shared)), "l"(global) : "memory");
 }
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -234,23 +236,60 @@ __device__ __forceinline__ void store_remote(SoftState* place, int cta, SoftStat
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(st.m), "f"(st.s) : "memory");
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+__device__ __forceinline__ void store_remote(int* place, int cta, int v) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(place)), "r"(cta));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void store_remote(float* place, int cta, float v) {
+    store_remote(reinterpret_cast<int*>(place), cta, __float_as_int(v));
+}
+
+// A float32 sum that keeps what its additions round off: about 48 bits, without 64-bit arithmetic
+// (of which this GPU has little).
+struct alignas(8) Sum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float x) {
+        const float s = __fadd_rn(hi, x), b = __fsub_rn(s, hi);
+        lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b));
+        hi = s;
+    }
+    __device__ __forceinline__ void add(const Sum& q) {
+        add(q.hi);
+        lo += q.lo;
+    }
+    __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
+
+// Over a warp; valid in lane 0.
+__device__ __forceinline__ Sum warp_sum(Sum v) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    for (int o = 16; o > 0; o >>= 1) {
+        Sum q;
+        q.hi = __shfl_down_sync(~0u, v.hi, o);
+        q.lo = __shfl_down_sync(~0u, v.lo, o);
+        v.add(q);
+    }
     return v;
 }
 
-// Sum over a CTA of NT threads, in a fixed order; valid in thread 0.
-template <int NT>
-__device__ __forceinline__ double cta_sum(double v, double* sh) {
-    v = warp_sum(v);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (lane == 0) sh[warp] = v;
+// The kernel that follows in the stream may be launched (it waits for this one's results where it
+// needs them), and such a wait.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Whether this CTA is the last of `ctas` to come here; the others' writes to global memory before
+// it are seen by the last one's threads.  Called by all threads of a CTA.
+__device__ __forceinline__ bool last_to_come(unsigned* ticket, unsigned ctas) {
+    __shared__ bool last;
+    __threadfence();
     __syncthreads();
-    v = lane < NT / 32 ? sh[lane] : 0.0;
-    if (warp == 0) v = warp_sum(v);
+    if (threadIdx.x == 0) last = atomicAdd(ticket, 1u) == ctas - 1;
     __syncthreads();
-    return v;
+    __threadfence();
+    return last;
 }
 
 }  // namespace isodev

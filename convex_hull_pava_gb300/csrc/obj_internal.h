@@ -24,8 +24,8 @@ struct PolicyArgs {
     const float *old_logp, *advantages, *ref_logp, *weights;
     float low, high, kl_coef, grad_scale;
     float *logp, *norm, *coef;
-    float* terms;           // [3][rows] workspace: weighted policy term, KL term, clipped
-    const float* inv_count; // device: 1 / labelled rows (weights == NULL)
+    float *loss, *stats;
+    struct PolicyShared* shared;  // workspace
 };
 
 struct PreferenceArgs {
@@ -36,11 +36,13 @@ struct PreferenceArgs {
     float beta, smooth;
     float *loss, *margins, *seq_logp;
     uint32_t* pair_status;
-    float* each;  // [pairs] workspace
+    unsigned* ticket;  // workspace
+    float* each;       // [pairs] workspace
 };
 
+// With `zero_coef`, that many zeros are written there; with `zero_ticket`, a zero.
 cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, float* zero_coef,
-                       uint32_t* row_status, cudaStream_t st);
+                       unsigned* zero_ticket, uint32_t* row_status, cudaStream_t st);
 // out = grad_scale * (grad_scale_dev ? *grad_scale_dev : 1) * coef (onehot - p) / T;
 // with `changed_only` nothing is written when that device value is 1.
 cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,
@@ -48,9 +50,8 @@ cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm
                                 void* out, int64_t out_stride, cudaStream_t st);
 
 size_t policy_workspace(int64_t rows);
-cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& p, float* loss,
-                        float* stats, void* out, int64_t out_stride, void* ws,
-                        uint32_t* row_status, cudaStream_t st);
+cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& p, void* out,
+                        int64_t out_stride, void* ws, uint32_t* row_status, cudaStream_t st);
 
 size_t preference_workspace(int64_t rows, int64_t pairs);
 cudaError_t preference_loss(int dtype, const ScoreRows& s, PreferenceArgs p, float* logp,

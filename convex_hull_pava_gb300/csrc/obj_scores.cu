@@ -10,9 +10,8 @@
 // log-probability and its gradient are 0.
 #include "obj_internal.h"
 #include "obj_device.cuh"
-#include "iso_internal.h"
+#include "obj_launch.h"
 
-#include <algorithm>
 #include <type_traits>
 #define MINB 3
 
@@ -23,7 +22,26 @@ namespace {
 
 inline __host__ __device__ size_t align256o(size_t x) { return (x + 255) & ~size_t(255); }
 
-inline int row_grid(int64_t rows) { return (int)std::min<int64_t>(rows, 1 << 20); }
+// The most teams of a launch: what the workspace has room for.
+constexpr int64_t kMaxTeams = 32768;
+
+// Partial sums of the policy loss: policy term, KL term, clipped weight.
+struct PolicyTerms {
+    Sum v[3];
+};
+
+}  // namespace
+
+// The policy loss's workspace.  A begin kernel zeroes the ticket and counts the labels; every team
+// leaves its rows' terms; the last CTA adds them up.
+struct PolicyShared {
+    unsigned ticket;
+    float inv_count;
+    char pad[56];
+    PolicyTerms of_team[1];
+};
+
+namespace {
 
 // One row's part of the policy loss, from its log-probability.
 struct PolicyRow {
@@ -141,7 +159,7 @@ __global__ void __launch_bounds__(NT, NT * K >= 4096 ? 2 : NT == 128 ? 6 : 3)
 score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
     constexpr int N = Word<T>::N, W = NT / 32;
     extern __shared__ uint4 ahead_words[];
-    __shared__ SoftState part[2][TEAM == 32 ? 1 : 8 * W];
+    __shared__ SoftState part[2][TEAM == 32 ? 2 : 8 * W];
     const int ctas = TEAM == 32 ? 1 : (int)cluster_size(), rank = TEAM == 32 ? 0 : (int)cluster_rank();
     const int shift = 31 - __clz(ctas);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -181,10 +199,36 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
         return h;
     };
 
-    if (r >= sc.rows) return;
+    PolicyTerms terms;
+    auto finish = [&]() {
+        // the teams' sums, by the last CTA, in the teams' order
+        if (rank == 0 && tt == 0) p.shared->of_team[TEAM == 32 ? blockIdx.x * W + warp : blockIdx.x >> shift] = terms;
+        if (!last_to_come(&p.shared->ticket, gridDim.x)) return;
+        if (warp < 3) {
+            Sum v;
+            for (int64_t i = lane; i < teams; i += 32) {
+                const float2 f = __ldcg(reinterpret_cast<const float2*>(&p.shared->of_team[i].v[warp]));
+                Sum q;
+                q.hi = f.x;
+                q.lo = f.y;
+                v.add(q);
+            }
+            v = warp_sum(v);
+            if (lane == 0) reinterpret_cast<Sum*>(part)[warp] = v;
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            Sum* v = reinterpret_cast<Sum*>(part);
+            for (int i = 0; i < 3; ++i) p.stats[i] = v[i].value();
+            // the KL term's product rounds once
+            *p.loss = p.ref_logp ? fmaf(p.kl_coef, v[1].value(), v[0].value()) : v[0].value();
+        }
+    };
+    let_next_start();
     int64_t label_next = r + teams < sc.rows ? sc.labels[r + teams] : -1;
-    RowAhead cur = start(r, sc.labels[r]), next;
-    const float inv_count = ASK == Ask::kPolicy && !p.weights ? *p.inv_count : 0.f;
+    RowAhead cur = start(r, r < sc.rows ? sc.labels[r] : -1), next;
+    if (ASK == Ask::kPolicy) wait_for_previous();
+    const float inv_count = ASK == Ask::kPolicy && !p.weights ? *(volatile float*)&p.shared->inv_count : 0.f;
     for (int turn = 0; r < sc.rows; r += teams, cur = next) {
         const int64_t after = r + 2 * teams;
         const int64_t label_after = after < sc.rows ? sc.labels[after] : -1;
@@ -216,8 +260,6 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
                 o.norm[2 * r + 1] = 1.f;
                 if (o.coef) o.coef[r] = 0.f;
                 if (o.status) o.status[r] = 0u;
-                if (ASK == Ask::kPolicy)
-                    for (int i = 0; i < 3; ++i) p.terms[i * sc.rows + r] = 0.f;
             }
             if (ASK == Ask::kPolicy && o.out) {
                 if (o.out_words) {
@@ -317,9 +359,9 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
             if (o.coef) o.coef[r] = q.coef;
             if (o.status) o.status[r] = norm_status(st) | (cur.label >= n ? ISO_ROW_BAD_LABEL : 0u);
             if (ASK == Ask::kPolicy) {
-                p.terms[r] = q.pg;
-                p.terms[sc.rows + r] = q.kl;
-                p.terms[2 * sc.rows + r] = q.cut;
+                terms.v[0].add(q.pg);
+                terms.v[1].add(q.kl);
+                terms.v[2].add(q.cut);
             }
         }
         if (ASK == Ask::kLogp || !o.out) continue;
@@ -352,6 +394,169 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
         if (s.owner(cur.label, TEAM) == tt) out[cur.label] = grad.one(cur.at_label, true);
     }
     copy_async_wait_all();
+    if (ASK == Ask::kPolicy) finish();
+}
+
+// The rows of one CTA (or of a cluster's CTAs together) in turn: every `teams`-th, those with a
+// label.  The labels of 32 of them are looked at in one load.
+struct LabelledRows {
+    const int64_t* labels;
+    int64_t rows, teams, block;  // block: the first row of the current 32
+    unsigned left;               // of the current 32, the labelled rows still to come
+    __device__ __forceinline__ LabelledRows(const ScoreRows& sc, int64_t first, int64_t step)
+        : labels(sc.labels), rows(sc.rows), teams(step), block(first - 32 * step), left(0u) {}
+    // Steps to the next labelled row, or to `rows`.  `unlabelled` is called for lane l's row of
+    // each new 32 if it has no label.
+    template <class F>
+    __device__ __forceinline__ int64_t next(F unlabelled) {
+        while (left == 0u) {
+            block += 32 * teams;
+            if (block >= rows) return rows;
+            const int64_t r = block + (threadIdx.x & 31) * teams;
+            const bool has = r < rows && labels[r] >= 0;
+            if (r < rows && !has) unlabelled(r);
+            left = __ballot_sync(~0u, has);
+        }
+        const int l = __ffs(left) - 1;
+        left &= left - 1;
+        return block + l * teams;
+    }
+};
+
+// Log-probabilities alone: a stream of the rows' words through a ring in shared memory, D groups of
+// U words a thread in flight across the ends of rows, a running (maximum, sum) a thread, and one
+// meeting of the CTA (or of a cluster's CTAs) a row, after which all warps but the first go on.
+template <class T, int NT, int U, int D>
+__global__ void __launch_bounds__(NT, 3)
+score_stream_kernel(ScoreRows sc, RowOuts o, unsigned* zero_ticket) {
+    constexpr int N = Word<T>::N, W = NT / 32;
+    extern __shared__ uint4 ring[];
+    __shared__ SoftState part[2][8 * W];
+    const int ctas = (int)cluster_size(), rank = (int)cluster_rank(), shift = 31 - __clz(ctas);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = threadIdx.x;
+    const int64_t teams = gridDim.x >> shift, first = blockIdx.x >> shift;
+    uint4* mine = ring + tt;
+    const float a = kLog2e * sc.inv_t;
+    const int n = sc.n;
+    const bool edges = rank == 0 && warp == 0;
+    const T* const base = static_cast<const T*>(sc.x);
+    if (zero_ticket && blockIdx.x == 0 && tt == 0) *zero_ticket = 0u;
+    let_next_start();
+
+    // what is copied next: group `at` of row `row`
+    LabelledRows ahead(sc, first, teams);
+    int64_t row = -1;
+    int at = 0, groups = 0, count = 0;
+    const uint4* src = nullptr;
+    auto copy_group = [&](int slot) {
+        if (at == groups && row < sc.rows) {
+            row = ahead.next([](int64_t) {});
+            if (row < sc.rows) {
+                const T* x = base + row * sc.stride;
+                const RowShape<T> s(x, n, rank, ctas, shift);
+                src = reinterpret_cast<const uint4*>(x + s.head) + s.first + tt;
+                count = s.count;
+                at = 0;
+                groups = max(1, (count + NT * U - 1) / (NT * U));
+            }
+        }
+        if (at < groups && row < sc.rows) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int j = (at * U + u) * NT;
+                if (tt + j < count) copy_async(mine + (slot * U + u) * NT, src + j);
+            }
+            ++at;
+        }
+        copy_async_commit();
+    };
+#pragma unroll
+    for (int d = 0; d < D; ++d) copy_group(d);
+
+    LabelledRows here(sc, first, teams);
+    int slot = 0, turn = 0;
+    for (;;) {
+        const int64_t r = here.next([&](int64_t q) {
+            if (rank == 0 && warp == 0) {
+                o.logp[q] = 0.f;
+                o.norm[2 * q] = 0.f;
+                o.norm[2 * q + 1] = 1.f;
+                if (o.coef) o.coef[q] = 0.f;
+                if (o.status) o.status[q] = 0u;
+            }
+        });
+        if (r >= sc.rows) break;
+        const T* x = base + r * sc.stride;
+        const RowShape<T> s(x, n, rank, ctas, shift);
+        int64_t label = 0;
+        float at_label = 0.f, edge = -INFINITY;
+        if (edges) {
+            label = sc.labels[r];
+            at_label = label < n ? to_f32(x[label]) : NAN;
+            const int e = s.edge(n, lane);
+            if (e >= 0) edge = to_f32(x[e]);
+        }
+        SoftState st = soft_empty();
+        const int end = max(1, (s.count + NT * U - 1) / (NT * U));
+        for (int g = 0; g < end; ++g) {
+            copy_async_wait<D - 1>();
+            uint4 w[U];
+            float m = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                w[u] = tt + (g * U + u) * NT < s.count ? mine[(slot * U + u) * NT] : word_closed(T());
+                m = fmaxf(m, word_max(w[u], T()));
+            }
+            copy_group(slot);
+            slot = slot + 1 == D ? 0 : slot + 1;
+            soft_raise(st, m, a);
+            const SoftRef ref(st.m, a);
+            float2 sum{0.f, 0.f};
+            auto add = [&](auto far) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    float2 v[N / 2];
+                    word_exp<T, decltype(far)::value>(w[u], ref, v);
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) sum = add2(sum, v[i]);
+                }
+            };
+            ref.far ? add(std::true_type()) : add(std::false_type());
+            st.s += sum.x + sum.y;
+        }
+        if (edges) {
+            soft_raise(st, edge, a);
+            st.s += SoftRef(st.m, a).exp(edge);
+        }
+        st = soft_warp(st, a);
+        SoftState* place = part[turn++ & 1];  // as in score_rows_kernel
+        if (ctas == 1) {
+            if (lane == 0) place[warp] = st;
+            __syncthreads();
+        } else {
+            if (lane == 0) store_remote(&place[rank * W + warp], 0, st);
+            __syncwarp();
+            cluster_sync();
+        }
+        if (!edges) continue;
+        st = soft_empty();
+        for (int i = lane; i < ctas * W; i += 32) {
+            const SoftState q = place[i];
+            soft_raise(st, q.m, a);
+            st.s += q.s * SoftRef(st.m, a).factor(q.m);
+        }
+        st = soft_warp(st, a);
+        if (lane == 0) {
+            o.logp[r] = SoftRef(st.m, a).of(at_label) * kLn2 - logf(st.s);
+            o.norm[2 * r] = st.m;
+            o.norm[2 * r + 1] = st.s;
+            if (o.coef) o.coef[r] = 0.f;
+            if (o.status) o.status[r] = norm_status(st) | (label >= n ? ISO_ROW_BAD_LABEL : 0u);
+        }
+    }
+    copy_async_wait_all();
+    __syncwarp();
+    if (ctas > 1) cluster_sync();  // the first CTA's shared memory outlives the others' writes
 }
 
 // out = g (onehot - p) with g from the rows' coefficients: a CTA takes K words a thread of one
@@ -363,6 +568,7 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
                       float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o,
                       int parts) {
     constexpr int N = Word<T>::N;
+    wait_for_previous();
     if (grad_scale_dev) {
         const float g = *grad_scale_dev;
         if (changed_only && g == 1.f) return;
@@ -412,159 +618,148 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
     }
 }
 
-// 1 / (number of labelled rows), for the mean over them; 0 when there are none.
+// Before the policy loss: its ticket, and 1 / (number of labelled rows); 0 when there are none.
+// One cluster counts, so that nothing has to be zeroed first.
 __global__ void __launch_bounds__(1024)
-count_labels_kernel(const int64_t* __restrict__ labels, int64_t rows, float* __restrict__ inv) {
-    __shared__ double sh[32];
-    double c = 0.0;
-    for (int64_t r = threadIdx.x; r < rows; r += 1024) c += labels[r] >= 0 ? 1.0 : 0.0;
-    c = cta_sum<1024>(c, sh);
-    if (threadIdx.x == 0) *inv = c > 0.0 ? (float)(1.0 / c) : 0.f;
-}
-
-// The rows' terms, summed in 64 bits in a fixed order.
-__global__ void __launch_bounds__(1024)
-policy_finish_kernel(const float* __restrict__ terms, int64_t rows, float kl_coef,
-                     float* __restrict__ loss, float* __restrict__ stats) {
-    __shared__ double sh[32];
-    double v[3];
-    for (int i = 0; i < 3; ++i) {
-        double c = 0.0;
-        for (int64_t r = threadIdx.x; r < rows; r += 1024) c += terms[i * rows + r];
-        v[i] = cta_sum<1024>(c, sh);
+policy_begin_kernel(const int64_t* __restrict__ labels, int64_t rows, PolicyShared* __restrict__ sh) {
+    __shared__ int of_warp[8 * 32];
+    let_next_start();
+    const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int c = 0;
+    if (labels)
+        for (int64_t r = rank * 1024 + threadIdx.x; r < rows; r += ctas * 1024) c += labels[r] >= 0 ? 1 : 0;
+    c = __reduce_add_sync(~0u, c);
+    if (ctas == 1) {
+        if (lane == 0) of_warp[warp] = c;
+        __syncthreads();
+    } else {
+        if (lane == 0) store_remote(&of_warp[rank * 32 + warp], 0, c);
+        __syncwarp();
+        cluster_sync();
     }
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < 3; ++i) stats[i] = (float)v[i];
-        *loss = (float)(v[0] + (double)kl_coef * v[1]);
-    }
-}
-
-// One CTA per pair: the two sequences' sums, the pair's loss and the
-// coefficient of every labelled token of the two.
-__global__ void __launch_bounds__(256)
-preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
-                        const float* __restrict__ logp, float* __restrict__ coef) {
-    __shared__ double sh[8];
-    __shared__ float sh_each[2];
-    for (int64_t q = blockIdx.x; q < p.pairs; q += gridDim.x) {
-        double seq[2], gain[2], count[2];
-        bool bad = false;
-        for (int i = 0; i < 2; ++i) {
-            const int64_t a = p.offsets[2 * q + i], b = p.offsets[2 * q + i + 1];
-            const bool ok = a >= 0 && b >= a && b <= rows;
-            bad = bad || !ok;
-            double s = 0.0, g = 0.0, c = 0.0;
-            if (ok)
-                for (int64_t r = a + threadIdx.x; r < b; r += 256)
-                    if (labels[r] >= 0) {
-                        const double lp = logp[r];
-                        s += lp;
-                        g += p.ref_logp ? lp - (double)p.ref_logp[r] : lp;
-                        c += 1.0;
-                    }
-            seq[i] = cta_sum<256>(s, sh);
-            gain[i] = cta_sum<256>(g, sh);
-            count[i] = cta_sum<256>(c, sh);
+    if (rank == 0 && warp == 0) {
+        c = 0;
+        for (int i = lane; i < ctas * 32; i += 32) c += of_warp[i];
+        c = __reduce_add_sync(~0u, c);
+        if (lane == 0) {
+            sh->ticket = 0u;
+            sh->inv_count = c > 0 ? 1.f / (float)c : 0.f;
         }
+    }
+}
+
+// No rows: the losses of none.
+__global__ void zero_kernel(float* a, int na, float* b, int nb) {
+    if ((int)threadIdx.x < na) a[threadIdx.x] = 0.f;
+    if ((int)threadIdx.x < nb) b[threadIdx.x] = 0.f;
+}
+
+// One CTA per pair, half of it for each of the two sequences: their sums, the pair's loss and the
+// coefficient of every labelled token.  The last CTA adds up the loss.
+__global__ void __launch_bounds__(512)
+preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
+                        const float* logp, float* coef) {
+    constexpr int W = 16;
+    __shared__ Sum sh[3][W];
+    __shared__ float sh_coef[2];
+    let_next_start();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, side = threadIdx.x >> 8, tt = threadIdx.x & 255;
+    bool waited = false;
+    for (int64_t q = blockIdx.x; q < p.pairs; q += gridDim.x) {
+        const int64_t o0 = p.offsets[2 * q], o1 = p.offsets[2 * q + 1], o2 = p.offsets[2 * q + 2];
+        const int64_t a = side ? o1 : o0, b = side ? o2 : o1;
+        const bool ok = a >= 0 && b >= a && b <= rows;
+        const bool bad = !(o0 >= 0 && o1 >= o0 && o2 >= o1 && o2 <= rows);
+        if (!waited) wait_for_previous();
+        waited = true;
+        Sum seq, gain, count;
+        if (ok)
+            for (int64_t r = a + tt; r < b; r += 256)
+                if (labels[r] >= 0) {
+                    const float lp = logp[r];
+                    seq.add(lp);
+                    gain.add(p.ref_logp ? lp - p.ref_logp[r] : lp);
+                    count.add(1.f);
+                }
+        seq = warp_sum(seq);
+        gain = warp_sum(gain);
+        count = warp_sum(count);
+        if (lane == 0) {
+            sh[0][warp] = seq;
+            sh[1][warp] = gain;
+            sh[2][warp] = count;
+        }
+        __syncthreads();
         if (threadIdx.x == 0) {
-            double share[2];
+            float total[3][2], share[2];
+            for (int v = 0; v < 3; ++v)
+                for (int i = 0; i < 2; ++i) {
+                    Sum s;
+                    for (int w = 0; w < W / 2; ++w) s.add(sh[v][i * (W / 2) + w]);
+                    total[v][i] = s.value();
+                }
             for (int i = 0; i < 2; ++i) {
-                share[i] = p.average ? 1.0 / fmax(count[i], 1.0) : 1.0;
-                seq[i] *= share[i];
-                gain[i] *= share[i];
-                p.seq_logp[2 * q + i] = bad ? NAN : (float)seq[i];
+                share[i] = p.average ? 1.f / fmaxf(total[2][i], 1.f) : 1.f;
+                p.seq_logp[2 * q + i] = bad ? NAN : total[0][i] * share[i];
             }
-            const double h = gain[0] - gain[1], beta = p.beta, z = beta * h;
-            double each, slope;  // the pair's loss and its derivative in h
+            const float h = total[1][0] * share[0] - total[1][1] * share[1], beta = p.beta, z = beta * h;
+            float each, slope;  // the pair's loss and its derivative in h
             if (p.kind == ISO_PREFERENCE_SIGMOID) {
-                const double e = exp(-fabs(z)), over = log1p(e);
-                const double up = z >= 0 ? 1.0 / (1.0 + e) : e / (1.0 + e);  // sigmoid(z)
-                const double dn = z >= 0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // sigmoid(-z)
-                each = over + (1.0 - p.smooth) * (z < 0 ? -z : 0.0) + p.smooth * (z > 0 ? z : 0.0);
-                slope = beta * (p.smooth * up - (1.0 - p.smooth) * dn);
+                const float e = expf(-fabsf(z)), over = log1pf(e);
+                const float up = (z >= 0.f ? 1.f : e) / (1.f + e);  // sigmoid(z)
+                const float down = (z >= 0.f ? e : 1.f) / (1.f + e);  // sigmoid(-z)
+                each = over + (1.f - p.smooth) * (z < 0.f ? -z : 0.f) + p.smooth * (z > 0.f ? z : 0.f);
+                slope = beta * (p.smooth * up - (1.f - p.smooth) * down);
             } else if (p.kind == ISO_PREFERENCE_HINGE) {
-                each = z < 1.0 ? 1.0 - z : (z >= 1.0 ? 0.0 : z);
-                slope = z < 1.0 ? -beta : 0.0;
+                each = z < 1.f ? 1.f - z : z >= 1.f ? 0.f : z;
+                slope = z < 1.f ? -beta : 0.f;
             } else {
-                const double d = h - 0.5 / beta;
+                const float d = h - 0.5f / beta;
                 each = d * d;
-                slope = 2.0 * d;
+                slope = 2.f * d;
             }
             if (bad) each = slope = NAN;
-            p.margins[q] = bad ? NAN : (float)z;
-            p.each[q] = (float)each;
+            p.margins[q] = bad ? NAN : z;
+            p.each[q] = each;
             if (p.pair_status) p.pair_status[q] = bad ? ISO_ROW_BAD_SHAPE : 0u;
-            sh_each[0] = (float)(slope * share[0] / (double)p.pairs);
-            sh_each[1] = (float)(-slope * share[1] / (double)p.pairs);
+            sh_coef[0] = slope * share[0] / (float)p.pairs;
+            sh_coef[1] = -slope * share[1] / (float)p.pairs;
         }
         __syncthreads();
-        if (coef)
-            for (int i = 0; i < 2; ++i) {
-                const int64_t a = p.offsets[2 * q + i], b = p.offsets[2 * q + i + 1];
-                if (a < 0 || b < a || b > rows) continue;
-                for (int64_t r = a + threadIdx.x; r < b; r += 256)
-                    if (labels[r] >= 0) coef[r] = sh_each[i];
-            }
-        __syncthreads();
+        if (ok)
+            for (int64_t r = a + tt; r < b; r += 256)
+                if (labels[r] >= 0) coef[r] = sh_coef[side];
     }
-}
-
-__global__ void __launch_bounds__(256)
-preference_finish_kernel(const float* __restrict__ each, int64_t pairs, float* __restrict__ loss) {
-    __shared__ double sh[8];
-    double c = 0.0;
-    for (int64_t q = threadIdx.x; q < pairs; q += 256) c += each[q];
-    c = cta_sum<256>(c, sh);
-    if (threadIdx.x == 0) *loss = pairs > 0 ? (float)(c / (double)pairs) : 0.f;
+    if (!waited) wait_for_previous();
+    if (!last_to_come(p.ticket, gridDim.x)) return;
+    if (warp == 0) {
+        Sum v;
+        for (int64_t q = lane; q < p.pairs; q += 32) v.add(__ldcg(p.each + q));
+        v = warp_sum(v);
+        if (lane == 0) *p.loss = v.value() / (float)p.pairs;
+    }
 }
 
 template <class T, Ask ASK, int NT, int TEAM, int K, bool LONG>
 cudaError_t launch_rows(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, int ctas, cudaStream_t st) {
     auto* kernel = score_rows_kernel<T, ASK, NT, TEAM, K, LONG>;
-    constexpr size_t shared = LONG ? 0 : (size_t)NT * K * 16;
-    cudaLaunchConfig_t c{};
-    c.blockDim = dim3(NT);
-    c.dynamicSmemBytes = shared;
-    c.stream = st;
-    cudaLaunchAttribute at{};
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = ctas;
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.attrs = &at;
-    c.numAttrs = TEAM == 32 ? 0 : 1;
-    // the clusters of this size that the GPU holds at once (a cluster's CTAs share a group of SMs,
-    // so that they are fewer than its SMs alone would take); asked once
+    ClusterLaunch l(1, NT, LONG ? 0 : (size_t)NT * K * 16, ctas, ASK == Ask::kPolicy, st);
     static int held[64][4];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    int fit = 0;
+    const cudaError_t e = clusters_held(kernel, l.c, ctas, held, &fit);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    int& fit = held[dev][ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3];
-    if (fit == 0) {
-        if (shared > 48 * 1024 &&
-            (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)shared)) != cudaSuccess)
-            return e;
-        int n = 0;
-        c.gridDim = dim3((unsigned)(device_sms() * ctas));
-        if (ctas == 1) {
-            if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, NT, shared)) != cudaSuccess) return e;
-            n *= device_sms();
-        } else if ((e = cudaOccupancyMaxActiveClusters(&n, kernel, &c)) != cudaSuccess) {
-            return e;
-        }
-        fit = std::max(1, n);
-    }
     const int64_t wanted = TEAM == 32 ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows;
-    c.gridDim = dim3((unsigned)(std::min<int64_t>(wanted, fit) * ctas));
-    return cudaLaunchKernelEx(&c, kernel, s, p, o);
+    l.c.gridDim = dim3((unsigned)(std::min<int64_t>({wanted, fit, kMaxTeams / (TEAM == 32 ? NT / 32 : 1)}) * ctas));
+    return l(kernel, s, p, o);
 }
 
 // By a row's bytes: a warp holds up to 4 KB, a CTA 16, 32 or 64 KB and a cluster up to 8 times that;
 // longer rows are read twice.
-template <class T, Ask ASK>
-cudaError_t run_rows(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, cudaStream_t st) {
-    if (s.rows == 0) return cudaSuccess;
+template <class T>
+cudaError_t run_policy(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, cudaStream_t st) {
     const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
+    constexpr Ask ASK = Ask::kPolicy;
     if (words <= 32 * 8) return launch_rows<T, ASK, 256, 32, 8, false>(s, p, o, 1, st);
     if (words > 8 * 256 * 16) return launch_rows<T, ASK, 256, 256, 8, true>(s, p, o, 8, st);
     int ctas = 1;
@@ -576,13 +771,32 @@ cudaError_t run_rows(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, 
     return launch_rows<T, ASK, 256, 256, 16, false>(s, p, o, ctas, st);
 }
 
-template <class F>
-cudaError_t by_type(int dtype, F f) {
-    switch (dtype) {
-        case ISO_F32: return f(float{});
-        case ISO_BF16: return f(__nv_bfloat16{});
-        default: return f(__half{});
+// Rows of up to 4 KB by warps; longer ones as a stream, by as many CTAs a row (up to 8) as make
+// the slowest team's share smallest: a row costs a team its groups and about one more for the
+// meeting at its end.
+template <class T>
+cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, unsigned* zero_ticket, cudaStream_t st) {
+    constexpr int NT = 256, U = 4, D = 4;
+    const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
+    auto* kernel = score_stream_kernel<T, NT, U, D>;
+    static int held[64][4];
+    int best = 1, best_fit = 1;
+    double least = 0.0;
+    for (int ctas = 1; ctas <= 8 && (ctas == 1 || words >= (int64_t)ctas * NT); ctas *= 2) {
+        ClusterLaunch l(1, NT, (size_t)NT * U * D * 16, ctas, false, st);
+        int fit = 0;
+        const cudaError_t e = clusters_held(kernel, l.c, ctas, held, &fit);
+        if (e != cudaSuccess) return e;
+        const int64_t groups = (words + (int64_t)ctas * NT * U - 1) / ((int64_t)ctas * NT * U);
+        const double cost = (double)((s.rows + fit - 1) / fit) * (double)(groups + 1);
+        if (ctas == 1 || cost < 0.97 * least) {
+            best = ctas;
+            best_fit = fit;
+            least = cost;
+        }
     }
+    ClusterLaunch l(std::min<int64_t>(s.rows, best_fit) * best, NT, (size_t)NT * U * D * 16, best, false, st);
+    return l(kernel, s, o, zero_ticket);
 }
 
 // Whether the gradient's rows start at the same place within 16 bytes as the scores' rows.
@@ -595,11 +809,9 @@ inline int words_agree(const ScoreRows& s, const void* out, int64_t out_stride, 
 }  // namespace
 
 cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, float* zero_coef,
-                       uint32_t* row_status, cudaStream_t st) {
+                       unsigned* zero_ticket, uint32_t* row_status, cudaStream_t st) {
     const RowOuts o{logp, norm, zero_coef, nullptr, 0, 0, row_status};
-    return by_type(dtype, [&](auto t) {
-        return run_rows<decltype(t), Ask::kLogp>(s, PolicyArgs{}, o, st);
-    });
+    return by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, zero_ticket, st); });
 }
 
 cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,
@@ -612,31 +824,29 @@ cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm
         constexpr int NT = 256, K = 4;
         const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
         const int parts = (int)std::max<int64_t>(1, (words + NT * K - 1) / (NT * K));
-        score_backward_kernel<T, NT, K><<<(unsigned)std::min<int64_t>(s.rows * parts, 1 << 30), NT, 0, st>>>(
-            s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, parts);
-        return cudaGetLastError();
+        ClusterLaunch l(std::min<int64_t>(s.rows * parts, 1 << 30), NT, 0, 1, true, st);
+        return l(score_backward_kernel<T, NT, K>, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, parts);
     });
 }
 
-size_t policy_workspace(int64_t rows) { return 256 + align256o((size_t)rows * 12); }
+size_t policy_workspace(int64_t rows) {
+    return align256o(sizeof(PolicyShared) + (size_t)std::min<int64_t>((rows + 7) / 8 * 8, kMaxTeams) * sizeof(PolicyTerms));
+}
 
-cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& args, float* loss,
-                        float* stats, void* out, int64_t out_stride, void* ws,
-                        uint32_t* row_status, cudaStream_t st) {
+cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& args, void* out,
+                        int64_t out_stride, void* ws, uint32_t* row_status, cudaStream_t st) {
     PolicyArgs p = args;
-    float* inv = static_cast<float*>(ws);
-    p.inv_count = inv;
-    p.terms = inv + 64;
-    cudaError_t e = cudaSuccess;
-    if (!p.weights) {
-        count_labels_kernel<<<1, 1024, 0, st>>>(s.labels, s.rows, inv);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    p.shared = static_cast<PolicyShared*>(ws);
+    if (s.rows == 0) {
+        zero_kernel<<<1, 32, 0, st>>>(p.loss, 1, p.stats, 3);
+        return cudaGetLastError();
     }
-    const RowOuts o{p.logp, p.norm, p.coef, out, out_stride, out ? words_agree(s, out, out_stride, dtype) : 0, row_status};
-    e = by_type(dtype, [&](auto t) { return run_rows<decltype(t), Ask::kPolicy>(s, p, o, st); });
+    const int counting = s.rows > 16384 ? 8 : 1;
+    ClusterLaunch l(counting, 1024, 0, counting, false, st);
+    const cudaError_t e = l(policy_begin_kernel, p.weights ? nullptr : s.labels, s.rows, p.shared);
     if (e != cudaSuccess) return e;
-    policy_finish_kernel<<<1, 1024, 0, st>>>(p.terms, s.rows, p.kl_coef, loss, stats);
-    return cudaGetLastError();
+    const RowOuts o{p.logp, p.norm, p.coef, out, out_stride, out ? words_agree(s, out, out_stride, dtype) : 0, row_status};
+    return by_type(dtype, [&](auto t) { return run_policy<decltype(t)>(s, p, o, st); });
 }
 
 size_t preference_workspace(int64_t, int64_t pairs) { return align256o((size_t)pairs * 4) + 256; }
@@ -644,16 +854,24 @@ size_t preference_workspace(int64_t, int64_t pairs) { return align256o((size_t)p
 cudaError_t preference_loss(int dtype, const ScoreRows& s, PreferenceArgs p, float* logp,
                             float* norm, float* coef, float grad_scale, void* out,
                             int64_t out_stride, void* ws, uint32_t* row_status, cudaStream_t st) {
-    p.each = static_cast<float*>(ws);
-    cudaError_t e = token_logp(dtype, s, logp, norm, coef, row_status, st);
-    if (e != cudaSuccess) return e;
-    if (p.pairs > 0) {
-        preference_pairs_kernel<<<row_grid(p.pairs), 256, 0, st>>>(p, s.labels, s.rows, logp, coef);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    p.ticket = static_cast<unsigned*>(ws);
+    p.each = reinterpret_cast<float*>(p.ticket + 64);
+    cudaError_t e = cudaSuccess;
+    if (s.rows > 0) {
+        e = token_logp(dtype, s, logp, norm, coef, p.ticket, row_status, st);
+    } else {  // pairs of empty sequences: the ticket's zero
+        zero_kernel<<<1, 32, 0, st>>>(reinterpret_cast<float*>(p.ticket), 1, nullptr, 0);
+        e = cudaGetLastError();
     }
-    preference_finish_kernel<<<1, 256, 0, st>>>(p.each, p.pairs, p.loss);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (!out) return cudaSuccess;
+    if (e != cudaSuccess) return e;
+    if (p.pairs == 0) {
+        zero_kernel<<<1, 32, 0, st>>>(p.loss, 1, nullptr, 0);
+        e = cudaGetLastError();
+    } else {
+        ClusterLaunch l(std::min<int64_t>(p.pairs, 1024), 512, 0, 1, true, st);
+        e = l(preference_pairs_kernel, p, s.labels, s.rows, logp, coef);
+    }
+    if (e != cudaSuccess || !out) return e;
     return token_logp_backward(dtype, s, norm, coef, grad_scale, nullptr, 0, out, out_stride, st);
 }
 
