@@ -26,122 +26,167 @@ run on ``stream`` (default: the current one); what they allocate belongs to it.
 """
 from __future__ import annotations
 
-import contextlib
 from collections import namedtuple
 
-from . import ISO_OK, IsoError, _check_dev, _torch, load_library
+from . import ISO_OK, IsoError, _torch, load_library
 
 MAX_EXPERTS = 1024   # ISO_MAX_EXPERTS
 MAX_TOP_K = 32       # ISO_MAX_TOP_K
 ISO_ROW_BAD_LABEL = 8
 KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
 
-PolicyLoss = namedtuple("PolicyLoss", "loss stats logp norm coef dlogits row_status")
-PreferenceLoss = namedtuple("PreferenceLoss",
-                            "loss margins seq_logp logp norm coef dlogits row_status pair_status")
 BalanceLoss = namedtuple("BalanceLoss", "loss counts experts gates live mask renormalize")
 
+
+class _Result:
+    """Named outputs, some of them views of one buffer that are made when they are asked for."""
+    _fields = ()
+    __slots__ = ("_buf", "_rows", "_shape")
+
+    def __iter__(self):
+        return (getattr(self, name) for name in self._fields)
+
+    def __len__(self):
+        return len(self._fields)
+
+    # the buffer's tail, in 4-byte words: norm [rows, 2], coef [rows], row_status [rows]
+    @property
+    def norm(self):
+        return self._buf[-4 * self._rows:][:2 * self._rows].view(self._rows, 2)
+
+    @property
+    def coef(self):
+        return self._buf[-4 * self._rows:][2 * self._rows:3 * self._rows].view(self._shape)
+
+    @property
+    def row_status(self):
+        return self._buf[-4 * self._rows:][3 * self._rows:].view(_torch().int32)
+
+
+class PolicyLoss(_Result):
+    """What :func:`iso_policy_loss` returns."""
+    _fields = ("loss", "stats", "logp", "norm", "coef", "dlogits", "row_status")
+    __slots__ = ("loss", "stats", "logp", "dlogits")
+
+
+class PreferenceLoss(_Result):
+    """What :func:`iso_preference_loss` returns."""
+    _fields = ("loss", "margins", "seq_logp", "logp", "norm", "coef", "dlogits", "row_status", "pair_status")
+    __slots__ = ("loss", "margins", "seq_logp", "logp", "dlogits", "pair_status")
+
+
+_abi = None      # the loaded library
 _dtypes = None
+_raw_stream = None
+
+
+def _setup():
+    global _abi, _dtypes, _raw_stream
+    torch = _torch()
+    _dtypes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _abi = load_library()
+    return torch
 
 
 def _scores(t, name="logits"):
-    """(dtype code, rows, n, row stride) of a tensor of scores."""
-    global _dtypes
-    torch = _torch()
-    if _dtypes is None:
-        _dtypes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+    """(dtype code, rows, n, row stride, device) of a tensor of scores."""
+    torch = _setup() if _dtypes is None else _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     code = _dtypes.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    if t.dim() == 2:
-        (rows, n), (stride, inner) = t.shape, t.stride()
-    elif t.dim() == 1:
-        rows, n, stride, inner = 1, t.shape[0], t.shape[0], t.stride(0)
+    dim = t.dim()
+    if dim == 2:
+        rows, n = t.shape
+        stride, inner = t.stride()
+    elif dim == 1:
+        rows, n, inner = 1, t.shape[0], t.stride(0)
+        stride = n
     else:
         raise ValueError(f"{name} must be [n] or [rows, n]")
     if n < 1:
         raise ValueError(f"{name} must have at least one score a row")
     if inner != 1 and n > 1:
         raise ValueError(f"{name} must be contiguous within a row")
-    return code, rows, n, stride
+    return code, rows, n, stride, t.device
 
 
 def _check(t, name, dtype, shape, device):
-    _check_dev(t, name, dtype)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}")
+    if getattr(t, "dtype", None) == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
+    if not isinstance(t, _torch().Tensor) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a {dtype} tensor")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _check_out(t, shape, like):
-    """A caller's gradient buffer: (dtype code checked) its row stride."""
-    code, rows, n, stride = _scores(t, "out")
-    if t.dtype != like.dtype or t.shape != shape or t.device != like.device:
+def _check_out(t, like):
+    """A caller's gradient buffer: its row stride."""
+    _, rows, n, stride, _ = _scores(t, "out")
+    if t.dtype != like.dtype or t.shape != like.shape or t.device != like.device:
         raise ValueError("out must have the logits' shape, type and device")
     if rows > 1 and stride < n:
         raise ValueError("out's rows must not overlap")
     return stride
 
 
-def _like(t, rows, n, stride):
+def _like(torch, t, rows, n, stride):
     """A gradient's buffer beside the scores t, with their row stride where rows are only
     padded: its rows are then aligned as theirs."""
-    torch = _torch()
     if n <= stride <= n + max(64, n >> 3) and t.dim() == 2:
         return torch.empty_strided((rows, n), (stride, 1), dtype=t.dtype, device=t.device), stride
     return torch.empty(t.shape, dtype=t.dtype, device=t.device), n
 
 
-@contextlib.contextmanager
-def _entered(device, stream):
-    torch = _torch()
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+def _elsewhere(torch, device, stream):
+    """None where the call belongs on the current device's current stream; otherwise the
+    context that makes it so."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return None
 
 
-def _call(name, *args):
-    st = getattr(load_library(), name)(*args)
-    if st != ISO_OK:
-        raise IsoError(st, name)
+def _done(status, name):
+    if status != ISO_OK:
+        raise IsoError(status, name)
 
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(nbytes, workspace, device):
+def _own_workspace(workspace, device):
     torch = _torch()
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes
-    _check_dev(workspace, "workspace", torch.uint8)
-    return workspace, workspace.numel()
-
-
-def _labels(labels, logits, device):
-    _check(labels, "labels", _torch().int64, logits.shape[:-1], device)
+    if not isinstance(workspace, torch.Tensor) or workspace.dtype != torch.uint8 or \
+            workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
+    return workspace.data_ptr(), workspace.numel()
 
 
 def iso_token_logp(logits, labels, *, temperature: float = 1.0, stream=None):
     """The labels' log-probabilities.  Returns ``(logp, norm, row_status)``: float32 of the
-    labels' shape; the rows' largest score and sum of exponentials ``[rows, 2]`` for the
-    backward; int32 ``[rows]``."""
+    labels' shape; the rows' softmax statistics ``[rows, 2]`` for the backward; int32 ``[rows]``."""
+    code, rows, n, stride, dev = _scores(logits)
     torch = _torch()
-    code, rows, n, stride = _scores(logits)
-    dev = logits.device
-    _labels(labels, logits, dev)
-    with _entered(dev, stream) as st:
-        logp = torch.empty(labels.shape, dtype=torch.float32, device=dev)
-        norm = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-        status = torch.empty(rows, dtype=torch.int32, device=dev)
-        _call("iso_token_logp", logits.data_ptr(), code, rows, n, stride, labels.data_ptr(),
-              temperature, logp.data_ptr(), norm.data_ptr(), status.data_ptr(), st)
+    _check(labels, "labels", torch.int64, logits.shape[:-1], dev)
+    there = _elsewhere(torch, dev, stream)
+    if there is not None:
+        with there:
+            return iso_token_logp(logits, labels, temperature=temperature)
+    logp = torch.empty(labels.shape, dtype=torch.float32, device=dev)
+    norm = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    status = torch.empty(rows, dtype=torch.int32, device=dev)
+    _done(_abi.iso_token_logp(
+        logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), temperature, logp.data_ptr(),
+        norm.data_ptr(), status.data_ptr(), _raw_stream(dev.index)), "iso_token_logp")
     return logp, norm, status
 
 
@@ -150,25 +195,30 @@ def iso_token_logp_backward(grad_logp, logits, labels, norm, *, temperature: flo
                             changed_only: bool = False, out=None, stream=None):
     """The gradient of ``grad_scale * grad_scale_dev * sum(grad_logp * logp)`` in the logits.
     ``norm`` is the forward's.  With ``changed_only`` and ``out`` given, nothing is written
-    when the device scalar ``grad_scale_dev`` is 1."""
+    when the device scalar ``grad_scale_dev`` is 1.  ``out`` may be the logits themselves."""
+    code, rows, n, stride, dev = _scores(logits)
     torch = _torch()
-    code, rows, n, stride = _scores(logits)
-    dev = logits.device
-    _labels(labels, logits, dev)
+    _check(labels, "labels", torch.int64, logits.shape[:-1], dev)
     _check(grad_logp, "grad_logp", torch.float32, labels.shape, dev)
     _check(norm, "norm", torch.float32, (rows, 2), dev)
     if grad_scale_dev is not None:
-        _check(grad_scale_dev, "grad_scale_dev", torch.float32, torch.Size(()), dev)
+        _check(grad_scale_dev, "grad_scale_dev", torch.float32, (), dev)
     if changed_only and out is None:
         raise ValueError("changed_only needs out")
-    with _entered(dev, stream) as st:
-        if out is None:
-            out, out_stride = _like(logits, rows, n, stride)
-        else:
-            out_stride = _check_out(out, logits.shape, logits)
-        _call("iso_token_logp_backward", logits.data_ptr(), code, rows, n, stride,
-              labels.data_ptr(), temperature, norm.data_ptr(), grad_logp.data_ptr(), grad_scale,
-              _ptr(grad_scale_dev), int(changed_only), out.data_ptr(), out_stride, st)
+    there = _elsewhere(torch, dev, stream)
+    if there is not None:
+        with there:
+            return iso_token_logp_backward(
+                grad_logp, logits, labels, norm, temperature=temperature, grad_scale=grad_scale,
+                grad_scale_dev=grad_scale_dev, changed_only=changed_only, out=out)
+    if out is None:
+        out, out_stride = _like(torch, logits, rows, n, stride)
+    else:
+        out_stride = _check_out(out, logits)
+    _done(_abi.iso_token_logp_backward(
+        logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), temperature, norm.data_ptr(),
+        grad_logp.data_ptr(), grad_scale, _ptr(grad_scale_dev), bool(changed_only), out.data_ptr(),
+        out_stride, _raw_stream(dev.index)), "iso_token_logp_backward")
     return out
 
 
@@ -179,38 +229,48 @@ def iso_policy_loss(logits, labels, old_logp, advantages, ref_logp=None, weights
     """Clipped policy loss with a KL term, and its gradient in the logits, in one pass over
     them.  Returns a :class:`PolicyLoss`: ``loss`` (scalar), ``stats`` (``[3]``: policy term,
     KL term, share of clipped rows), ``logp``, ``norm``, ``coef`` (the loss's derivative in
-    ``logp``), ``dlogits`` (None without ``want_grad``; times ``grad_scale``), ``row_status``."""
+    ``logp``), ``dlogits`` (None without ``want_grad``; times ``grad_scale``; written to ``out``
+    when given, which may be the logits themselves), ``row_status``."""
+    code, rows, n, stride, dev = _scores(logits)
     torch = _torch()
-    code, rows, n, stride = _scores(logits)
-    dev, f32 = logits.device, torch.float32
-    _labels(labels, logits, dev)
-    shape = labels.shape
+    f32 = torch.float32
+    shape = logits.shape[:-1]
+    _check(labels, "labels", torch.int64, shape, dev)
     _check(old_logp, "old_logp", f32, shape, dev)
     _check(advantages, "advantages", f32, shape, dev)
     if ref_logp is not None:
         _check(ref_logp, "ref_logp", f32, shape, dev)
     if weights is not None:
         _check(weights, "weights", f32, shape, dev)
-    lib = load_library()
-    with _entered(dev, stream) as st:
-        ws, ws_bytes = _workspace(lib.iso_policy_loss_workspace_bytes(rows), workspace, dev)
-        loss = torch.empty((), dtype=f32, device=dev)
-        stats = torch.empty(3, dtype=f32, device=dev)
-        logp = torch.empty(shape, dtype=f32, device=dev)
-        norm = torch.empty((rows, 2), dtype=f32, device=dev)
-        coef = torch.empty(shape, dtype=f32, device=dev)
-        status = torch.empty(rows, dtype=torch.int32, device=dev)
-        out_stride = n
-        if out is not None:
-            out_stride = _check_out(out, logits.shape, logits)
-        elif want_grad:
-            out, out_stride = _like(logits, rows, n, stride)
-        _call("iso_policy_loss", logits.data_ptr(), code, rows, n, stride, labels.data_ptr(),
-              temperature, old_logp.data_ptr(), advantages.data_ptr(), _ptr(ref_logp),
-              _ptr(weights), clip_low, clip_high, kl_coef, grad_scale, loss.data_ptr(),
-              stats.data_ptr(), logp.data_ptr(), norm.data_ptr(), coef.data_ptr(), _ptr(out),
-              out_stride, ws.data_ptr(), ws_bytes, status.data_ptr(), st)
-    return PolicyLoss(loss, stats, logp, norm, coef, out, status)
+    there = _elsewhere(torch, dev, stream)
+    if there is not None:
+        with there:
+            return iso_policy_loss(
+                logits, labels, old_logp, advantages, ref_logp, weights, clip_low=clip_low,
+                clip_high=clip_high, kl_coef=kl_coef, temperature=temperature,
+                grad_scale=grad_scale, want_grad=want_grad, out=out, workspace=workspace)
+    need = _abi.iso_policy_loss_workspace_bytes(rows)
+    r = PolicyLoss()
+    r._rows, r._shape = rows, shape
+    r.loss = loss = torch.empty((), dtype=f32, device=dev)
+    r.stats = stats = torch.empty(3, dtype=f32, device=dev)
+    r.logp = logp = torch.empty(shape, dtype=f32, device=dev)
+    r._buf = buf = torch.empty((need >> 2) + 4 * rows, dtype=f32, device=dev)
+    ws, ws_bytes = (buf.data_ptr(), need) if workspace is None else _own_workspace(workspace, dev)
+    rest = buf.data_ptr() + need
+    out_stride = n
+    if out is not None:
+        out_stride = _check_out(out, logits)
+    elif want_grad:
+        out, out_stride = _like(torch, logits, rows, n, stride)
+    r.dlogits = out
+    _done(_abi.iso_policy_loss(
+        logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), temperature,
+        old_logp.data_ptr(), advantages.data_ptr(), _ptr(ref_logp), _ptr(weights), clip_low,
+        clip_high, kl_coef, grad_scale, loss.data_ptr(), stats.data_ptr(), logp.data_ptr(), rest,
+        rest + 8 * rows, _ptr(out), out_stride, ws, ws_bytes, rest + 12 * rows,
+        _raw_stream(dev.index)), "iso_policy_loss")
+    return r
 
 
 def iso_preference_loss(logits, labels, offsets, ref_logp=None, *, kind: str = "sigmoid",
@@ -221,54 +281,65 @@ def iso_preference_loss(logits, labels, offsets, ref_logp=None, *, kind: str = "
     logits.  ``offsets``: int64 CUDA tensor of ``2 * pairs + 1`` entries (not read by the
     host); sequence ``2q`` is pair q's chosen one, ``2q + 1`` its rejected one.  ``kind``:
     "sigmoid", "hinge" or "squared".  Returns a :class:`PreferenceLoss`."""
+    code, rows, n, stride, dev = _scores(logits)
     torch = _torch()
-    code, rows, n, stride = _scores(logits)
-    dev, f32 = logits.device, torch.float32
-    _labels(labels, logits, dev)
-    _check_dev(offsets, "offsets", torch.int64)
-    if offsets.dim() != 1 or offsets.numel() % 2 != 1 or offsets.device != dev:
-        raise ValueError("offsets must hold 2 * pairs + 1 entries, beside the logits")
-    if kind not in KINDS:
+    f32 = torch.float32
+    shape = logits.shape[:-1]
+    _check(labels, "labels", torch.int64, shape, dev)
+    if not isinstance(offsets, torch.Tensor) or offsets.dim() != 1 or offsets.numel() % 2 != 1:
+        raise ValueError("offsets must hold 2 * pairs + 1 entries")
+    _check(offsets, "offsets", torch.int64, offsets.shape, dev)
+    how = KINDS.get(kind)
+    if how is None:
         raise ValueError(f"kind must be one of {sorted(KINDS)}")
     if ref_logp is not None:
-        _check(ref_logp, "ref_logp", f32, labels.shape, dev)
+        _check(ref_logp, "ref_logp", f32, shape, dev)
+    there = _elsewhere(torch, dev, stream)
+    if there is not None:
+        with there:
+            return iso_preference_loss(
+                logits, labels, offsets, ref_logp, kind=kind, beta=beta,
+                label_smoothing=label_smoothing, average=average, grad_scale=grad_scale,
+                want_grad=want_grad, out=out, workspace=workspace)
     pairs = offsets.numel() // 2
-    lib = load_library()
-    with _entered(dev, stream) as st:
-        ws, ws_bytes = _workspace(lib.iso_preference_loss_workspace_bytes(rows, pairs), workspace, dev)
-        loss = torch.empty((), dtype=f32, device=dev)
-        margins = torch.empty(pairs, dtype=f32, device=dev)
-        seq_logp = torch.empty(2 * pairs, dtype=f32, device=dev)
-        logp = torch.empty(labels.shape, dtype=f32, device=dev)
-        norm = torch.empty((rows, 2), dtype=f32, device=dev)
-        coef = torch.empty(labels.shape, dtype=f32, device=dev)
-        status = torch.empty(rows, dtype=torch.int32, device=dev)
-        pair_status = torch.empty(pairs, dtype=torch.int32, device=dev)
-        out_stride = n
-        if out is not None:
-            out_stride = _check_out(out, logits.shape, logits)
-        elif want_grad:
-            out, out_stride = _like(logits, rows, n, stride)
-        _call("iso_preference_loss", logits.data_ptr(), code, rows, n, stride, labels.data_ptr(),
-              offsets.data_ptr(), pairs, _ptr(ref_logp), KINDS[kind], beta, label_smoothing,
-              int(bool(average)), grad_scale, loss.data_ptr(), margins.data_ptr(),
-              seq_logp.data_ptr(), logp.data_ptr(), norm.data_ptr(), coef.data_ptr(), _ptr(out),
-              out_stride, ws.data_ptr(), ws_bytes, status.data_ptr(), pair_status.data_ptr(), st)
-    return PreferenceLoss(loss, margins, seq_logp, logp, norm, coef, out, status, pair_status)
+    need = _abi.iso_preference_loss_workspace_bytes(rows, pairs)
+    r = PreferenceLoss()
+    r._rows, r._shape = rows, shape
+    r.loss = loss = torch.empty((), dtype=f32, device=dev)
+    r.margins = margins = torch.empty(pairs, dtype=f32, device=dev)
+    r.seq_logp = seq_logp = torch.empty(2 * pairs, dtype=f32, device=dev)
+    r.logp = logp = torch.empty(shape, dtype=f32, device=dev)
+    r.pair_status = pair_status = torch.empty(pairs, dtype=torch.int32, device=dev)
+    r._buf = buf = torch.empty((need >> 2) + 4 * rows, dtype=f32, device=dev)
+    ws, ws_bytes = (buf.data_ptr(), need) if workspace is None else _own_workspace(workspace, dev)
+    rest = buf.data_ptr() + need
+    out_stride = n
+    if out is not None:
+        out_stride = _check_out(out, logits)
+    elif want_grad:
+        out, out_stride = _like(torch, logits, rows, n, stride)
+    r.dlogits = out
+    _done(_abi.iso_preference_loss(
+        logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), offsets.data_ptr(), pairs,
+        _ptr(ref_logp), how, beta, label_smoothing, bool(average), grad_scale, loss.data_ptr(),
+        margins.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), rest, rest + 8 * rows, _ptr(out),
+        out_stride, ws, ws_bytes, rest + 12 * rows, pair_status.data_ptr(),
+        _raw_stream(dev.index)), "iso_preference_loss")
+    return r
 
 
 def _router(logits, top_k, mask):
-    code, tokens, experts, stride = _scores(logits)
+    code, tokens, experts, stride, dev = _scores(logits)
     if logits.dim() != 2:
         raise ValueError("logits must be [tokens, experts]")
     if experts > MAX_EXPERTS or not 1 <= top_k <= min(experts, MAX_TOP_K):
         raise ValueError(f"at most {MAX_EXPERTS} experts, and 1 <= top_k <= min(experts, {MAX_TOP_K})")
+    torch = _torch()
     if mask is not None:
-        torch = _torch()
         if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
             mask = mask.view(torch.uint8)
-        _check(mask, "mask", torch.uint8, logits.shape[:1], logits.device)
-    return code, tokens, experts, stride, mask
+        _check(mask, "mask", torch.uint8, logits.shape[:1], dev)
+    return torch, code, tokens, experts, stride, dev, mask
 
 
 def iso_balance_loss(logits, top_k: int, mask=None, *, renormalize: bool = False, workspace=None,
@@ -278,48 +349,58 @@ def iso_balance_loss(logits, top_k: int, mask=None, *, renormalize: bool = False
     where a token takes no part.  Returns a :class:`BalanceLoss`: ``loss`` (scalar), ``counts``
     (int64 ``[experts]``), ``experts`` (int32 ``[tokens, top_k]``, -1 where none), ``gates``
     (float32), ``live`` (int64 scalar: the tokens that take part), ``mask``, ``renormalize``."""
-    torch = _torch()
-    code, tokens, experts, stride, mask = _router(logits, top_k, mask)
-    dev = logits.device
-    lib = load_library()
-    with _entered(dev, stream) as st:
-        ws, ws_bytes = _workspace(lib.iso_balance_loss_workspace_bytes(tokens, experts), workspace, dev)
-        loss = torch.empty((), dtype=torch.float32, device=dev)
-        counts = torch.empty(experts, dtype=torch.int64, device=dev)
-        chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
-        gates = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
-        live = torch.empty((), dtype=torch.int64, device=dev)
-        _call("iso_balance_loss", logits.data_ptr(), code, tokens, experts, stride, top_k,
-              _ptr(mask), int(bool(renormalize)), loss.data_ptr(), counts.data_ptr(),
-              chosen.data_ptr(), gates.data_ptr(), live.data_ptr(), ws.data_ptr(), ws_bytes, st)
-    return BalanceLoss(loss, counts, chosen, gates, live, mask, bool(renormalize))
+    torch, code, tokens, experts, stride, dev, mask = _router(logits, top_k, mask)
+    there = _elsewhere(torch, dev, stream)
+    if there is not None:
+        with there:
+            return iso_balance_loss(logits, top_k, mask, renormalize=renormalize, workspace=workspace)
+    need = _abi.iso_balance_loss_workspace_bytes(tokens, experts)
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    counts = torch.empty(experts, dtype=torch.int64, device=dev)
+    chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
+    gates = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+    live = torch.empty((), dtype=torch.int64, device=dev)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws, ws_bytes = _own_workspace(workspace, dev)
+    renormalize = bool(renormalize)
+    _done(_abi.iso_balance_loss(
+        logits.data_ptr(), code, tokens, experts, stride, top_k, _ptr(mask), renormalize,
+        loss.data_ptr(), counts.data_ptr(), chosen.data_ptr(), gates.data_ptr(), live.data_ptr(),
+        ws, ws_bytes, _raw_stream(dev.index)), "iso_balance_loss")
+    return BalanceLoss(loss, counts, chosen, gates, live, mask, renormalize)
 
 
 def iso_balance_loss_backward(logits, result, *, grad_loss: float = 1.0, grad_loss_dev=None,
                               grad_gates=None, out=None, stream=None):
     """The gradient of ``grad_loss * grad_loss_dev * loss + sum(grad_gates * gates)`` in the
     logits, ``result`` being :func:`iso_balance_loss`'s for them."""
-    torch = _torch()
     shape = result.experts.shape
-    code, tokens, experts, stride, mask = _router(logits, shape[1], result.mask)
-    dev = logits.device
+    torch, code, tokens, experts, stride, dev, mask = _router(logits, shape[1], result.mask)
     _check(result.experts, "experts", torch.int32, (tokens, shape[1]), dev)
     _check(result.gates, "gates", torch.float32, shape, dev)
     _check(result.counts, "counts", torch.int64, (experts,), dev)
-    _check(result.live, "live", torch.int64, torch.Size(()), dev)
+    _check(result.live, "live", torch.int64, (), dev)
     if grad_gates is not None:
         _check(grad_gates, "grad_gates", torch.float32, shape, dev)
     if grad_loss_dev is not None:
-        _check(grad_loss_dev, "grad_loss_dev", torch.float32, torch.Size(()), dev)
-    with _entered(dev, stream) as st:
-        if out is None:
-            out, out_stride = _like(logits, tokens, experts, stride)
-        else:
-            out_stride = _check_out(out, logits.shape, logits)
-        _call("iso_balance_loss_backward", logits.data_ptr(), code, tokens, experts, stride,
-              shape[1], _ptr(mask), int(result.renormalize), result.counts.data_ptr(),
-              result.experts.data_ptr(), result.gates.data_ptr(), result.live.data_ptr(),
-              _ptr(grad_gates), grad_loss, _ptr(grad_loss_dev), out.data_ptr(), out_stride, st)
+        _check(grad_loss_dev, "grad_loss_dev", torch.float32, (), dev)
+    there = _elsewhere(torch, dev, stream)
+    if there is not None:
+        with there:
+            return iso_balance_loss_backward(logits, result, grad_loss=grad_loss,
+                                             grad_loss_dev=grad_loss_dev, grad_gates=grad_gates,
+                                             out=out)
+    if out is None:
+        out, out_stride = _like(torch, logits, tokens, experts, stride)
+    else:
+        out_stride = _check_out(out, logits)
+    _done(_abi.iso_balance_loss_backward(
+        logits.data_ptr(), code, tokens, experts, stride, shape[1], _ptr(mask),
+        result.renormalize, result.counts.data_ptr(), result.experts.data_ptr(),
+        result.gates.data_ptr(), result.live.data_ptr(), _ptr(grad_gates), grad_loss,
+        _ptr(grad_loss_dev), out.data_ptr(), out_stride, _raw_stream(dev.index)),
+        "iso_balance_loss_backward")
     return out
 
 
