@@ -19,8 +19,10 @@ namespace {
 
 // Threads of a CTA: fewer where a lane holds 32 scores, for its registers and the CTA's shared memory.
 template <int EPL>
-constexpr int token_threads = EPL == 32 ? 256 : 512;
-constexpr int kTokCtas = 304;  // two CTAs for each of 152 SMs: what the workspace has room for
+constexpr int token_threads = EPL >= 16 ? 256 : 512;
+template <int EPL>
+constexpr int token_ctas_an_sm = EPL == 32 ? 1 : EPL == 16 ? 3 : 2;
+constexpr int kMaxCtas = 3 * 152;  // what the workspace has room for
 constexpr int kFinishCtas = 8;
 
 // Order-preserving key of a score; 0 for what is never chosen (-inf and NaN), equal for both zeros.
@@ -94,18 +96,29 @@ struct TokenRow {
             }
         }
     }
-    // The scores, -inf past the last expert.
-    __device__ __forceinline__ void scores(float (&s)[EPL], int lane, int experts) const {
+    // -inf everywhere: what is past the last expert keeps it, as no load writes there.
+    __device__ __forceinline__ TokenRow() {
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s[i] = expert(lane, i) < experts ? to_f32(v[i]) : -INFINITY;
+        for (int i = 0; i < EPL; ++i) v[i] = from_f32<T>(-INFINITY);
+    }
+    __device__ __forceinline__ void scores(float (&s)[EPL], bool on) const {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) s[i] = to_f32(v[i]);
+        if (!on) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) s[i] = -INFINITY;
+        }
     }
 };
 
+// The lanes of this lane's group.
+template <int G>
+__device__ __forceinline__ unsigned group_lanes() {
+    return G == 32 ? ~0u : ((1u << (G & 31)) - 1u) << (threadIdx.x & 31 & ~(G - 1));
+}
 template <int G>
 __device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-    return v;
+    return warp_max(v, group_lanes<G>());
 }
 template <int G>
 __device__ __forceinline__ float group_add(float v) {
@@ -124,11 +137,15 @@ __device__ __forceinline__ SoftState token_softmax(const float (&v)[EPL], float 
     st.m = group_max<G>(m);
     const SoftRef ref(st.m, kLog2e);
     float s = 0.f;
+    if (ref.far) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        e[i] = ref.exp(v[i]);
-        s += e[i];
+        for (int i = 0; i < EPL; ++i) e[i] = ref.exp(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) e[i] = ex2(fmaf(v[i], kLog2e, -ref.c));
     }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) s += e[i];
     st.s = group_add<G>(s);
     return st;
 }
@@ -136,21 +153,25 @@ __device__ __forceinline__ SoftState token_softmax(const float (&v)[EPL], float 
 // Whether a token takes part, given its mask: some score is above -inf (or NaN, which shows).
 __device__ __forceinline__ bool token_open(SoftState st) { return !(st.m == -INFINITY && st.s == 0.f); }
 
-// A group of G lanes a token.  The choice: with EPL = 1 each lane counts the scores above its own.
-// Otherwise the k-th largest of the lanes' largest scores bounds the k-th largest score from below;
-// the scores that reach it (k and a few more) are collected and each counts those above it.  When
-// more than 32 reach it, k rounds of one maximum each.
+// A group of G lanes a token, several tokens to a warp where G < 32 (then EPL is 1).  The choice: with EPL = 1 each
+// lane counts the scores above its own.  Otherwise the k-th largest of the lanes' largest scores
+// bounds the k-th largest score from below; the scores that reach it (k and a few more) are
+// collected and each counts those above it.  When more than 32 reach it, k rounds of one maximum
+// each.
 template <class T, int G, int EPL>
-__global__ void __launch_bounds__(token_threads<EPL>, EPL <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(token_threads<EPL>, token_ctas_an_sm<EPL>)
 balance_tokens_kernel(RouterArgs a, BalanceParts b, int whole, int32_t* __restrict__ chosen,
                       float* __restrict__ gates) {
-    constexpr int kTokThreads = token_threads<EPL>, kTokWarps = kTokThreads / 32;
+    constexpr int kTokThreads = token_threads<EPL>, kTokWarps = kTokThreads / 32, TPW = 32 / G;
     static_assert(G == 32 || EPL == 1, "several tokens to a warp hold a score a lane");
-    __shared__ uint64_t found[EPL == 1 ? 1 : kTokWarps][32];
+    __shared__ __align__(16) float found[EPL == 1 ? 1 : kTokWarps][36];  // scores that may be among the k largest
+    __shared__ int found_at[EPL == 1 ? 1 : kTokWarps][32];               // their experts
+    __shared__ int found_n[EPL == 1 ? 1 : kTokWarps];
     __shared__ float sh_p[G * EPL];
     __shared__ uint32_t sh_n[G * EPL];
     __shared__ uint32_t sh_live;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane & (G - 1), E = a.experts, k = a.top_k;
+    const unsigned group = group_lanes<G>(), before = group & ((1u << lane) - 1u);
     for (int e = threadIdx.x; e < G * EPL; e += kTokThreads) {
         sh_n[e] = 0u;
         sh_p[e] = 0.f;
@@ -162,8 +183,8 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, int whole, int32_t* __restri
 #pragma unroll
     for (int i = 0; i < EPL; ++i) psum[i] = 0.f;
     uint32_t tokens = 0;
-    const int64_t step = (int64_t)gridDim.x * kTokWarps * (32 / G);
-    const int64_t warp_first = ((int64_t)blockIdx.x * kTokWarps + warp) * (32 / G);
+    const int64_t step = (int64_t)gridDim.x * kTokWarps * TPW;
+    const int64_t warp_first = ((int64_t)blockIdx.x * kTokWarps + warp) * TPW;
     const T* const base = static_cast<const T*>(a.x);
     TokenRow<T, G, EPL> row;
     bool on = false;
@@ -175,24 +196,20 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, int whole, int32_t* __restri
     for (int64_t first = warp_first; first < a.tokens; first += step) {
         const int64_t t = first + lane / G;
         float v[EPL], e[EPL];
-        row.scores(v, gl, E);
+        row.scores(v, on);
         const bool was_on = on;
         fetch(t + step);
-        if (!was_on) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-        }
         const SoftState st = token_softmax<G, EPL>(v, e);
         const bool open = was_on && token_open(st);
-        const float inv = open ? 1.f / st.s : 0.f;
+        const float inv = open ? __frcp_rn(st.s) : 0.f;
         if (gl == 0 && open) ++tokens;
-        const SoftRef ref(st.m, kLog2e);
         if (open) {
 #pragma unroll
             for (int i = 0; i < EPL; ++i) psum[i] = fmaf(e[i], inv, psum[i]);
         }
         int32_t* const to = chosen + t * k;
         float* const gate_to = gates + t * k;
+        int taken = 0;  // places filled
         if constexpr (EPL == 1) {
             const uint32_t key = choice_key(v[0]);
             int rank = 0;
@@ -209,102 +226,102 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, int whole, int32_t* __restri
                 gate_to[rank] = gate;
                 atomicAdd(&sh_n[gl], 1u);
             }
-            // the places that no open expert takes
-            const unsigned in_group = G == 32 ? ~0u : ((1u << (G & 31)) - 1u) << (lane & ~(G - 1));
-            const int taken = __popc(__ballot_sync(~0u, mine) & in_group);
-            if (t < a.tokens)
-                for (int c = taken + gl; c < k; c += G) {
-                    to[c] = -1;
-                    gate_to[c] = 0.f;
-                }
+            taken = __popc(__ballot_sync(~0u, mine) & group);
         } else {
-            if (!open) {
-                if (lane < k) {
-                    to[lane] = -1;
-                    gate_to[lane] = 0.f;
-                }
-                continue;
-            }
-            float top = v[0];
+            const SoftRef ref(st.m, kLog2e);
+            float most = v[0];
 #pragma unroll
-            for (int i = 1; i < EPL; ++i) top = fmaxf(top, v[i]);
-            uint32_t most = choice_key(top), bound = 0u;
+            for (int i = 1; i < EPL; ++i) most = fmaxf(most, v[i]);
+            float least = 0.f;
+#pragma unroll 4
             for (int c = 0; c < k; ++c) {
-                bound = __reduce_max_sync(~0u, most);
-                if (most == bound) most = 0u;
+                least = group_max<G>(most);
+                if (most == least) most = -INFINITY;
             }
-            const float least = bound == 0u ? __uint_as_float(0xff7fffffu) : choice_score(bound);
-            int n = 0;
-            uint64_t* const list = found[warp];
+            least = !open ? INFINITY : least > -INFINITY ? least : __uint_as_float(0xff7fffffu);  // (lowest)
+            float* const list = found[warp];
+            int* const list_at = found_at[warp];
+            if (lane == 0) found_n[warp] = 0;
             __syncwarp();
+            // in whatever order: the ranks below do not depend on it
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                const bool is = v[i] >= least;
-                const unsigned all = __ballot_sync(~0u, is);
-                if (all == 0u) continue;
-                const int at = n + __popc(all & ((1u << lane) - 1u));
-                if (is && at < 32)
-                    list[at] = (uint64_t)choice_key(v[i]) << 32 | (0xffffffffu - (uint32_t)row.expert(lane, i));
-                n += __popc(all);
-            }
-            __syncwarp();
-            int mine = -1, rank = 32;
-            float gate = 0.f;
-            if (n <= 32) {
-                const uint64_t own = lane < n ? list[lane] : 0u;
-                rank = 0;
-                for (int j = 0; j < n; ++j) rank += list[j] > own ? 1 : 0;
-                if (lane < n && rank < k) {
-                    mine = (int)(0xffffffffu - (uint32_t)own);
-                    gate = ref.exp(choice_score((uint32_t)(own >> 32)));
-                    atomicAdd(&sh_n[mine], 1u);
+            for (int i = 0; i < EPL; ++i)
+                if (v[i] >= least) {
+                    const int at = atomicAdd(&found_n[warp], 1);
+                    if (at < 32) {
+                        list[at] = v[i];
+                        list_at[at] = row.expert(lane, i);
+                    }
                 }
-                n = min(n, k);
+            __syncwarp();
+            const int n = found_n[warp];
+            if (n <= 32) {
+                if (lane < 4) list[n + lane] = -INFINITY;  // four are read at a time
+                __syncwarp();
+                const float own = lane < n ? list[lane] : 0.f;
+                const int own_at = lane < n ? list_at[lane] : 0;
+                int rank = -1;  // the score itself is counted too
+                for (int j = 0; j < n; j += 4) {
+                    const float4 q = *reinterpret_cast<const float4*>(&list[j]);
+                    rank += (q.x >= own) + (q.y >= own) + (q.z >= own) + (q.w >= own);
+                }
+                // without equal scores the ranks are 0 .. n - 1
+                if (__reduce_add_sync(~0u, lane < n ? rank : 0) != n * (n - 1) / 2) {
+                    rank = 0;
+                    for (int j = 0; j < n; ++j) rank += list[j] > own || (list[j] == own && list_at[j] < own_at) ? 1 : 0;
+                }
+                if (lane < n && rank < k) {
+                    to[rank] = own_at;
+                    gate_to[rank] = ref.exp(own) * inv;
+                    atomicAdd(&sh_n[own_at], 1u);
+                }
+                taken = min(n, k);
             } else {
                 unsigned gone = 0u;  // of this lane's scores
-                n = 0;
-                for (int c = 0; c < k; ++c) {
+                for (; taken < k; ++taken) {
                     uint32_t key = 0u;
                     int at = -1;
 #pragma unroll
                     for (int i = 0; i < EPL; ++i) {
                         const uint32_t q = choice_key(v[i]);
-                        if (!(gone >> i & 1u) && (q > key || (q == key && q != 0u && row.expert(lane, i) < row.expert(lane, at)))) {
+                        if (!(gone >> i & 1u) && (q > key || (q == key && q != 0u && row.expert(gl, i) < row.expert(gl, at)))) {
                             key = q;
                             at = i;
                         }
                     }
-                    const uint32_t best = __reduce_max_sync(~0u, key);
+                    const uint32_t best = __reduce_max_sync(group, key);
                     if (best == 0u) break;
-                    const unsigned which = key == best ? (unsigned)row.expert(lane, at) : ~0u;
-                    const unsigned winner = __reduce_min_sync(~0u, which);
+                    const unsigned which = key == best ? (unsigned)row.expert(gl, at) : ~0u;
+                    const unsigned winner = __reduce_min_sync(group, which);
                     if (which == winner) {
                         gone |= 1u << at;
+                        to[taken] = (int)winner;
+                        gate_to[taken] = ref.exp(choice_score(best)) * inv;
                         atomicAdd(&sh_n[winner], 1u);
                     }
-                    if (lane == c) {
-                        mine = (int)winner;
-                        rank = c;
-                        gate = ref.exp(choice_score(best));
-                    }
-                    n = c + 1;
                 }
             }
-            gate *= a.renormalize ? 1.f / warp_add(gate) : inv;
-            if (mine >= 0) {
-                to[rank] = mine;
-                gate_to[rank] = gate;
-            }
-            if (lane >= n && lane < k) {
-                to[lane] = -1;
-                gate_to[lane] = 0.f;
+            __syncwarp();
+            if (a.renormalize) {  // the gates over their sum
+                float mine = 0.f;
+                for (int c = gl; c < taken; c += G) mine += gate_to[c];
+                const float scale = 1.f / group_add<G>(mine);
+                for (int c = gl; c < taken; c += G) gate_to[c] *= scale;
             }
         }
+        // the places that no open expert takes
+        if (t < a.tokens)
+            for (int c = taken + gl; c < k; c += G) {
+                to[c] = -1;
+                gate_to[c] = 0.f;
+            }
     }
     // the CTA's sums, in the order of its warps
     if constexpr (G < 32) {
 #pragma unroll
-        for (int o = 16; o >= G; o >>= 1) psum[0] += __shfl_xor_sync(~0u, psum[0], o);
+        for (int i = 0; i < EPL; ++i)
+#pragma unroll
+            for (int o = 16; o >= G; o >>= 1) psum[i] += __shfl_xor_sync(~0u, psum[i], o);
     }
     for (int w = 0; w < kTokWarps; ++w) {
         if (warp == w && lane < G) {
@@ -387,7 +404,7 @@ balance_finish_kernel(BalanceParts b, int grid, int E, int top_k, float* __restr
 
 // The last tokens first: what the forward read last is still in L2.
 template <class T, int G, int EPL>
-__global__ void __launch_bounds__(token_threads<EPL>, EPL <= 8 ? 2 : 1)
+__global__ void __launch_bounds__(token_threads<EPL>, token_ctas_an_sm<EPL>)
 balance_backward_kernel(RouterArgs a, int whole, const int64_t* __restrict__ counts,
                         const int32_t* __restrict__ chosen, const float* __restrict__ gates,
                         const int64_t* __restrict__ live, const float* __restrict__ grad_gates,
@@ -432,15 +449,11 @@ balance_backward_kernel(RouterArgs a, int whole, const int64_t* __restrict__ cou
     for (int64_t first = warp_first; first < a.tokens; first += step) {
         const int64_t t = a.tokens - 1 - (first + lane / G);
         float v[EPL], e[EPL];
-        row.scores(v, gl, E);
+        row.scores(v, on);
         const bool was_on = on;
         const int slot = at;
         const float g_slot = g, gate_slot = gate;
         fetch(t - step);
-        if (!was_on) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) v[i] = -INFINITY;
-        }
         const SoftState st = token_softmax<G, EPL>(v, e);
         const bool open = was_on && token_open(st);
         // k <= experts <= G where EPL is 1, and k <= 32 = G otherwise: a slot a lane
@@ -467,7 +480,7 @@ balance_backward_kernel(RouterArgs a, int whole, const int64_t* __restrict__ cou
         }
         dot = group_add<G>(dot);
         if (t < 0) continue;
-        TokenRow<T, G, EPL> d;
+        TokenRow<T, G, EPL> d;  // (its -inf are all written over)
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
             d.v[i] = from_f32<T>(!open ? 0.f : a.renormalize ? fmaf(e[i], u[i] - dot, x[i]) : e[i] * (u[i] + x[i] - dot));
@@ -475,13 +488,17 @@ balance_backward_kernel(RouterArgs a, int whole, const int64_t* __restrict__ cou
     }
 }
 
-inline int token_grid(int64_t tokens, int per_warp, int threads) {
-    const int64_t per = (int64_t)(threads / 32) * per_warp;
-    return (int)std::max<int64_t>(1, std::min<int64_t>((tokens + per - 1) / per, kTokCtas));
+// CTAs for the tokens, `per` at a time each.
+inline int token_grid(int64_t tokens, int per, int most) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>((tokens + per - 1) / per, most));
+}
+template <int G, int EPL>
+int token_grid(int64_t tokens) {
+    return token_grid(tokens, token_threads<EPL> / G, 152 * token_ctas_an_sm<EPL>);
 }
 
-// Lanes a token and scores a lane: the fewest lanes that hold a score each up to 32 experts, then
-// the smallest power of two of scores a lane.
+// The fewest lanes that hold a score each up to 32 experts, then the smallest power of two of scores
+// a lane.
 template <class F>
 cudaError_t by_experts(int experts, F f) {
     using std::integral_constant;
@@ -504,7 +521,7 @@ inline bool chunks_fit(const void* x, int64_t rows, int64_t stride, int experts,
 }  // namespace
 
 size_t balance_workspace(int64_t tokens, int experts) {
-    return 2048 + (size_t)token_grid(tokens, 1, 256) * experts * 8;
+    return 2048 + (size_t)token_grid(tokens, 8, kMaxCtas) * experts * 8;
 }
 
 cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* counts,
@@ -516,7 +533,7 @@ cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* c
         return by_experts(a.experts, [&](auto g, auto epl) {
             using T = decltype(t);
             constexpr int G = decltype(g)::value, EPL = decltype(epl)::value;
-            grid = token_grid(a.tokens, 32 / G, token_threads<EPL>);
+            grid = token_grid<G, EPL>(a.tokens);
             b.p = reinterpret_cast<float*>(static_cast<char*>(ws) + 2048);
             b.n = reinterpret_cast<uint32_t*>(b.p + (int64_t)grid * a.experts);
             const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, TokenRow<T, G, EPL>::CH, sizeof(T));
@@ -540,7 +557,7 @@ cudaError_t balance_backward(int dtype, const RouterArgs& a, const int64_t* coun
             constexpr int G = decltype(g)::value, EPL = decltype(epl)::value, CH = TokenRow<T, G, EPL>::CH;
             const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, CH, sizeof(T)) &&
                               chunks_fit(out, a.tokens, out_stride, a.experts, CH, sizeof(T));
-            ClusterLaunch l(token_grid(a.tokens, 32 / G, token_threads<EPL>), token_threads<EPL>, 0, 1, true, st);
+            ClusterLaunch l(token_grid<G, EPL>(a.tokens), token_threads<EPL>, 0, 1, true, st);
             return l(balance_backward_kernel<T, G, EPL>, a, whole, counts, chosen, gates, live, grad_gates,
                      grad_loss, grad_loss_dev, static_cast<T*>(out), out_stride);
         });

@@ -209,10 +209,12 @@ __device__ __forceinline__ void word_exp(const uint4& w, const SoftRef& ref, flo
     }
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
-    return v;
+// Over the lanes of a warp (or the given ones, which all call with the same), in one instruction;
+// NaN are passed over.
+__device__ __forceinline__ float warp_max(float v, unsigned lanes = ~0u) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(lanes));
+    return r;
 }
 
 __device__ __forceinline__ float warp_add(float v) {
