@@ -47,7 +47,8 @@ EXPORTS = ("iso_version", "iso_status_string", "iso_fit_workspace_bytes", "iso_f
            "iso_fit_copy_control_workspace_bytes", "iso_fit_copy_control",
            "iso_fit_f64", "iso_backward_f64", "iso_backward_w_f64", "iso_fit_ragged_f64",
            "iso_profile_enable", "iso_profile_read", "iso_bridge_stats_mode",
-           "iso_bridge_stats_read", "iso_token_logp", "iso_token_logp_backward",
+           "iso_bridge_stats_read", "iso_token_logp_workspace_bytes", "iso_token_logp",
+           "iso_token_logp_backward",
            "iso_policy_loss_workspace_bytes", "iso_policy_loss",
            "iso_preference_loss_workspace_bytes", "iso_preference_loss",
            "iso_balance_loss_workspace_bytes", "iso_balance_loss", "iso_balance_loss_backward")
@@ -113,7 +114,9 @@ def load_library(path: str | None = None):
         lib.iso_bridge_stats_read.restype = ci
         cf = ctypes.c_float
         scores = [vp, ci, i64, i64, i64]   # logits, dtype, rows, n, stride
-        lib.iso_token_logp.argtypes = scores + [vp, cf, vp, vp, vp, vp]
+        lib.iso_token_logp_workspace_bytes.argtypes = [i64]
+        lib.iso_token_logp_workspace_bytes.restype = sz
+        lib.iso_token_logp.argtypes = scores + [vp, cf, vp, vp, vp, sz, vp, vp]
         lib.iso_token_logp_backward.argtypes = scores + [vp, cf, vp, vp, cf, vp, ci, vp, i64, vp]
         lib.iso_policy_loss_workspace_bytes.argtypes = [i64]
         lib.iso_policy_loss.argtypes = (scores + [vp, cf, vp, vp, vp, vp] + [cf] * 4 + [vp] * 6

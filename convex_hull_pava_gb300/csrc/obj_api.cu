@@ -37,14 +37,21 @@ isodev::ScoreRows score_rows(const void* logits, int64_t rows, int64_t n, int64_
 
 extern "C" {
 
+size_t iso_token_logp_workspace_bytes(int64_t rows) {
+    return rows < 0 || rows > kMaxN ? 0 : isodev::token_logp_workspace(rows);
+}
+
 iso_status iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t n, int64_t stride,
                           const int64_t* labels, float temperature, float* logp, float* norm,
-                          uint32_t* row_status, void* stream) {
+                          void* workspace, size_t workspace_bytes, uint32_t* row_status,
+                          void* stream) {
     if (!rows_ok(dtype, rows, n, stride, 0) || !temperature_ok(temperature)) return ISO_ERR_INVALID_ARG;
     if (rows == 0) return ISO_OK;
     if (!logits || !labels || !logp || !norm) return ISO_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, isodev::token_logp_workspace(rows)))
+        return ISO_ERR_WORKSPACE;
     return from_cuda(isodev::token_logp(dtype, score_rows(logits, rows, n, stride, labels, temperature),
-                                        logp, norm, nullptr, nullptr, row_status,
+                                        logp, norm, workspace, row_status,
                                         static_cast<cudaStream_t>(stream)));
 }
 

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 namespace isodev {
 
@@ -215,6 +216,32 @@ __device__ __forceinline__ float warp_max(float v, unsigned lanes = ~0u) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "r"(lanes));
     return r;
+}
+
+// Takes U words into a state whose scores' maximum is `top`.
+template <class T, int U>
+__device__ __forceinline__ void add_words(SoftState& st, const uint4 (&w)[U], float a, float top) {
+    soft_raise(st, top, a);
+    const SoftRef ref(st.m, a);
+    float2 sum{0.f, 0.f};
+    auto add = [&](auto far) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float2 v[Word<T>::N / 2];
+            word_exp<T, decltype(far)::value>(w[u], ref, v);
+#pragma unroll
+            for (int i = 0; i < Word<T>::N / 2; ++i) sum = add2(sum, v[i]);
+        }
+    };
+    ref.far ? add(std::true_type()) : add(std::false_type());
+    st.s += sum.x + sum.y;
+}
+template <class T, int U>
+__device__ __forceinline__ void add_words(SoftState& st, const uint4 (&w)[U], float a) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) top = fmaxf(top, word_max(w[u], T()));
+    add_words<T, U>(st, w, a, top);
 }
 
 __device__ __forceinline__ float warp_add(float v) {

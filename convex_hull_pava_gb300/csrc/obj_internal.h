@@ -19,13 +19,23 @@ struct ScoreRows {
     float inv_t;  // 1 / temperature
 };
 
+// At the front of a call's workspace: the CTAs that have come to the end of a kernel, and the rows
+// with a label.
+struct ListHead {
+    unsigned ticket;
+    int labelled;
+    float inv_count;
+};
+struct PolicyTerms;
+
 // What the policy loss takes and gives for each row beside its scores.
 struct PolicyArgs {
     const float *old_logp, *advantages, *ref_logp, *weights;
     float low, high, kl_coef, grad_scale;
     float *logp, *norm, *coef;
     float *loss, *stats;
-    struct PolicyShared* shared;  // workspace
+    ListHead* head;               // workspace
+    struct PolicyTerms* of_team;  // workspace
 };
 
 struct PreferenceArgs {
@@ -40,9 +50,9 @@ struct PreferenceArgs {
     float* each;       // [pairs] workspace
 };
 
-// With `zero_coef`, that many zeros are written there; with `zero_ticket`, a zero.
-cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, float* zero_coef,
-                       unsigned* zero_ticket, uint32_t* row_status, cudaStream_t st);
+size_t token_logp_workspace(int64_t rows);
+cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, void* ws,
+                       uint32_t* row_status, cudaStream_t st);
 // out = grad_scale * (grad_scale_dev ? *grad_scale_dev : 1) * coef (onehot - p) / T;
 // with `changed_only` nothing is written when that device value is 1.
 cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,

@@ -25,23 +25,22 @@ inline __host__ __device__ size_t align256o(size_t x) { return (x + 255) & ~size
 // The most teams of a launch: what the workspace has room for.
 constexpr int64_t kMaxTeams = 32768;
 
+}  // namespace
+
 // Partial sums of the policy loss: policy term, KL term, clipped weight.
 struct PolicyTerms {
     Sum v[3];
 };
 
-}  // namespace
-
-// The policy loss's workspace.  A begin kernel zeroes the ticket and counts the labels; every team
-// leaves its rows' terms; the last CTA adds them up.
-struct PolicyShared {
-    unsigned ticket;
-    float inv_count;
-    char pad[56];
-    PolicyTerms of_team[1];
-};
-
 namespace {
+
+// Rows with a label, counted and listed before the kernels that take them, so that teams of equal
+// numbers of rows have equal work: the labelled rows in order from the list's front, the others in
+// order from its back.  Without a list (no more rows than teams) a team takes the row of its number.
+struct RowList {
+    const ListHead* head;
+    const int32_t* list;
+};
 
 // One row's part of the policy loss, from its log-probability.
 struct PolicyRow {
@@ -89,9 +88,6 @@ struct RowGrad {
 __device__ __forceinline__ uint32_t norm_status(SoftState st) {
     return isfinite(st.m) && isfinite(st.s) ? 0u : ISO_ROW_BAD_Y;
 }
-
-// What is asked of a row's scores.
-enum class Ask { kLogp, kPolicy };
 
 struct RowOuts {
     float *logp, *norm, *coef;
@@ -141,12 +137,21 @@ __device__ __forceinline__ void store_word(T* at, const uint4& w, bool whole) {
     }
 }
 
-// What a team has of its next row before that row's turn; the scores' words are on their way to
-// shared memory.
+// What a team has of its next row before that row's turn, beside its words, which are on their way
+// to shared memory.
 struct RowAhead {
-    int64_t label;
-    float at_label, edge, old, adv, ref, w;
+    int row;     // -1: none
+    int label;   // -1: none; n where it is not below n
+    float edge;  // the single score that this lane takes, or -inf
 };
+
+// A row without a label: zeros.
+__device__ __forceinline__ void unlabelled_row(const RowOuts& o, int64_t r) {
+    o.logp[r] = 0.f;
+    *reinterpret_cast<float2*>(o.norm + 2 * r) = {0.f, 1.f};
+    if (o.coef) o.coef[r] = 0.f;
+    if (o.status) o.status[r] = 0u;
+}
 
 // Teams of TEAM threads (a warp; a CTA; the CTAs of a cluster) take the rows in turn.  Each thread
 // copies its words of the next row (up to K) to a place of its own in shared memory while it works
@@ -154,9 +159,9 @@ struct RowAhead {
 // read once.  A thread reads only what it has copied, so the one thing that a team shares is the
 // row's (maximum, sum); the warps of a cluster write theirs to every CTA and meet once a row.
 // LONG: rows longer than the team's registers are read twice, the second time from L2.
-template <class T, Ask ASK, int NT, int TEAM, int K, bool LONG>
+template <class T, int NT, int TEAM, int K, bool LONG>
 __global__ void __launch_bounds__(NT, NT * K >= 4096 ? 2 : NT == 128 ? 6 : 3)
-score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
+policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     constexpr int N = Word<T>::N, W = NT / 32;
     extern __shared__ uint4 ahead_words[];
     __shared__ SoftState part[2][TEAM == 32 ? 2 : 8 * W];
@@ -164,18 +169,16 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
     const int shift = 31 - __clz(ctas);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tt = TEAM == 32 ? lane : threadIdx.x;
-    const int64_t teams = TEAM == 32 ? (int64_t)gridDim.x * W : gridDim.x >> shift;
-    int64_t r = TEAM == 32 ? (int64_t)blockIdx.x * W + warp : blockIdx.x >> shift;
+    const uint32_t teams = TEAM == 32 ? gridDim.x * W : gridDim.x >> shift;
+    const uint32_t team = TEAM == 32 ? blockIdx.x * W + warp : blockIdx.x >> shift;
     uint4* mine = ahead_words + (TEAM == 32 ? warp * 32 * K : 0) + tt;
     const float a = kLog2e * sc.inv_t;
     const int n = sc.n;
     const bool edges = rank == 0 && tt < 32;
     const T* const base = static_cast<const T*>(sc.x);
 
-    auto start = [&](int64_t row, int64_t label) {
-        RowAhead h;
-        h.label = label;
-        h.at_label = h.edge = h.old = h.adv = h.ref = h.w = 0.f;
+    auto start = [&](int row, int64_t label) {
+        RowAhead h{row, label < 0 ? -1 : label < n ? (int)label : n, -INFINITY};
         if (label >= 0) {
             const T* x = base + row * sc.stride;
             const RowShape<T> s(x, n, rank, ctas, shift);
@@ -185,53 +188,54 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
                 for (int k = 0; k < K; ++k)
                     if (tt + k * TEAM < s.count) copy_async(mine + k * TEAM, src + k * TEAM);
             }
-            h.at_label = label < n ? to_f32(x[label]) : NAN;
             const int e = edges ? s.edge(n, tt) : -1;
-            h.edge = e >= 0 ? to_f32(x[e]) : -INFINITY;
-            if (ASK == Ask::kPolicy) {
-                h.old = p.old_logp[row];
-                h.adv = p.advantages[row];
-                if (p.ref_logp) h.ref = p.ref_logp[row];
-                if (p.weights) h.w = p.weights[row];
-            }
+            if (e >= 0) h.edge = to_f32(x[e]);
         }
         copy_async_commit();
         return h;
     };
-
-    PolicyTerms terms;
-    auto finish = [&]() {
-        // the teams' sums, by the last CTA, in the teams' order
-        if (rank == 0 && tt == 0) p.shared->of_team[TEAM == 32 ? blockIdx.x * W + warp : blockIdx.x >> shift] = terms;
-        if (!last_to_come(&p.shared->ticket, gridDim.x)) return;
-        if (warp < 3) {
-            Sum v;
-            for (int64_t i = lane; i < teams; i += 32) {
-                const float2 f = __ldcg(reinterpret_cast<const float2*>(&p.shared->of_team[i].v[warp]));
-                Sum q;
-                q.hi = f.x;
-                q.lo = f.y;
-                v.add(q);
-            }
-            v = warp_sum(v);
-            if (lane == 0) reinterpret_cast<Sum*>(part)[warp] = v;
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            Sum* v = reinterpret_cast<Sum*>(part);
-            for (int i = 0; i < 3; ++i) p.stats[i] = v[i].value();
-            // the KL term's product rounds once
-            *p.loss = p.ref_logp ? fmaf(p.kl_coef, v[1].value(), v[0].value()) : v[0].value();
-        }
+    auto zero_row = [&](int64_t row) {
+        if (rank == 0 && tt == 0) unlabelled_row(o, row);
+        if (!o.out) return;
+        T* out = static_cast<T*>(o.out) + row * o.out_stride;
+        const RowShape<T> s(o.out_words ? base + row * sc.stride : out, n, rank, ctas, shift);
+        uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
+        for (int j = tt; j < s.count; j += TEAM) store_streaming(dst + j, uint4{0, 0, 0, 0});
+        const int e = edges ? s.edge(n, tt) : -1;
+        if (e >= 0) out[e] = from_f32<T>(0.f);
     };
+
     let_next_start();
-    int64_t label_next = r + teams < sc.rows ? sc.labels[r + teams] : -1;
-    RowAhead cur = start(r, r < sc.rows ? sc.labels[r] : -1), next;
-    if (ASK == Ask::kPolicy) wait_for_previous();
-    const float inv_count = ASK == Ask::kPolicy && !p.weights ? *(volatile float*)&p.shared->inv_count : 0.f;
-    for (int turn = 0; r < sc.rows; r += teams, cur = next) {
-        const int64_t after = r + 2 * teams;
-        const int64_t label_after = after < sc.rows ? sc.labels[after] : -1;
+    if (rl.list) wait_for_previous();
+    // the team's rows: the current one, the next (its words copied while the current one's turn
+    // lasts), the one after (its label known), and the one after that
+    const uint32_t items = rl.list ? (uint32_t)rl.head->labelled : (uint32_t)sc.rows;
+    auto item = [&](uint32_t i) { return i >= items ? -1 : rl.list ? rl.list[i] : (int)i; };
+    auto label_of = [&](int row) { return row >= 0 ? sc.labels[row] : (int64_t)-1; };
+    uint32_t at = team;
+    int row1 = item(at + teams), row2 = item(at + 2 * teams), row3;
+    int64_t label1 = label_of(row1);
+    const int row0 = item(at);
+    RowAhead cur = start(row0, label_of(row0)), next;
+    if (!rl.list) wait_for_previous();
+    const float inv_count = p.weights ? 0.f : rl.head->inv_count;
+    // rows without a label are spread between the labelled ones, from the last team to the first
+    // (those have had fewer labelled ones)
+    uint32_t zeros = (uint32_t)sc.rows - items, zero_at = teams - 1 - team;
+    int64_t due = (int64_t)items * team / teams;
+    PolicyTerms terms;
+    for (int turn = 0; cur.row >= 0; row1 = row2, row2 = row3, at += teams, cur = next) {
+        const int r = cur.row;
+        const int64_t label2 = label_of(row2);
+        row3 = item(at + 3 * teams);
+        float at_label = NAN, old = 0.f, adv = 0.f, base_lp = 0.f, weight = 0.f;
+        if (cur.label >= 0) {
+            if (cur.label < n) at_label = to_f32(base[r * sc.stride + cur.label]);
+            old = p.old_logp[r];
+            adv = p.advantages[r];
+            if (p.ref_logp) base_lp = p.ref_logp[r];
+            weight = p.weights ? p.weights[r] : inv_count;
+        }
         const T* x = base + r * sc.stride;
         const RowShape<T> s(x, n, rank, ctas, shift);
         const int rounds = (s.count + TEAM - 1) / TEAM;  // the same in all threads, as is what depends on it
@@ -251,28 +255,13 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
                     }
             }
         }
-        next = start(r + teams, label_next);
-        label_next = label_after;
+        next = start(row1, label1);
+        label1 = label2;
         if (cur.label < 0) {
-            if (rank == 0 && tt == 0) {
-                o.logp[r] = 0.f;
-                o.norm[2 * r] = 0.f;
-                o.norm[2 * r + 1] = 1.f;
-                if (o.coef) o.coef[r] = 0.f;
-                if (o.status) o.status[r] = 0u;
-            }
-            if (ASK == Ask::kPolicy && o.out) {
-                if (o.out_words) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
-                    for (int j = tt; j < s.count; j += TEAM) store_streaming(dst + j, uint4{0, 0, 0, 0});
-                    const int e = edges ? s.edge(n, tt) : -1;
-                    if (e >= 0) out[e] = from_f32<T>(0.f);
-                } else {
-                    for (int j = rank * TEAM + tt; j < n; j += ctas * TEAM) out[j] = from_f32<T>(0.f);
-                }
-            }
+            zero_row(r);
             continue;
         }
+        for (due += zeros; due >= items && zero_at < zeros; due -= items, zero_at += teams) zero_row(rl.list[sc.rows - 1 - zero_at]);
 
         // the warp's sum, against the warp's maximum
         SoftState st;
@@ -297,25 +286,9 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
             st.m = cur.edge;
             st.s = edges ? SoftRef(st.m, a).exp(cur.edge) : 0.f;
             for (int j = tt; j < s.count; j += K * TEAM) {
-                float m = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < K; ++k) w[k] = j + k * TEAM < s.count ? src[j + k * TEAM] : word_closed(T());
-#pragma unroll
-                for (int k = 0; k < K; ++k) m = fmaxf(m, word_max(w[k], T()));
-                soft_raise(st, m, a);
-                const SoftRef ref(st.m, a);
-                sum = {0.f, 0.f};
-                auto add = [&](auto far) {
-#pragma unroll
-                    for (int k = 0; k < K; ++k) {
-                        float2 v[N / 2];
-                        word_exp<T, decltype(far)::value>(w[k], ref, v);
-#pragma unroll
-                        for (int i = 0; i < N / 2; ++i) sum = add2(sum, v[i]);
-                    }
-                };
-                ref.far ? add(std::true_type()) : add(std::false_type());
-                st.s += sum.x + sum.y;
+                add_words<T, K>(st, w, a);
             }
             st = soft_warp(st, a);
         }
@@ -348,23 +321,18 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
         }
 
         const SoftRef ref(st.m, a);
-        const float lp = ref.of(cur.at_label) * kLn2 - logf(st.s);
-        PolicyRow q{};
-        if (ASK == Ask::kPolicy)
-            q = policy_row(p, lp, cur.old, cur.adv, cur.ref, p.weights ? cur.w : inv_count);
+        const float lp = ref.of(at_label) * kLn2 - logf(st.s);
+        const PolicyRow q = policy_row(p, lp, old, adv, base_lp, weight);
         if (rank == 0 && tt == 0) {
             o.logp[r] = lp;
-            o.norm[2 * r] = st.m;
-            o.norm[2 * r + 1] = st.s;
-            if (o.coef) o.coef[r] = q.coef;
+            *reinterpret_cast<float2*>(o.norm + 2 * r) = {st.m, st.s};
+            o.coef[r] = q.coef;
             if (o.status) o.status[r] = norm_status(st) | (cur.label >= n ? ISO_ROW_BAD_LABEL : 0u);
-            if (ASK == Ask::kPolicy) {
-                terms.v[0].add(q.pg);
-                terms.v[1].add(q.kl);
-                terms.v[2].add(q.cut);
-            }
+            terms.v[0].add(q.pg);
+            terms.v[1].add(q.kl);
+            terms.v[2].add(q.cut);
         }
-        if (ASK == Ask::kLogp || !o.out) continue;
+        if (!o.out) continue;
 
         const float g = q.coef * p.grad_scale * sc.inv_t;
         const RowGrad<T> grad{g, -g / st.s, ref};
@@ -391,80 +359,101 @@ score_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o) {
         const int e = edges ? s.edge(n, tt) : -1;
         if (e >= 0) out[e] = grad.one(cur.edge, e == cur.label);
         // the label's score again, by the thread that has just written its word
-        if (s.owner(cur.label, TEAM) == tt) out[cur.label] = grad.one(cur.at_label, true);
+        if (s.owner(cur.label, TEAM) == tt) out[cur.label] = grad.one(at_label, true);
     }
     copy_async_wait_all();
-    if (ASK == Ask::kPolicy) finish();
+    for (; zero_at < zeros; zero_at += teams) zero_row(rl.list[sc.rows - 1 - zero_at]);
+
+    // the teams' sums, by the last CTA, in the teams' order
+    if (rank == 0 && tt == 0) p.of_team[team] = terms;
+    if (!last_to_come(&p.head->ticket, gridDim.x)) return;
+    Sum* const total = reinterpret_cast<Sum*>(part);
+    if (warp < 3) {
+        Sum v;
+        for (uint32_t i = lane; i < teams; i += 32) {
+            const float2 f = __ldcg(reinterpret_cast<const float2*>(&p.of_team[i].v[warp]));
+            Sum q;
+            q.hi = f.x;
+            q.lo = f.y;
+            v.add(q);
+        }
+        v = warp_sum(v);
+        if (lane == 0) total[warp] = v;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 3; ++i) p.stats[i] = total[i].value();
+        // the KL term's product rounds once
+        *p.loss = p.ref_logp ? fmaf(p.kl_coef, total[1].value(), total[0].value()) : total[0].value();
+    }
 }
 
-// The rows of one CTA (or of a cluster's CTAs together) in turn: every `teams`-th, those with a
-// label.  The labels of 32 of them are looked at in one load.
-struct LabelledRows {
+// A team's rows in turn, for a reader that has only the index: those listed, or the row of the
+// team's number if it has a label.
+struct TeamRows {
+    RowList rl;
     const int64_t* labels;
-    int64_t rows, teams, block;  // block: the first row of the current 32
-    unsigned left;               // of the current 32, the labelled rows still to come
-    __device__ __forceinline__ LabelledRows(const ScoreRows& sc, int64_t first, int64_t step)
-        : labels(sc.labels), rows(sc.rows), teams(step), block(first - 32 * step), left(0u) {}
-    // Steps to the next labelled row, or to `rows`.  `unlabelled` is called for lane l's row of
-    // each new 32 if it has no label.
-    template <class F>
-    __device__ __forceinline__ int64_t next(F unlabelled) {
-        while (left == 0u) {
-            block += 32 * teams;
-            if (block >= rows) return rows;
-            const int64_t r = block + (threadIdx.x & 31) * teams;
-            const bool has = r < rows && labels[r] >= 0;
-            if (r < rows && !has) unlabelled(r);
-            left = __ballot_sync(~0u, has);
-        }
-        const int l = __ffs(left) - 1;
-        left &= left - 1;
-        return block + l * teams;
+    int64_t items, teams, at, upcoming;
+    __device__ __forceinline__ TeamRows(const ScoreRows& sc, const RowList& list, int64_t team, int64_t step)
+        : rl(list), labels(sc.labels), teams(step), at(team) {
+        items = rl.list ? rl.head->labelled : sc.rows;
+        upcoming = at < items ? (rl.list ? rl.list[at] : labels[at] >= 0 ? at : -1) : -1;
+    }
+    // The next row, or -1 when there are none left.
+    __device__ __forceinline__ int64_t next() {
+        const int64_t r = upcoming;
+        at += teams;
+        upcoming = rl.list && at < items ? rl.list[at] : -1;
+        return r;
     }
 };
 
 // Log-probabilities alone: a stream of the rows' words through a ring in shared memory, D groups of
 // U words a thread in flight across the ends of rows, a running (maximum, sum) a thread, and one
 // meeting of the CTA (or of a cluster's CTAs) a row, after which all warps but the first go on.
-template <class T, int NT, int U, int D>
+// Short rows are a warp's each.
+template <class T, int NT, int TEAM, int U, int D>
 __global__ void __launch_bounds__(NT, 3)
-score_stream_kernel(ScoreRows sc, RowOuts o, unsigned* zero_ticket) {
-    constexpr int N = Word<T>::N, W = NT / 32;
+score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) {
+    constexpr int W = NT / 32;
     extern __shared__ uint4 ring[];
-    __shared__ SoftState part[2][8 * W];
-    const int ctas = (int)cluster_size(), rank = (int)cluster_rank(), shift = 31 - __clz(ctas);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = threadIdx.x;
-    const int64_t teams = gridDim.x >> shift, first = blockIdx.x >> shift;
-    uint4* mine = ring + tt;
+    __shared__ SoftState part[2][TEAM == 32 ? 1 : 8 * W];
+    const int ctas = TEAM == 32 ? 1 : (int)cluster_size(), rank = TEAM == 32 ? 0 : (int)cluster_rank();
+    const int shift = 31 - __clz(ctas);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tt = TEAM == 32 ? lane : threadIdx.x;
+    const int64_t teams = TEAM == 32 ? (int64_t)gridDim.x * W : gridDim.x >> shift;
+    const int64_t team = TEAM == 32 ? (int64_t)blockIdx.x * W + warp : blockIdx.x >> shift;
+    uint4* mine = ring + (TEAM == 32 ? warp * 32 * U * D : 0) + tt;
     const float a = kLog2e * sc.inv_t;
     const int n = sc.n;
-    const bool edges = rank == 0 && warp == 0;
+    const bool edges = rank == 0 && tt < 32;
     const T* const base = static_cast<const T*>(sc.x);
-    if (zero_ticket && blockIdx.x == 0 && tt == 0) *zero_ticket = 0u;
     let_next_start();
+    if (rl.list) wait_for_previous();
+    if (zero_ticket && blockIdx.x == 0 && threadIdx.x == 0) *zero_ticket = 0u;
 
     // what is copied next: group `at` of row `row`
-    LabelledRows ahead(sc, first, teams);
-    int64_t row = -1;
+    TeamRows ahead(sc, rl, team, teams);
+    int64_t row = 0;
     int at = 0, groups = 0, count = 0;
     const uint4* src = nullptr;
     auto copy_group = [&](int slot) {
-        if (at == groups && row < sc.rows) {
-            row = ahead.next([](int64_t) {});
-            if (row < sc.rows) {
+        if (at == groups && row >= 0) {
+            row = ahead.next();
+            if (row >= 0) {
                 const T* x = base + row * sc.stride;
                 const RowShape<T> s(x, n, rank, ctas, shift);
                 src = reinterpret_cast<const uint4*>(x + s.head) + s.first + tt;
                 count = s.count;
                 at = 0;
-                groups = max(1, (count + NT * U - 1) / (NT * U));
+                groups = max(1, (count + TEAM * U - 1) / (TEAM * U));
             }
         }
-        if (at < groups && row < sc.rows) {
+        if (at < groups && row >= 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int j = (at * U + u) * NT;
-                if (tt + j < count) copy_async(mine + (slot * U + u) * NT, src + j);
+                const int j = (at * U + u) * TEAM;
+                if (tt + j < count) copy_async(mine + (slot * U + u) * TEAM, src + j);
             }
             ++at;
         }
@@ -473,19 +462,9 @@ score_stream_kernel(ScoreRows sc, RowOuts o, unsigned* zero_ticket) {
 #pragma unroll
     for (int d = 0; d < D; ++d) copy_group(d);
 
-    LabelledRows here(sc, first, teams);
+    TeamRows here(sc, rl, team, teams);
     int slot = 0, turn = 0;
-    for (;;) {
-        const int64_t r = here.next([&](int64_t q) {
-            if (rank == 0 && warp == 0) {
-                o.logp[q] = 0.f;
-                o.norm[2 * q] = 0.f;
-                o.norm[2 * q + 1] = 1.f;
-                if (o.coef) o.coef[q] = 0.f;
-                if (o.status) o.status[q] = 0u;
-            }
-        });
-        if (r >= sc.rows) break;
+    for (int64_t r = here.next(); r >= 0; r = here.next()) {
         const T* x = base + r * sc.stride;
         const RowShape<T> s(x, n, rank, ctas, shift);
         int64_t label = 0;
@@ -497,72 +476,67 @@ score_stream_kernel(ScoreRows sc, RowOuts o, unsigned* zero_ticket) {
             if (e >= 0) edge = to_f32(x[e]);
         }
         SoftState st = soft_empty();
-        const int end = max(1, (s.count + NT * U - 1) / (NT * U));
+        const int end = max(1, (s.count + TEAM * U - 1) / (TEAM * U));
         for (int g = 0; g < end; ++g) {
             copy_async_wait<D - 1>();
             uint4 w[U];
             float m = -INFINITY;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                w[u] = tt + (g * U + u) * NT < s.count ? mine[(slot * U + u) * NT] : word_closed(T());
-                m = fmaxf(m, word_max(w[u], T()));
+                w[u] = tt + (g * U + u) * TEAM < s.count ? mine[(slot * U + u) * TEAM] : word_closed(T());
+                m = fmaxf(m, word_max(w[u], T()));  // (read, before the place is copied to again)
             }
             copy_group(slot);
             slot = slot + 1 == D ? 0 : slot + 1;
-            soft_raise(st, m, a);
-            const SoftRef ref(st.m, a);
-            float2 sum{0.f, 0.f};
-            auto add = [&](auto far) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    float2 v[N / 2];
-                    word_exp<T, decltype(far)::value>(w[u], ref, v);
-#pragma unroll
-                    for (int i = 0; i < N / 2; ++i) sum = add2(sum, v[i]);
-                }
-            };
-            ref.far ? add(std::true_type()) : add(std::false_type());
-            st.s += sum.x + sum.y;
+            add_words<T, U>(st, w, a, m);
         }
         if (edges) {
             soft_raise(st, edge, a);
             st.s += SoftRef(st.m, a).exp(edge);
         }
         st = soft_warp(st, a);
-        SoftState* place = part[turn++ & 1];  // as in score_rows_kernel
-        if (ctas == 1) {
-            if (lane == 0) place[warp] = st;
-            __syncthreads();
-        } else {
-            if (lane == 0) store_remote(&place[rank * W + warp], 0, st);
-            __syncwarp();
-            cluster_sync();
+        if (TEAM != 32) {
+            SoftState* place = part[turn++ & 1];  // as in policy_rows_kernel
+            if (ctas == 1) {
+                if (lane == 0) place[warp] = st;
+                __syncthreads();
+            } else {
+                if (lane == 0) store_remote(&place[rank * W + warp], 0, st);
+                __syncwarp();
+                cluster_sync();
+            }
+            if (!edges) continue;
+            st = soft_empty();
+            for (int i = lane; i < ctas * W; i += 32) {
+                const SoftState q = place[i];
+                soft_raise(st, q.m, a);
+                st.s += q.s * SoftRef(st.m, a).factor(q.m);
+            }
+            st = soft_warp(st, a);
         }
-        if (!edges) continue;
-        st = soft_empty();
-        for (int i = lane; i < ctas * W; i += 32) {
-            const SoftState q = place[i];
-            soft_raise(st, q.m, a);
-            st.s += q.s * SoftRef(st.m, a).factor(q.m);
-        }
-        st = soft_warp(st, a);
         if (lane == 0) {
             o.logp[r] = SoftRef(st.m, a).of(at_label) * kLn2 - logf(st.s);
-            o.norm[2 * r] = st.m;
-            o.norm[2 * r + 1] = st.s;
+            *reinterpret_cast<float2*>(o.norm + 2 * r) = {st.m, st.s};
             if (o.coef) o.coef[r] = 0.f;
             if (o.status) o.status[r] = norm_status(st) | (label >= n ? ISO_ROW_BAD_LABEL : 0u);
         }
     }
     copy_async_wait_all();
+    // the rows without a label
+    const int64_t thread = (int64_t)blockIdx.x * NT + threadIdx.x, threads = (int64_t)gridDim.x * NT;
+    if (rl.list) {
+        for (int64_t j = thread; j < sc.rows - rl.head->labelled; j += threads) unlabelled_row(o, rl.list[sc.rows - 1 - j]);
+    } else if (rank == 0 && tt == 0 && team < sc.rows && sc.labels[team] < 0) {
+        unlabelled_row(o, team);
+    }
     __syncwarp();
     if (ctas > 1) cluster_sync();  // the first CTA's shared memory outlives the others' writes
 }
 
-// out = g (onehot - p) with g from the rows' coefficients: a CTA takes K words a thread of one
-// row, from the last row to the first (the forward has read them in order, so that the last
-// ones are in L2).
-template <class T, int NT, int K>
+// out = g (onehot - p) with g from the rows' coefficients: a CTA (or, of a short row, a warp) takes
+// K words a thread of one row, from the last row to the first (the forward has read them in order,
+// so that the last ones are in L2).
+template <class T, int NT, int TEAM, int K>
 __global__ void __launch_bounds__(NT)
 score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float* __restrict__ coef,
                       float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o,
@@ -575,77 +549,92 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
         grad_scale *= g;
     }
     const float a = kLog2e * sc.inv_t;
-    const int n = sc.n, tt = threadIdx.x;
-    for (int64_t unit = blockIdx.x; unit < sc.rows * parts; unit += gridDim.x) {
+    const int n = sc.n, tt = threadIdx.x & (TEAM - 1);
+    const int64_t teams = (int64_t)gridDim.x * (NT / TEAM);
+    for (int64_t unit = (int64_t)blockIdx.x * (NT / TEAM) + threadIdx.x / TEAM; unit < sc.rows * parts; unit += teams) {
         const int64_t r = sc.rows - 1 - unit / parts;
         const int part = (int)(unit % parts);
         const T* x = static_cast<const T*>(sc.x) + r * sc.stride;
         T* out = static_cast<T*>(o.out) + r * o.out_stride;
-        const RowShape<T> s(x, n, part, parts);
         const int64_t label = sc.labels[r];
-        const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
-        uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
-        const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
         if (label < 0) {
-            if (o.out_words) {
-                for (int j = tt; j < s.count; j += NT) store_streaming(dst + j, uint4{0, 0, 0, 0});
-            } else {
-                for (int j = tt; j < s.count * N; j += NT) out[s.head + (int64_t)s.first * N + j] = from_f32<T>(0.f);
-            }
+            const RowShape<T> s(o.out_words ? x : out, n, part, parts);
+            uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
+            for (int j = tt; j < s.count; j += TEAM) store_streaming(dst + j, uint4{0, 0, 0, 0});
+            const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
             if (e >= 0) out[e] = from_f32<T>(0.f);
             continue;
         }
+        const RowShape<T> s(x, n, part, parts);
+        const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
+        T* dst = out + s.head + (int64_t)s.first * N;
+        const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
         const float edge = e >= 0 ? to_f32(x[e]) : 0.f;
-        const float m = norm[2 * r], sum = norm[2 * r + 1];
-        const float g = coef[r] * grad_scale * sc.inv_t;
-        const RowGrad<T> grad{g, -g / sum, SoftRef(m, a)};
-        const bool owner = s.owner(label, NT) == tt;
+        const bool owner = s.owner(label, TEAM) == tt;
         const float at_label = owner ? to_f32(x[label]) : 0.f;
-        for (int j = tt; j < s.count; j += K * NT) {
+        const float2 ms = *reinterpret_cast<const float2*>(norm + 2 * r);
+        const float g = coef[r] * grad_scale * sc.inv_t;
+        const RowGrad<T> grad{g, -g / ms.y, SoftRef(ms.x, a)};
+        for (int j = tt; j < s.count; j += K * TEAM) {
             uint4 w[K];
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (j + k * NT < s.count) w[k] = load_streaming(src + j + k * NT);
+                if (j + k * TEAM < s.count) w[k] = load_streaming(src + j + k * TEAM);
+            auto give = [&](auto far) {
 #pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (j + k * NT < s.count) {
-                    const uint4 d = grad.ref.far ? grad.template word<true>(w[k]) : grad.template word<false>(w[k]);
-                    store_word(out + s.head + (int64_t)(s.first + j + k * NT) * N, d, o.out_words);
-                }
+                for (int k = 0; k < K; ++k)
+                    if (j + k * TEAM < s.count)
+                        store_word(dst + (int64_t)(j + k * TEAM) * N, grad.template word<decltype(far)::value>(w[k]), o.out_words);
+            };
+            grad.ref.far ? give(std::true_type()) : give(std::false_type());
         }
         if (e >= 0) out[e] = grad.one(edge, e == label);
         if (owner) out[label] = grad.one(at_label, true);
     }
 }
 
-// Before the policy loss: its ticket, and 1 / (number of labelled rows); 0 when there are none.
-// One cluster counts, so that nothing has to be zeroed first.
+// The list of rows (see RowList), its counts, and a zeroed ticket; with list == NULL the counts
+// alone.  One CTA, or one cluster of which each CTA has a stretch of the rows, so that nothing has
+// to be zeroed first.
 __global__ void __launch_bounds__(1024)
-policy_begin_kernel(const int64_t* __restrict__ labels, int64_t rows, PolicyShared* __restrict__ sh) {
-    __shared__ int of_warp[8 * 32];
+row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, ListHead* __restrict__ head, int32_t* __restrict__ list) {
+    __shared__ int of_cta[8], of_warp[2][32];
     let_next_start();
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t share = (rows + ctas - 1) / ctas, first = min(rows, rank * share), end = min(rows, first + share);
     int c = 0;
-    if (labels)
-        for (int64_t r = rank * 1024 + threadIdx.x; r < rows; r += ctas * 1024) c += labels[r] >= 0 ? 1 : 0;
+    for (int64_t r = first + threadIdx.x; r < end; r += 1024) c += labels[r] >= 0 ? 1 : 0;
     c = __reduce_add_sync(~0u, c);
-    if (ctas == 1) {
-        if (lane == 0) of_warp[warp] = c;
-        __syncthreads();
-    } else {
-        if (lane == 0) store_remote(&of_warp[rank * 32 + warp], 0, c);
-        __syncwarp();
-        cluster_sync();
+    if (lane == 0) of_warp[0][warp] = c;
+    __syncthreads();
+    c = __reduce_add_sync(~0u, of_warp[0][lane]);
+    if (warp == 0 && lane < ctas) store_remote(&of_cta[rank], lane, c);
+    __syncwarp();
+    cluster_sync();
+    int run = 0, labelled = 0;  // labelled rows before this CTA's; of all
+    for (int q = 0; q < ctas; ++q) {
+        if (q < rank) run += of_cta[q];
+        labelled += of_cta[q];
     }
-    if (rank == 0 && warp == 0) {
-        c = 0;
-        for (int i = lane; i < ctas * 32; i += 32) c += of_warp[i];
-        c = __reduce_add_sync(~0u, c);
-        if (lane == 0) {
-            sh->ticket = 0u;
-            sh->inv_count = c > 0 ? 1.f / (float)c : 0.f;
-        }
+    if (rank == 0 && threadIdx.x == 0) {
+        head->ticket = 0u;
+        head->labelled = labelled;
+        head->inv_count = labelled > 0 ? 1.f / (float)labelled : 0.f;
+    }
+    if (!list) return;
+    int turn = 1;
+    for (int64_t from = first; from < end; from += 1024, turn ^= 1) {
+        const int64_t r = from + threadIdx.x;
+        const bool has = r < end && labels[r] >= 0;
+        const unsigned all = __ballot_sync(~0u, has);
+        if (lane == 0) of_warp[turn][warp] = __popc(all);
+        __syncthreads();  // (of_warp's other half is written after the next one)
+        const int mine = of_warp[turn][lane];
+        const int before = __reduce_add_sync(~0u, lane < warp ? mine : 0) + __popc(all & ((1u << lane) - 1u));
+        if (has) list[run + before] = (int32_t)r;
+        else if (r < end) list[rows - 1 - (r - (run + before))] = (int32_t)r;
+        run += __reduce_add_sync(~0u, mine);
     }
 }
 
@@ -741,51 +730,69 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
     }
 }
 
-template <class T, Ask ASK, int NT, int TEAM, int K, bool LONG>
-cudaError_t launch_rows(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, int ctas, cudaStream_t st) {
-    auto* kernel = score_rows_kernel<T, ASK, NT, TEAM, K, LONG>;
-    ClusterLaunch l(1, NT, LONG ? 0 : (size_t)NT * K * 16, ctas, ASK == Ask::kPolicy, st);
+// The workspace: a head, the list of rows, what follows.
+inline size_t list_bytes(int64_t rows) { return 256 + align256o((size_t)rows * 4); }
+inline ListHead* list_head(void* ws) { return static_cast<ListHead*>(ws); }
+inline int32_t* list_rows(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + 256); }
+inline char* after_list(void* ws, int64_t rows) { return static_cast<char*>(ws) + list_bytes(rows); }
+
+cudaError_t make_list(const ScoreRows& s, void* ws, bool list, cudaStream_t st) {
+    const int ctas = s.rows > 1024 ? 8 : 1;
+    ClusterLaunch l(ctas, 1024, 0, ctas, false, st);
+    return l(row_list_kernel, s.labels, s.rows, list_head(ws), list ? list_rows(ws) : nullptr);
+}
+
+template <class T, int NT, int TEAM, int K, bool LONG>
+cudaError_t launch_policy(const ScoreRows& s, PolicyArgs p, const RowOuts& o, int ctas, void* ws, cudaStream_t st) {
+    auto* kernel = policy_rows_kernel<T, NT, TEAM, K, LONG>;
+    ClusterLaunch l(1, NT, LONG ? 0 : (size_t)NT * K * 16, ctas, true, st);
     static int held[64][4];
     int fit = 0;
-    const cudaError_t e = clusters_held(kernel, l.c, ctas, held, &fit);
+    cudaError_t e = clusters_held(kernel, l.c, ctas, held, &fit);
     if (e != cudaSuccess) return e;
-    const int64_t wanted = TEAM == 32 ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows;
-    l.c.gridDim = dim3((unsigned)(std::min<int64_t>({wanted, fit, kMaxTeams / (TEAM == 32 ? NT / 32 : 1)}) * ctas));
-    return l(kernel, s, p, o);
+    constexpr int per_cta = TEAM == 32 ? NT / 32 : 1;
+    const int64_t grid = std::min<int64_t>({(s.rows + per_cta - 1) / per_cta, fit, kMaxTeams / per_cta});
+    const bool list = s.rows > grid * per_cta;
+    if ((e = make_list(s, ws, list, st)) != cudaSuccess) return e;
+    p.head = list_head(ws);
+    p.of_team = reinterpret_cast<PolicyTerms*>(after_list(ws, s.rows));
+    l.c.gridDim = dim3((unsigned)(grid * ctas));
+    return l(kernel, s, p, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr});
 }
 
 // By a row's bytes: a warp holds up to 4 KB, a CTA 16, 32 or 64 KB and a cluster up to 8 times that;
 // longer rows are read twice.
 template <class T>
-cudaError_t run_policy(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, cudaStream_t st) {
+cudaError_t run_policy(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, void* ws, cudaStream_t st) {
     const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
-    constexpr Ask ASK = Ask::kPolicy;
-    if (words <= 32 * 8) return launch_rows<T, ASK, 256, 32, 8, false>(s, p, o, 1, st);
-    if (words > 8 * 256 * 16) return launch_rows<T, ASK, 256, 256, 8, true>(s, p, o, 8, st);
+    if (words <= 32 * 8) return launch_policy<T, 256, 32, 8, false>(s, p, o, 1, ws, st);
+    if (words > 8 * 256 * 16) return launch_policy<T, 256, 256, 8, true>(s, p, o, 8, ws, st);
     int ctas = 1;
     while (words > (int64_t)ctas * 256 * 16) ctas *= 2;
     // few rows: more CTAs for each, down to a word a thread
     while (ctas < 8 && s.rows * ctas < device_sms() && words > (int64_t)ctas * 256) ctas *= 2;
-    if (words <= ctas * 128 * 8) return launch_rows<T, ASK, 128, 128, 8, false>(s, p, o, ctas, st);
-    if (words <= ctas * 256 * 8) return launch_rows<T, ASK, 256, 256, 8, false>(s, p, o, ctas, st);
-    return launch_rows<T, ASK, 256, 256, 16, false>(s, p, o, ctas, st);
+    if (words <= ctas * 128 * 8) return launch_policy<T, 128, 128, 8, false>(s, p, o, ctas, ws, st);
+    if (words <= ctas * 256 * 8) return launch_policy<T, 256, 256, 8, false>(s, p, o, ctas, ws, st);
+    return launch_policy<T, 256, 256, 16, false>(s, p, o, ctas, ws, st);
 }
 
-// Rows of up to 4 KB by warps; longer ones as a stream, by as many CTAs a row (up to 8) as make
-// the slowest team's share smallest: a row costs a team its groups and about one more for the
-// meeting at its end.
+// Rows of up to 4 KB by warps; longer ones by as many CTAs a row (up to 8) as make the slowest
+// team's share smallest: a row costs a team its groups and about one more for the meeting at its end.
 template <class T>
-cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, unsigned* zero_ticket, cudaStream_t st) {
+cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, void* ws, bool zero_ticket, cudaStream_t st) {
     constexpr int NT = 256, U = 4, D = 4;
+    constexpr size_t shared = (size_t)NT * U * D * 16;
     const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
-    auto* kernel = score_stream_kernel<T, NT, U, D>;
-    static int held[64][4];
+    const bool warps = words <= 32 * 8;
+    const int per_cta = warps ? NT / 32 : 1;
+    auto* kernel = warps ? score_stream_kernel<T, NT, 32, U, D> : score_stream_kernel<T, NT, NT, U, D>;
+    static int held[2][64][4];
     int best = 1, best_fit = 1;
     double least = 0.0;
-    for (int ctas = 1; ctas <= 8 && (ctas == 1 || words >= (int64_t)ctas * NT); ctas *= 2) {
-        ClusterLaunch l(1, NT, (size_t)NT * U * D * 16, ctas, false, st);
+    for (int ctas = 1; ctas <= 8 && (ctas == 1 || (!warps && words >= (int64_t)ctas * NT)); ctas *= 2) {
+        ClusterLaunch l(1, NT, shared, ctas, false, st);
         int fit = 0;
-        const cudaError_t e = clusters_held(kernel, l.c, ctas, held, &fit);
+        const cudaError_t e = clusters_held(kernel, l.c, ctas, held[warps], &fit);
         if (e != cudaSuccess) return e;
         const int64_t groups = (words + (int64_t)ctas * NT * U - 1) / ((int64_t)ctas * NT * U);
         const double cost = (double)((s.rows + fit - 1) / fit) * (double)(groups + 1);
@@ -795,8 +802,15 @@ cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, unsigned* zero_ticket
             least = cost;
         }
     }
-    ClusterLaunch l(std::min<int64_t>(s.rows, best_fit) * best, NT, (size_t)NT * U * D * 16, best, false, st);
-    return l(kernel, s, o, zero_ticket);
+    const int64_t grid = std::min<int64_t>((s.rows + per_cta - 1) / per_cta, best_fit);
+    const bool list = s.rows > grid * per_cta;
+    if (list) {
+        const cudaError_t e = make_list(s, ws, true, st);
+        if (e != cudaSuccess) return e;
+    }
+    ClusterLaunch l(grid * best, NT, shared, best, list, st);
+    return l(kernel, s, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr},
+             zero_ticket && !list ? &list_head(ws)->ticket : nullptr);
 }
 
 // Whether the gradient's rows start at the same place within 16 bytes as the scores' rows.
@@ -808,10 +822,12 @@ inline int words_agree(const ScoreRows& s, const void* out, int64_t out_stride, 
 
 }  // namespace
 
-cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, float* zero_coef,
-                       unsigned* zero_ticket, uint32_t* row_status, cudaStream_t st) {
-    const RowOuts o{logp, norm, zero_coef, nullptr, 0, 0, row_status};
-    return by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, zero_ticket, st); });
+size_t token_logp_workspace(int64_t rows) { return list_bytes(rows); }
+
+cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, void* ws,
+                       uint32_t* row_status, cudaStream_t st) {
+    const RowOuts o{logp, norm, nullptr, nullptr, 0, 0, row_status};
+    return by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, ws, false, st); });
 }
 
 cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,
@@ -823,42 +839,40 @@ cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm
         using T = decltype(t);
         constexpr int NT = 256, K = 4;
         const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
-        const int parts = (int)std::max<int64_t>(1, (words + NT * K - 1) / (NT * K));
-        ClusterLaunch l(std::min<int64_t>(s.rows * parts, 1 << 30), NT, 0, 1, true, st);
-        return l(score_backward_kernel<T, NT, K>, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, parts);
+        const bool warps = words <= 32 * 8;
+        const int parts = warps ? 1 : (int)((words + NT * K - 1) / (NT * K));
+        const int64_t ctas = warps ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows * parts;
+        ClusterLaunch l(std::min<int64_t>(ctas, 1 << 30), NT, 0, 1, true, st);
+        auto* kernel = warps ? score_backward_kernel<T, NT, 32, K> : score_backward_kernel<T, NT, NT, K>;
+        return l(kernel, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, parts);
     });
 }
 
 size_t policy_workspace(int64_t rows) {
-    return align256o(sizeof(PolicyShared) + (size_t)std::min<int64_t>((rows + 7) / 8 * 8, kMaxTeams) * sizeof(PolicyTerms));
+    return list_bytes(rows) + align256o((size_t)std::min<int64_t>((rows + 7) / 8 * 8, kMaxTeams) * sizeof(PolicyTerms));
 }
 
-cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& args, void* out,
+cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& p, void* out,
                         int64_t out_stride, void* ws, uint32_t* row_status, cudaStream_t st) {
-    PolicyArgs p = args;
-    p.shared = static_cast<PolicyShared*>(ws);
     if (s.rows == 0) {
         zero_kernel<<<1, 32, 0, st>>>(p.loss, 1, p.stats, 3);
         return cudaGetLastError();
     }
-    const int counting = s.rows > 16384 ? 8 : 1;
-    ClusterLaunch l(counting, 1024, 0, counting, false, st);
-    const cudaError_t e = l(policy_begin_kernel, p.weights ? nullptr : s.labels, s.rows, p.shared);
-    if (e != cudaSuccess) return e;
     const RowOuts o{p.logp, p.norm, p.coef, out, out_stride, out ? words_agree(s, out, out_stride, dtype) : 0, row_status};
-    return by_type(dtype, [&](auto t) { return run_policy<decltype(t)>(s, p, o, st); });
+    return by_type(dtype, [&](auto t) { return run_policy<decltype(t)>(s, p, o, ws, st); });
 }
 
-size_t preference_workspace(int64_t, int64_t pairs) { return align256o((size_t)pairs * 4) + 256; }
+size_t preference_workspace(int64_t rows, int64_t pairs) { return list_bytes(rows) + align256o((size_t)pairs * 4); }
 
 cudaError_t preference_loss(int dtype, const ScoreRows& s, PreferenceArgs p, float* logp,
                             float* norm, float* coef, float grad_scale, void* out,
                             int64_t out_stride, void* ws, uint32_t* row_status, cudaStream_t st) {
-    p.ticket = static_cast<unsigned*>(ws);
-    p.each = reinterpret_cast<float*>(p.ticket + 64);
+    p.ticket = &list_head(ws)->ticket;
+    p.each = reinterpret_cast<float*>(after_list(ws, s.rows));
     cudaError_t e = cudaSuccess;
     if (s.rows > 0) {
-        e = token_logp(dtype, s, logp, norm, coef, p.ticket, row_status, st);
+        const RowOuts o{logp, norm, coef, nullptr, 0, 0, row_status};
+        e = by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, ws, true, st); });
     } else {  // pairs of empty sequences: the ticket's zero
         zero_kernel<<<1, 32, 0, st>>>(reinterpret_cast<float*>(p.ticket), 1, nullptr, 0);
         e = cudaGetLastError();

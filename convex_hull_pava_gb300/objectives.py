@@ -26,17 +26,12 @@ run on ``stream`` (default: the current one); what they allocate belongs to it.
 """
 from __future__ import annotations
 
-from collections import namedtuple
-
 from . import ISO_OK, IsoError, _torch, load_library
 
 MAX_EXPERTS = 1024   # ISO_MAX_EXPERTS
 MAX_TOP_K = 32       # ISO_MAX_TOP_K
 ISO_ROW_BAD_LABEL = 8
 KINDS = {"sigmoid": 0, "hinge": 1, "squared": 2}
-
-BalanceLoss = namedtuple("BalanceLoss", "loss counts experts gates live mask renormalize")
-
 
 class _Result:
     """Named outputs, some of them views of one buffer that are made when they are asked for."""
@@ -73,6 +68,26 @@ class PreferenceLoss(_Result):
     """What :func:`iso_preference_loss` returns."""
     _fields = ("loss", "margins", "seq_logp", "logp", "norm", "coef", "dlogits", "row_status", "pair_status")
     __slots__ = ("loss", "margins", "seq_logp", "logp", "dlogits", "pair_status")
+
+
+class BalanceLoss:
+    """What :func:`iso_balance_loss` returns."""
+    _fields = ("loss", "counts", "experts", "gates", "live", "mask", "renormalize")
+    __slots__ = ("loss", "counts", "experts", "gates", "mask", "renormalize", "_buf")
+
+    def __init__(self, loss, counts, experts, gates, buf, mask, renormalize):
+        self.loss, self.counts, self.experts, self.gates = loss, counts, experts, gates
+        self._buf, self.mask, self.renormalize = buf, mask, renormalize
+
+    def __iter__(self):
+        return (getattr(self, name) for name in self._fields)
+
+    def __len__(self):
+        return len(self._fields)
+
+    @property
+    def live(self):
+        return self._buf[0]   # int64; the call's workspace follows
 
 
 _abi = None      # the loaded library
@@ -171,7 +186,7 @@ def _own_workspace(workspace, device):
     return workspace.data_ptr(), workspace.numel()
 
 
-def iso_token_logp(logits, labels, *, temperature: float = 1.0, stream=None):
+def iso_token_logp(logits, labels, *, temperature: float = 1.0, workspace=None, stream=None):
     """The labels' log-probabilities.  Returns ``(logp, norm, row_status)``: float32 of the
     labels' shape; the rows' softmax statistics ``[rows, 2]`` for the backward; int32 ``[rows]``."""
     code, rows, n, stride, dev = _scores(logits)
@@ -180,13 +195,19 @@ def iso_token_logp(logits, labels, *, temperature: float = 1.0, stream=None):
     there = _elsewhere(torch, dev, stream)
     if there is not None:
         with there:
-            return iso_token_logp(logits, labels, temperature=temperature)
+            return iso_token_logp(logits, labels, temperature=temperature, workspace=workspace)
     logp = torch.empty(labels.shape, dtype=torch.float32, device=dev)
     norm = torch.empty((rows, 2), dtype=torch.float32, device=dev)
-    status = torch.empty(rows, dtype=torch.int32, device=dev)
+    need = _abi.iso_token_logp_workspace_bytes(rows)
+    if workspace is None:   # the statuses behind it
+        buf = torch.empty((need >> 2) + rows, dtype=torch.int32, device=dev)
+        ws, ws_bytes, status = buf.data_ptr(), need, buf[need >> 2:]
+    else:
+        ws, ws_bytes = _own_workspace(workspace, dev)
+        status = torch.empty(rows, dtype=torch.int32, device=dev)
     _done(_abi.iso_token_logp(
         logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), temperature, logp.data_ptr(),
-        norm.data_ptr(), status.data_ptr(), _raw_stream(dev.index)), "iso_token_logp")
+        norm.data_ptr(), ws, ws_bytes, status.data_ptr(), _raw_stream(dev.index)), "iso_token_logp")
     return logp, norm, status
 
 
@@ -359,28 +380,27 @@ def iso_balance_loss(logits, top_k: int, mask=None, *, renormalize: bool = False
     counts = torch.empty(experts, dtype=torch.int64, device=dev)
     chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
     gates = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
-    live = torch.empty((), dtype=torch.int64, device=dev)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws, ws_bytes = _own_workspace(workspace, dev)
+    buf = torch.empty(32 + (need >> 3 if workspace is None else 0), dtype=torch.int64, device=dev)
+    live = buf.data_ptr()
+    ws, ws_bytes = (live + 256, need) if workspace is None else _own_workspace(workspace, dev)
     renormalize = bool(renormalize)
     _done(_abi.iso_balance_loss(
         logits.data_ptr(), code, tokens, experts, stride, top_k, _ptr(mask), renormalize,
-        loss.data_ptr(), counts.data_ptr(), chosen.data_ptr(), gates.data_ptr(), live.data_ptr(),
-        ws, ws_bytes, _raw_stream(dev.index)), "iso_balance_loss")
-    return BalanceLoss(loss, counts, chosen, gates, live, mask, renormalize)
+        loss.data_ptr(), counts.data_ptr(), chosen.data_ptr(), gates.data_ptr(), live, ws, ws_bytes,
+        _raw_stream(dev.index)), "iso_balance_loss")
+    return BalanceLoss(loss, counts, chosen, gates, buf, mask, renormalize)
 
 
 def iso_balance_loss_backward(logits, result, *, grad_loss: float = 1.0, grad_loss_dev=None,
                               grad_gates=None, out=None, stream=None):
     """The gradient of ``grad_loss * grad_loss_dev * loss + sum(grad_gates * gates)`` in the
     logits, ``result`` being :func:`iso_balance_loss`'s for them."""
+    if not isinstance(result, BalanceLoss):
+        raise ValueError("result must be iso_balance_loss's")
     shape = result.experts.shape
     torch, code, tokens, experts, stride, dev, mask = _router(logits, shape[1], result.mask)
-    _check(result.experts, "experts", torch.int32, (tokens, shape[1]), dev)
-    _check(result.gates, "gates", torch.float32, shape, dev)
-    _check(result.counts, "counts", torch.int64, (experts,), dev)
-    _check(result.live, "live", torch.int64, (), dev)
+    if shape[0] != tokens or result.counts.numel() != experts or result.counts.device != dev:
+        raise ValueError("logits must have the shape and device that result was made for")
     if grad_gates is not None:
         _check(grad_gates, "grad_gates", torch.float32, shape, dev)
     if grad_loss_dev is not None:
@@ -398,7 +418,7 @@ def iso_balance_loss_backward(logits, result, *, grad_loss: float = 1.0, grad_lo
     _done(_abi.iso_balance_loss_backward(
         logits.data_ptr(), code, tokens, experts, stride, shape[1], _ptr(mask),
         result.renormalize, result.counts.data_ptr(), result.experts.data_ptr(),
-        result.gates.data_ptr(), result.live.data_ptr(), _ptr(grad_gates), grad_loss,
+        result.gates.data_ptr(), result._buf.data_ptr(), _ptr(grad_gates), grad_loss,
         _ptr(grad_loss_dev), out.data_ptr(), out_stride, _raw_stream(dev.index)),
         "iso_balance_loss_backward")
     return out
@@ -463,17 +483,17 @@ def _make():
         def forward(ctx, logits, top_k, mask, renormalize):
             ctx.set_materialize_grads(False)
             r = iso_balance_loss(logits, top_k, mask, renormalize=renormalize)
-            ctx.save_for_backward(logits, r.counts, r.experts, r.gates, r.live, r.mask)
+            ctx.save_for_backward(logits, r.counts, r.experts, r.gates, r._buf, r.mask)
             ctx.renormalize = renormalize
             ctx.mark_non_differentiable(r.counts, r.experts)
             return r.loss, r.gates, r.counts, r.experts
 
         @staticmethod
         def backward(ctx, g_loss, g_gates, *_):
-            logits, counts, experts, gates, live, mask = ctx.saved_tensors
+            logits, counts, experts, gates, buf, mask = ctx.saved_tensors
             if g_loss is None and g_gates is None:
                 return (None,) * 4
-            r = BalanceLoss(None, counts, experts, gates, live, mask, ctx.renormalize)
+            r = BalanceLoss(None, counts, experts, gates, buf, mask, ctx.renormalize)
             return iso_balance_loss_backward(
                 logits, r, grad_loss=0.0 if g_loss is None else 1.0,
                 grad_loss_dev=None if g_loss is None else g_loss.contiguous(),

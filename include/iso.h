@@ -325,8 +325,9 @@ iso_status iso_backward_noalloc(const float *grad, const uint8_t *blocks, const 
  *    value is an ordinary, very small score.  A row with a NaN or +inf, or
  *    with nothing but -inf, has no probabilities: its log-probability and
  *    gradient are NaN and its row_status has ISO_ROW_BAD_Y.
- *  - norm [rows, 2]: the row's largest score and sum_j exp((x[r, j] - largest) / T),
- *    from which the backward forms p without another pass.
+ *  - norm [rows, 2], 8-byte aligned: the row's softmax statistics (its largest score and the sum
+ *    of exponentials against it), from which the backward forms p without another pass.
+ *  - The gradient may be written over the scores (dlogits == logits, out_stride == stride).
  * ------------------------------------------------------------------------ */
 typedef enum { ISO_F32 = 0, ISO_BF16 = 1, ISO_F16 = 2 } iso_dtype;
 #define ISO_ROW_BAD_LABEL 8u /* the row's label is not below n                   */
@@ -336,11 +337,14 @@ typedef enum { ISO_F32 = 0, ISO_BF16 = 1, ISO_F16 = 2 } iso_dtype;
  *
  *  logp       [rows], written: lp_r, or 0 for a row without a label.
  *  norm       [rows, 2], written.
+ *  workspace  iso_token_logp_workspace_bytes(rows) bytes, 256-byte aligned.
  *  row_status [rows] uint32, written, or NULL.
  */
+size_t iso_token_logp_workspace_bytes(int64_t rows);
 iso_status iso_token_logp(const void *logits, int dtype, int64_t rows, int64_t n, int64_t stride,
                           const int64_t *labels, float temperature, float *logp, float *norm,
-                          uint32_t *row_status, void *stream);
+                          void *workspace, size_t workspace_bytes, uint32_t *row_status,
+                          void *stream);
 
 /*
  * iso_token_logp_backward -- dlogits[r, j] = g_r / T ([j == l_r] - p[r, j]) with

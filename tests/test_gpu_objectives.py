@@ -511,3 +511,51 @@ def test_refusals(cuda_ok):
     b = obj.iso_balance_loss(x, 2)
     no(obj.iso_balance_loss_backward, x[:3], b)
     no(obj.iso_balance_loss_backward, x, b, grad_gates=f)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,n,ignored", [(5000, 70, 0.3), (4100, 1999, 0.5), (1500, 5003, 0.25), (90, 131072, 0.3),
+                                            (1100, 6000, 0.999), (1100, 6000, 0.0)])
+def test_many_rows(cuda_ok, rows, n, ignored, dtype):
+    """More rows than the GPU takes at once, with and without a label, in one call of each."""
+    from convex_hull_pava_gb300 import objectives as obj
+    x, xw, labels, rng = make(rows, n, dtype, seed=rows, ignored=ignored)
+    lp, norm, st = obj.iso_token_logp(x, ids(labels))
+    want = ref.token_logp(xw, labels)
+    assert (np.abs(wide(lp) - want) <= lp_tol(want)).all() and not st.any()
+    g = rng.standard_normal(rows).astype(np.float32)
+    check_grad(obj.iso_token_logp_backward(put(g), x, ids(labels), norm), xw, labels, g.astype(np.float64),
+               np.zeros(rows), dtype)
+    old, adv, _ = policy_inputs(xw, labels, rng, 1.0)
+    r = obj.iso_policy_loss(x, ids(labels), put(old), put(adv), clip_high=0.3, grad_scale=1024.0)
+    loss, stats, lp, coef = ref.policy(xw, labels, old, adv, high=0.3)
+    live = labels >= 0
+    with np.errstate(all="ignore"):
+        size = np.where(live, np.abs(adv) * np.exp(lp - old), 0.0) / max(1, live.sum())
+    coef_tol = size * (lp_tol(lp) + 1e-6)
+    assert (np.abs(wide(r.coef) - coef) <= coef_tol).all()
+    assert abs(float(r.loss) - loss) <= coef_tol.sum() + 1e-6 * abs(loss) + 1e-7
+    check_grad(r.dlogits, xw, labels, coef, coef_tol, dtype, 1.0, 1024.0)
+    off = np.linspace(0, rows, 2 * min(40, rows // 2) + 1).astype(np.int64)
+    r = obj.iso_preference_loss(x, ids(labels), ids(off), beta=0.01, average=True)
+    loss, z, seq, lp, coef = ref.preference(xw, labels, off.tolist(), beta=0.01, average=True)
+    assert np.abs(wide(r.margins) - z).max() <= 0.02 * lp_tol(lp).max() + 1e-6 * np.abs(z).max()
+    assert (np.abs(wide(r.logp) - lp) <= lp_tol(lp)).all()
+    check_grad(r.dlogits, xw, labels, coef, 1e-5 * np.abs(coef), dtype)
+
+
+def test_gradient_over_the_scores(cuda_ok):
+    """`out` may be the scores themselves."""
+    from convex_hull_pava_gb300 import objectives as obj
+    for rows, n, dtype in ((40, 300, "bf16"), (9, 30011, "bf16"), (3, 131072, "f32"), (2, 600011, "bf16")):
+        x, xw, labels, rng = make(rows, n, dtype, seed=n)
+        old, adv, base = [put(v) for v in policy_inputs(xw, labels, rng, 1.0)]
+        want = obj.iso_policy_loss(x, ids(labels), old, adv, base, kl_coef=0.1).dlogits
+        y = x.clone()
+        obj.iso_policy_loss(y, ids(labels), old, adv, base, kl_coef=0.1, out=y)
+        assert bool((y == want).all())
+        lp, norm, _ = obj.iso_token_logp(x, ids(labels))
+        want = obj.iso_token_logp_backward(adv.nan_to_num(), x, ids(labels), norm)
+        y = x.clone()
+        obj.iso_token_logp_backward(adv.nan_to_num(), y, ids(labels), norm, out=y)
+        assert bool((y == want).all())

@@ -91,14 +91,19 @@ def test_objective_argument_checks():
     p, ws = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x100000)
     bad, no_ws = chp.ISO_ERR_INVALID_ARG, chp.ISO_ERR_WORKSPACE
 
-    def logp(x=p, dt=0, rows=4, n=10, stride=10, labels=p, t=1.0, lp=p, norm=p):
-        return lib.iso_token_logp(x, dt, rows, n, stride, labels, t, lp, norm, None, None)
+    need0 = lib.iso_token_logp_workspace_bytes(4)
+    assert need0 > 0 and lib.iso_token_logp_workspace_bytes(-1) == 0
+
+    def logp(x=p, dt=0, rows=4, n=10, stride=10, labels=p, t=1.0, lp=p, norm=p, w=ws, wb=need0):
+        return lib.iso_token_logp(x, dt, rows, n, stride, labels, t, lp, norm, w, wb, None, None)
 
     assert logp(rows=0, x=None, labels=None, lp=None, norm=None) == chp.ISO_OK
     for kw in (dict(x=None), dict(dt=3), dict(dt=-1), dict(rows=-1), dict(n=0), dict(n=1 << 31), dict(stride=-1),
                dict(rows=1 << 31), dict(rows=1 << 30, stride=1 << 30), dict(labels=None), dict(t=0.0), dict(t=-1.0),
                dict(t=float("nan")), dict(t=float("inf")), dict(t=1e-39), dict(lp=None), dict(norm=None)):
         assert logp(**kw) == bad, kw
+    for kw in (dict(w=None), dict(wb=need0 - 1), dict(w=ctypes.c_void_p(0x100010))):
+        assert logp(**kw) == no_ws, kw
 
     def back(x=p, norm=p, g=p, changed=0, out=p, out_stride=10, n=10):
         return lib.iso_token_logp_backward(x, 1, 4, n, 10, p, 1.0, norm, g, 1.0, None, changed, out, out_stride, None)
