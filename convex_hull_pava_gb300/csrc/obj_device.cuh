@@ -138,7 +138,7 @@ __device__ __forceinline__ void copy_async(void* shared, const void* global) {
 __device__ __forceinline__ void copy_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -274,6 +274,47 @@ __device__ __forceinline__ void store_remote(int* place, int cta, int v) {
 
 __device__ __forceinline__ void store_remote(float* place, int cta, float v) {
     store_remote(reinterpret_cast<int*>(place), cta, __float_as_int(v));
+}
+
+// Barriers in shared memory that count bytes: what the CTAs of a cluster send one another without
+// waiting for their stores to global memory, as a barrier of the whole cluster would.
+__device__ __forceinline__ void bytes_init(uint64_t* bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)) : "memory");
+}
+__device__ __forceinline__ void bytes_fence_init() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+// The current phase ends when `bytes` have come.
+__device__ __forceinline__ void bytes_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(bytes) : "memory");
+}
+// Waits for the end of the phase of that parity; false when it has not come within two seconds.
+__device__ __forceinline__ bool bytes_wait(uint64_t* bar, uint32_t parity) {
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(bar);
+    uint64_t since = 0;
+    for (uint32_t i = 1;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        if (done) return true;
+        if ((i & 255u) == 0u) {
+            uint64_t now;
+            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+            if (since == 0) since = now;
+            if (now - since > 2000000000ull) return false;
+        }
+    }
+}
+// Sends a state to the same place of another CTA, and its 8 bytes to that CTA's barrier.
+__device__ __forceinline__ void send_remote(SoftState* place, uint64_t* bar, int cta, SoftState st) {
+    uint32_t at, b;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at) : "r"((uint32_t)__cvta_generic_to_shared(place)), "r"(cta));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(b) : "r"((uint32_t)__cvta_generic_to_shared(bar)), "r"(cta));
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
+                 ::"r"(at), "r"(__float_as_uint(st.m)), "r"(__float_as_uint(st.s)), "r"(b) : "memory");
 }
 
 // A float32 sum that keeps what its additions round off: about 48 bits, without 64-bit arithmetic

@@ -165,6 +165,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     constexpr int N = Word<T>::N, W = NT / 32;
     extern __shared__ uint4 ahead_words[];
     __shared__ SoftState part[2][TEAM == 32 ? 2 : 8 * W];
+    __shared__ uint64_t come[2];
     const int ctas = TEAM == 32 ? 1 : (int)cluster_size(), rank = TEAM == 32 ? 0 : (int)cluster_rank();
     const int shift = 31 - __clz(ctas);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -205,6 +206,17 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         if (e >= 0) out[e] = from_f32<T>(0.f);
     };
 
+    if (ctas > 1) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < 2; ++i) {
+                bytes_init(&come[i]);
+                bytes_expect(&come[i], ctas * W * (int)sizeof(SoftState));
+            }
+            bytes_fence_init();
+        }
+        cluster_sync();
+    }
+    bool lost = false;  // a wait for the other CTAs has run out
     let_next_start();
     if (rl.list) wait_for_previous();
     // the team's rows: the current one, the next (its words copied while the current one's turn
@@ -295,15 +307,18 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         if (TEAM != 32) {
             // Two sets of places in turn: a CTA that writes to one again has been through the
             // meeting in between, for which every thread had read the first.
-            SoftState* slot = part[turn++ & 1];
+            SoftState* slot = part[turn & 1];
             if (ctas == 1) {
                 if (lane == 0) slot[warp] = st;
                 __syncthreads();
             } else {
-                if (lane < ctas) store_remote(&slot[rank * W + warp], lane, st);
-                __syncwarp();
-                cluster_sync();
+                // Not a barrier of the cluster: that would wait for the last row's gradient to be written.
+                uint64_t* bar = &come[turn & 1];
+                if (lane < ctas) send_remote(&slot[rank * W + warp], bar, lane, st);
+                if (!lost) lost = !bytes_wait(bar, turn >> 1 & 1);
+                if (threadIdx.x == 0) bytes_expect(bar, ctas * W * (int)sizeof(SoftState));  // for the row after next
             }
+            ++turn;
             constexpr int P = 8 * W / 32;
             SoftState q[P];
             float m = -INFINITY;
@@ -317,7 +332,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             float t = 0.f;
 #pragma unroll
             for (int i = 0; i < P; ++i) t += q[i].s * ref.factor(q[i].m);
-            st.s = warp_add(t);
+            st.s = lost ? NAN : warp_add(t);
         }
 
         const SoftRef ref(st.m, a);
@@ -327,7 +342,8 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             o.logp[r] = lp;
             *reinterpret_cast<float2*>(o.norm + 2 * r) = {st.m, st.s};
             o.coef[r] = q.coef;
-            if (o.status) o.status[r] = norm_status(st) | (cur.label >= n ? ISO_ROW_BAD_LABEL : 0u);
+            if (o.status)
+                o.status[r] = norm_status(st) | (cur.label >= n ? ISO_ROW_BAD_LABEL : 0u) | (lost ? ISO_ROW_TIMEOUT : 0u);
             terms.v[0].add(q.pg);
             terms.v[1].add(q.kl);
             terms.v[2].add(q.cut);

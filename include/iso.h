@@ -331,6 +331,8 @@ iso_status iso_backward_noalloc(const float *grad, const uint8_t *blocks, const 
  * ------------------------------------------------------------------------ */
 typedef enum { ISO_F32 = 0, ISO_BF16 = 1, ISO_F16 = 2 } iso_dtype;
 #define ISO_ROW_BAD_LABEL 8u /* the row's label is not below n                   */
+#define ISO_ROW_TIMEOUT 16u  /* a bounded wait of the row's CTAs for one another */
+                             /* gave up (a fault of the GPU); the row is NaN     */
 
 /*
  * iso_token_logp -- the labels' log-probabilities.
