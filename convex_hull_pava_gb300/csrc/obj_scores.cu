@@ -49,7 +49,7 @@ struct PolicyRow {
 
 __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, float logp, float old,
                                                 float adv, float ref, float w) {
-    const float ratio = expf(logp - old);
+    const float ratio = ex2((logp - old) * kLog2e);
     const float free = -adv * ratio;
     const float held = -adv * fminf(fmaxf(ratio, p.low), p.high);
     const bool cut = held > free;
@@ -160,7 +160,7 @@ __device__ __forceinline__ void unlabelled_row(const RowOuts& o, int64_t r) {
 // row's (maximum, sum); the warps of a cluster write theirs to every CTA and meet once a row.
 // LONG: rows longer than the team's registers are read twice, the second time from L2.
 template <class T, int NT, int TEAM, int K, bool LONG>
-__global__ void __launch_bounds__(NT, NT * K >= 4096 ? 2 : NT == 128 ? 6 : 3)
+__global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT * K >= 4096 ? 2 : NT == 128 ? 6 : 3)
 policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     constexpr int N = Word<T>::N, W = NT / 32;
     extern __shared__ uint4 ahead_words[];
@@ -242,7 +242,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         row3 = item(at + 3 * teams);
         float at_label = NAN, old = 0.f, adv = 0.f, base_lp = 0.f, weight = 0.f;
         if (cur.label >= 0) {
-            if (cur.label < n) at_label = to_f32(base[r * sc.stride + cur.label]);
+            if (lane == 0 && cur.label < n) at_label = to_f32(base[r * sc.stride + cur.label]);
             old = p.old_logp[r];
             adv = p.advantages[r];
             if (p.ref_logp) base_lp = p.ref_logp[r];
@@ -304,6 +304,9 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             }
             st = soft_warp(st, a);
         }
+        // Every warp has the label's score before it lets the others go on, who may write the gradient
+        // over it.
+        at_label = __shfl_sync(~0u, at_label, 0);
         if (TEAM != 32) {
             // Two sets of places in turn: a CTA that writes to one again has been through the
             // meeting in between, for which every thread had read the first.
@@ -336,7 +339,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         }
 
         const SoftRef ref(st.m, a);
-        const float lp = ref.of(at_label) * kLn2 - logf(st.s);
+        const float lp = (ref.of(at_label) - log2_of(st.s)) * kLn2;
         const PolicyRow q = policy_row(p, lp, old, adv, base_lp, weight);
         if (rank == 0 && tt == 0) {
             o.logp[r] = lp;
@@ -351,7 +354,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         if (!o.out) continue;
 
         const float g = q.coef * p.grad_scale * sc.inv_t;
-        const RowGrad<T> grad{g, -g / st.s, ref};
+        const RowGrad<T> grad{g, __fdividef(-g, st.s), ref};
         if (!LONG && o.out_words) {
             uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first + tt;
             auto give = [&](auto far) {
@@ -789,6 +792,7 @@ cudaError_t run_policy(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o
     while (ctas < 8 && s.rows * ctas < device_sms() && words > (int64_t)ctas * 256) ctas *= 2;
     if (words <= ctas * 128 * 8) return launch_policy<T, 128, 128, 8, false>(s, p, o, ctas, ws, st);
     if (words <= ctas * 256 * 8) return launch_policy<T, 256, 256, 8, false>(s, p, o, ctas, ws, st);
+    if (getenv("X512")) return launch_policy<T, 512, 512, 8, false>(s, p, o, ctas, ws, st);
     return launch_policy<T, 256, 256, 16, false>(s, p, o, ctas, ws, st);
 }
 
