@@ -25,7 +25,7 @@ bool rows_ok(int dtype, int64_t rows, int64_t n, int64_t stride, int64_t least) 
 bool temperature_ok(float t) { return std::isfinite(t) && t > 0.f && std::isfinite(1.f / t); }
 
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
-    return ws && bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0;
+    return need == 0 || (ws && bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
 }
 
 isodev::ScoreRows score_rows(const void* logits, int64_t rows, int64_t n, int64_t stride,

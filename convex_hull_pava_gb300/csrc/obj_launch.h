@@ -23,12 +23,17 @@ struct ClusterLaunch {
         c.dynamicSmemBytes = shared;
         c.stream = st;
         c.attrs = at;
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = ctas;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        at[1].val.programmaticStreamSerializationAllowed = 1;
-        c.numAttrs = early ? 2 : 1;
+        if (ctas > 1) {
+            at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            at[c.numAttrs].val.clusterDim.x = ctas;
+            at[c.numAttrs].val.clusterDim.y = at[c.numAttrs].val.clusterDim.z = 1;
+            ++c.numAttrs;
+        }
+        if (early) {
+            at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            at[c.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+            ++c.numAttrs;
+        }
     }
     ClusterLaunch(const ClusterLaunch&) = delete;
     template <class... P, class... A>

@@ -749,6 +749,9 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
     }
 }
 
+// Rows that log-probabilities alone need no list for.
+constexpr int64_t kNoList = 64;
+
 // The workspace: a head, the list of rows, what follows.
 inline size_t list_bytes(int64_t rows) { return 256 + align256o((size_t)rows * 4); }
 inline ListHead* list_head(void* ws) { return static_cast<ListHead*>(ws); }
@@ -822,8 +825,8 @@ cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, void* ws, bool zero_t
             least = cost;
         }
     }
-    const int64_t grid = std::min<int64_t>((s.rows + per_cta - 1) / per_cta, best_fit);
-    const bool list = s.rows > grid * per_cta;
+    const int64_t grid = std::min<int64_t>((s.rows + per_cta - 1) / per_cta, std::max<int64_t>(best_fit, kNoList));
+    const bool list = s.rows > grid * per_cta;  // (never for up to kNoList rows)
     if (list) {
         const cudaError_t e = make_list(s, ws, true, st);
         if (e != cudaSuccess) return e;
@@ -842,7 +845,7 @@ inline int words_agree(const ScoreRows& s, const void* out, int64_t out_stride, 
 
 }  // namespace
 
-size_t token_logp_workspace(int64_t rows) { return list_bytes(rows); }
+size_t token_logp_workspace(int64_t rows) { return rows <= kNoList ? 0 : list_bytes(rows); }
 
 cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, void* ws,
                        uint32_t* row_status, cudaStream_t st) {

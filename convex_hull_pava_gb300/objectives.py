@@ -67,7 +67,11 @@ class PolicyLoss(_Result):
 class PreferenceLoss(_Result):
     """What :func:`iso_preference_loss` returns."""
     _fields = ("loss", "margins", "seq_logp", "logp", "norm", "coef", "dlogits", "row_status", "pair_status")
-    __slots__ = ("loss", "margins", "seq_logp", "logp", "dlogits", "pair_status")
+    __slots__ = ("loss", "margins", "seq_logp", "logp", "dlogits")
+
+    @property
+    def pair_status(self):
+        return self._buf[:self.margins.numel()].view(_torch().int32)
 
 
 class BalanceLoss:
@@ -198,16 +202,17 @@ def iso_token_logp(logits, labels, *, temperature: float = 1.0, workspace=None, 
             return iso_token_logp(logits, labels, temperature=temperature, workspace=workspace)
     logp = torch.empty(labels.shape, dtype=torch.float32, device=dev)
     norm = torch.empty((rows, 2), dtype=torch.float32, device=dev)
+    status = torch.empty(rows, dtype=torch.int32, device=dev)
     need = _abi.iso_token_logp_workspace_bytes(rows)
-    if workspace is None:   # the statuses behind it
-        buf = torch.empty((need >> 2) + rows, dtype=torch.int32, device=dev)
-        ws, ws_bytes, status = buf.data_ptr(), need, buf[need >> 2:]
-    else:
-        ws, ws_bytes = _own_workspace(workspace, dev)
-        status = torch.empty(rows, dtype=torch.int32, device=dev)
+    ws = None
+    if workspace is not None:
+        ws, need = _own_workspace(workspace, dev)
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws = workspace.data_ptr()
     _done(_abi.iso_token_logp(
         logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), temperature, logp.data_ptr(),
-        norm.data_ptr(), ws, ws_bytes, status.data_ptr(), _raw_stream(dev.index)), "iso_token_logp")
+        norm.data_ptr(), ws, need, status.data_ptr(), _raw_stream(dev.index)), "iso_token_logp")
     return logp, norm, status
 
 
@@ -330,10 +335,11 @@ def iso_preference_loss(logits, labels, offsets, ref_logp=None, *, kind: str = "
     r.margins = margins = torch.empty(pairs, dtype=f32, device=dev)
     r.seq_logp = seq_logp = torch.empty(2 * pairs, dtype=f32, device=dev)
     r.logp = logp = torch.empty(shape, dtype=f32, device=dev)
-    r.pair_status = pair_status = torch.empty(pairs, dtype=torch.int32, device=dev)
-    r._buf = buf = torch.empty((need >> 2) + 4 * rows, dtype=f32, device=dev)
-    ws, ws_bytes = (buf.data_ptr(), need) if workspace is None else _own_workspace(workspace, dev)
-    rest = buf.data_ptr() + need
+    head = (pairs + 63) // 64 * 256   # bytes of the pairs' statuses, the workspace behind them
+    r._buf = buf = torch.empty((head + need >> 2) + 4 * rows, dtype=f32, device=dev)
+    pair_status = buf.data_ptr()
+    ws, ws_bytes = (pair_status + head, need) if workspace is None else _own_workspace(workspace, dev)
+    rest = pair_status + head + need
     out_stride = n
     if out is not None:
         out_stride = _check_out(out, logits)
@@ -344,7 +350,7 @@ def iso_preference_loss(logits, labels, offsets, ref_logp=None, *, kind: str = "
         logits.data_ptr(), code, rows, n, stride, labels.data_ptr(), offsets.data_ptr(), pairs,
         _ptr(ref_logp), how, beta, label_smoothing, bool(average), grad_scale, loss.data_ptr(),
         margins.data_ptr(), seq_logp.data_ptr(), logp.data_ptr(), rest, rest + 8 * rows, _ptr(out),
-        out_stride, ws, ws_bytes, rest + 12 * rows, pair_status.data_ptr(),
+        out_stride, ws, ws_bytes, rest + 12 * rows, pair_status,
         _raw_stream(dev.index)), "iso_preference_loss")
     return r
 

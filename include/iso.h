@@ -339,7 +339,8 @@ typedef enum { ISO_F32 = 0, ISO_BF16 = 1, ISO_F16 = 2 } iso_dtype;
  *
  *  logp       [rows], written: lp_r, or 0 for a row without a label.
  *  norm       [rows, 2], written.
- *  workspace  iso_token_logp_workspace_bytes(rows) bytes, 256-byte aligned.
+ *  workspace  iso_token_logp_workspace_bytes(rows) bytes, 256-byte aligned; may be NULL when that
+ *             is 0 (few rows).
  *  row_status [rows] uint32, written, or NULL.
  */
 size_t iso_token_logp_workspace_bytes(int64_t rows);

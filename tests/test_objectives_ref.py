@@ -91,10 +91,10 @@ def test_objective_argument_checks():
     p, ws = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x100000)
     bad, no_ws = chp.ISO_ERR_INVALID_ARG, chp.ISO_ERR_WORKSPACE
 
-    need0 = lib.iso_token_logp_workspace_bytes(4)
-    assert need0 > 0 and lib.iso_token_logp_workspace_bytes(-1) == 0
+    need0 = lib.iso_token_logp_workspace_bytes(4000)
+    assert need0 > 0 and lib.iso_token_logp_workspace_bytes(-1) == 0 and lib.iso_token_logp_workspace_bytes(1) == 0
 
-    def logp(x=p, dt=0, rows=4, n=10, stride=10, labels=p, t=1.0, lp=p, norm=p, w=ws, wb=need0):
+    def logp(x=p, dt=0, rows=4000, n=10, stride=10, labels=p, t=1.0, lp=p, norm=p, w=ws, wb=need0):
         return lib.iso_token_logp(x, dt, rows, n, stride, labels, t, lp, norm, w, wb, None, None)
 
     assert logp(rows=0, x=None, labels=None, lp=None, norm=None) == chp.ISO_OK
