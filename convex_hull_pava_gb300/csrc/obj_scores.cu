@@ -97,27 +97,37 @@ struct RowOuts {
     uint32_t* status;
 };
 
-// A row as words of 16 bytes between at most 2 (N - 1) single scores (N a word), of which a CTA
-// of a cluster takes an equal share.
+// A row as words of 16 bytes between at most 2 (N - 1) single scores (N a word), shared out to a number
+// of readers (CTAs) in stretches that start where 128 bytes do; a reader's threads take its words
+// so that those of 8 neighbouring threads share 128 bytes: thread t has words t - skew, t - skew +
+// threads, ... of its stretch.  Rows that start elsewhere (an odd number of scores) would otherwise
+// have every 128 bytes asked for twice: in 32,771-score rows of bfloat16, 14.8 million sectors of 32
+// bytes for 9.0 million.
 template <class T>
 struct RowShape {
-    int head, words, tail;  // single scores before the words, words, single scores after
-    int first, count;       // this CTA's words
-    // ctas: a power of two of which `shift` is the exponent, or any number with shift < 0
-    __device__ __forceinline__ RowShape(const T* x, int n, int rank, int ctas, int shift = -1) {
+    int head, words, tail;   // single scores before the words, words, single scores after
+    int first, count, skew;  // this reader's words, and the threads before the first one's
+    // readers: a power of two of which `shift` is the exponent, or any number with shift < 0
+    __device__ __forceinline__ RowShape(const T* x, int n, int rank, int readers, int shift = -1) {
         constexpr int N = Word<T>::N;
-        const int at = (int)(reinterpret_cast<uintptr_t>(x) / sizeof(T)) & (N - 1);
-        head = min(n, (N - at) & (N - 1));
+        const uintptr_t at = reinterpret_cast<uintptr_t>(x) / sizeof(T);
+        head = min(n, (int)(-at & (N - 1)));
         words = (n - head) / N;
         tail = n - head - words * N;
-        const int share = shift < 0 ? (words + ctas - 1) / ctas : (words + ctas - 1) >> shift;
-        first = min(words, rank * share);
-        count = min(words, first + share) - first;
+        const int before = (int)((at + head) / N) & 7, total = words + before;
+        const int share = ((shift < 0 ? (total + readers - 1) / readers : (total + readers - 1) >> shift) + 7) & ~7;
+        const int from = min(total, rank * share), end = min(total, from + share);
+        first = max(from, before) - before;
+        skew = max(before - from, 0);
+        count = max(end - max(from, before), 0);
     }
+    // The words of round k that thread t of `threads` takes: its index, in range or not.
+    __device__ __forceinline__ bool has(int j) const { return (unsigned)j < (unsigned)count; }
+    __device__ __forceinline__ int rounds(int threads) const { return (count + skew + threads - 1) / threads; }
     // The thread of a team that has the label's word, or -1.
     __device__ __forceinline__ int owner(int64_t label, int team) const {
         const int64_t j = label - head - (int64_t)first * Word<T>::N;
-        return j >= 0 && j < (int64_t)count * Word<T>::N ? (int)(j / Word<T>::N) % team : -1;
+        return j >= 0 && j < (int64_t)count * Word<T>::N ? ((int)(j / Word<T>::N) + skew) % team : -1;
     }
     // The single score that lane e of the row's first warp takes, or -1.
     __device__ __forceinline__ int edge(int n, int e) const {
@@ -184,10 +194,11 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             const T* x = base + row * sc.stride;
             const RowShape<T> s(x, n, rank, ctas, shift);
             if (!LONG) {
-                const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first + tt;
+                const int j = tt - s.skew;
+                const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first + j;
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (tt + k * TEAM < s.count) copy_async(mine + k * TEAM, src + k * TEAM);
+                    if (s.has(j + k * TEAM)) copy_async(mine + k * TEAM, src + k * TEAM);
             }
             const int e = edges ? s.edge(n, tt) : -1;
             if (e >= 0) h.edge = to_f32(x[e]);
@@ -201,7 +212,8 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         T* out = static_cast<T*>(o.out) + row * o.out_stride;
         const RowShape<T> s(o.out_words ? base + row * sc.stride : out, n, rank, ctas, shift);
         uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
-        for (int j = tt; j < s.count; j += TEAM) store_streaming(dst + j, uint4{0, 0, 0, 0});
+        for (int j = tt - s.skew; j < s.count; j += TEAM)
+            if (j >= 0) store_streaming(dst + j, uint4{0, 0, 0, 0});
         const int e = edges ? s.edge(n, tt) : -1;
         if (e >= 0) out[e] = from_f32<T>(0.f);
     };
@@ -250,7 +262,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         }
         const T* x = base + r * sc.stride;
         const RowShape<T> s(x, n, rank, ctas, shift);
-        const int rounds = (s.count + TEAM - 1) / TEAM;  // the same in all threads, as is what depends on it
+        const int rounds = s.rounds(TEAM), j0 = tt - s.skew;  // rounds: the same in all threads, as is what depends on it
         T* out = static_cast<T*>(o.out) + r * o.out_stride;
         uint4 w[K];
         float top = -INFINITY;
@@ -262,7 +274,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
                 for (int k = 0; k < K; ++k)
                     if (k < rounds) {
                         w[k] = mine[k * TEAM];
-                        if (tt + k * TEAM >= s.count) w[k] = word_closed(T());
+                        if (!s.has(j0 + k * TEAM)) w[k] = word_closed(T());
                         top = fmaxf(top, word_max(w[k], T()));
                     }
             }
@@ -297,9 +309,9 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
             st.m = cur.edge;
             st.s = edges ? SoftRef(st.m, a).exp(cur.edge) : 0.f;
-            for (int j = tt; j < s.count; j += K * TEAM) {
+            for (int j = j0; j < s.count; j += K * TEAM) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) w[k] = j + k * TEAM < s.count ? src[j + k * TEAM] : word_closed(T());
+                for (int k = 0; k < K; ++k) w[k] = s.has(j + k * TEAM) ? src[j + k * TEAM] : word_closed(T());
                 add_words<T, K>(st, w, a);
             }
             st = soft_warp(st, a);
@@ -356,13 +368,13 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         const float g = q.coef * p.grad_scale * sc.inv_t;
         const RowGrad<T> grad{g, __fdividef(-g, st.s), ref};
         if (!LONG && o.out_words) {
-            uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first + tt;
+            uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first + j0;
             auto give = [&](auto far) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
                     if (k < rounds) {
                         const uint4 d = grad.template word<decltype(far)::value>(w[k]);
-                        if (tt + k * TEAM < s.count) store_streaming(dst + k * TEAM, d);
+                        if (s.has(j0 + k * TEAM)) store_streaming(dst + k * TEAM, d);
                     }
             };
             ref.far ? give(std::true_type()) : give(std::false_type());
@@ -370,7 +382,8 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             // read again: the row is long, or its gradient lies at other places within 16 bytes
             const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
             T* dst = out + s.head + (int64_t)s.first * N;
-            for (int j = tt; j < s.count; j += TEAM) {
+            for (int j = j0; j < s.count; j += TEAM) {
+                if (j < 0) continue;
                 const uint4 word = src[j];
                 store_word(dst + (int64_t)j * N, ref.far ? grad.template word<true>(word) : grad.template word<false>(word), o.out_words);
             }
@@ -454,7 +467,7 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     // what is copied next: group `at` of row `row`
     TeamRows ahead(sc, rl, team, teams);
     int64_t row = 0;
-    int at = 0, groups = 0, count = 0;
+    int at = 0, groups = 0, count = 0, skew = 0;
     const uint4* src = nullptr;
     auto copy_group = [&](int slot) {
         if (at == groups && row >= 0) {
@@ -462,17 +475,18 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
             if (row >= 0) {
                 const T* x = base + row * sc.stride;
                 const RowShape<T> s(x, n, rank, ctas, shift);
-                src = reinterpret_cast<const uint4*>(x + s.head) + s.first + tt;
+                src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
                 count = s.count;
+                skew = s.skew;
                 at = 0;
-                groups = max(1, (count + TEAM * U - 1) / (TEAM * U));
+                groups = max(1, s.rounds(TEAM * U));
             }
         }
         if (at < groups && row >= 0) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int j = (at * U + u) * TEAM;
-                if (tt + j < count) copy_async(mine + (slot * U + u) * TEAM, src + j);
+                const int j = tt - skew + (at * U + u) * TEAM;
+                if ((unsigned)j < (unsigned)count) copy_async(mine + (slot * U + u) * TEAM, src + j);
             }
             ++at;
         }
@@ -495,14 +509,14 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
             if (e >= 0) edge = to_f32(x[e]);
         }
         SoftState st = soft_empty();
-        const int end = max(1, (s.count + TEAM * U - 1) / (TEAM * U));
+        const int end = max(1, s.rounds(TEAM * U));
         for (int g = 0; g < end; ++g) {
             copy_async_wait<D - 1>();
             uint4 w[U];
             float m = -INFINITY;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                w[u] = tt + (g * U + u) * TEAM < s.count ? mine[(slot * U + u) * TEAM] : word_closed(T());
+                w[u] = s.has(tt - s.skew + (g * U + u) * TEAM) ? mine[(slot * U + u) * TEAM] : word_closed(T());
                 m = fmaxf(m, word_max(w[u], T()));  // (read, before the place is copied to again)
             }
             copy_group(slot);
@@ -579,7 +593,8 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
         if (label < 0) {
             const RowShape<T> s(o.out_words ? x : out, n, part, parts);
             uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
-            for (int j = tt; j < s.count; j += TEAM) store_streaming(dst + j, uint4{0, 0, 0, 0});
+            for (int j = tt - s.skew; j < s.count; j += TEAM)
+                if (j >= 0) store_streaming(dst + j, uint4{0, 0, 0, 0});
             const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
             if (e >= 0) out[e] = from_f32<T>(0.f);
             continue;
@@ -594,15 +609,15 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
         const float2 ms = *reinterpret_cast<const float2*>(norm + 2 * r);
         const float g = coef[r] * grad_scale * sc.inv_t;
         const RowGrad<T> grad{g, -g / ms.y, SoftRef(ms.x, a)};
-        for (int j = tt; j < s.count; j += K * TEAM) {
+        for (int j = tt - s.skew; j < s.count; j += K * TEAM) {
             uint4 w[K];
 #pragma unroll
             for (int k = 0; k < K; ++k)
-                if (j + k * TEAM < s.count) w[k] = load_streaming(src + j + k * TEAM);
+                if (s.has(j + k * TEAM)) w[k] = load_streaming(src + j + k * TEAM);
             auto give = [&](auto far) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
-                    if (j + k * TEAM < s.count)
+                    if (s.has(j + k * TEAM))
                         store_word(dst + (int64_t)(j + k * TEAM) * N, grad.template word<decltype(far)::value>(w[k]), o.out_words);
             };
             grad.ref.far ? give(std::true_type()) : give(std::false_type());
@@ -752,6 +767,19 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
 // Rows that log-probabilities alone need no list for.
 constexpr int64_t kNoList = 64;
 
+// The words that a reader's threads have to hold, of the rows of a call (see RowShape): their number,
+// with the threads before the first one's.
+template <class T>
+struct RowWords {
+    int64_t words, before;
+    explicit RowWords(const ScoreRows& s) {
+        words = (s.n + Word<T>::N - 1) / Word<T>::N;
+        const bool aligned = reinterpret_cast<uintptr_t>(s.x) % 128 == 0 && (s.rows <= 1 || s.stride * sizeof(T) % 128 == 0);
+        before = aligned ? 0 : 7;
+    }
+    int64_t share(int64_t readers) const { return ((words + before + readers - 1) / readers + 7) & ~int64_t(7); }
+};
+
 // The workspace: a head, the list of rows, what follows.
 inline size_t list_bytes(int64_t rows) { return 256 + align256o((size_t)rows * 4); }
 inline ListHead* list_head(void* ws) { return static_cast<ListHead*>(ws); }
@@ -786,16 +814,15 @@ cudaError_t launch_policy(const ScoreRows& s, PolicyArgs p, const RowOuts& o, in
 // longer rows are read twice.
 template <class T>
 cudaError_t run_policy(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, void* ws, cudaStream_t st) {
-    const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
-    if (words <= 32 * 8) return launch_policy<T, 256, 32, 8, false>(s, p, o, 1, ws, st);
-    if (words > 8 * 256 * 16) return launch_policy<T, 256, 256, 8, true>(s, p, o, 8, ws, st);
+    const RowWords<T> w(s);
+    if (w.share(1) <= 32 * 8) return launch_policy<T, 256, 32, 8, false>(s, p, o, 1, ws, st);
+    if (w.share(8) > 256 * 16) return launch_policy<T, 256, 256, 8, true>(s, p, o, 8, ws, st);
     int ctas = 1;
-    while (words > (int64_t)ctas * 256 * 16) ctas *= 2;
+    while (w.share(ctas) > 256 * 16) ctas *= 2;
     // few rows: more CTAs for each, down to a word a thread
-    while (ctas < 8 && s.rows * ctas < device_sms() && words > (int64_t)ctas * 256) ctas *= 2;
-    if (words <= ctas * 128 * 8) return launch_policy<T, 128, 128, 8, false>(s, p, o, ctas, ws, st);
-    if (words <= ctas * 256 * 8) return launch_policy<T, 256, 256, 8, false>(s, p, o, ctas, ws, st);
-    if (getenv("X512")) return launch_policy<T, 512, 512, 8, false>(s, p, o, ctas, ws, st);
+    while (ctas < 8 && s.rows * ctas < device_sms() && w.share(ctas) > 256) ctas *= 2;
+    if (w.share(ctas) <= 128 * 8) return launch_policy<T, 128, 128, 8, false>(s, p, o, ctas, ws, st);
+    if (w.share(ctas) <= 256 * 8) return launch_policy<T, 256, 256, 8, false>(s, p, o, ctas, ws, st);
     return launch_policy<T, 256, 256, 16, false>(s, p, o, ctas, ws, st);
 }
 
@@ -805,19 +832,19 @@ template <class T>
 cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, void* ws, bool zero_ticket, cudaStream_t st) {
     constexpr int NT = 256, U = 4, D = 4;
     constexpr size_t shared = (size_t)NT * U * D * 16;
-    const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
-    const bool warps = words <= 32 * 8;
+    const RowWords<T> w(s);
+    const bool warps = w.share(1) <= 32 * 8;
     const int per_cta = warps ? NT / 32 : 1;
     auto* kernel = warps ? score_stream_kernel<T, NT, 32, U, D> : score_stream_kernel<T, NT, NT, U, D>;
     static int held[2][64][4];
     int best = 1, best_fit = 1;
     double least = 0.0;
-    for (int ctas = 1; ctas <= 8 && (ctas == 1 || (!warps && words >= (int64_t)ctas * NT)); ctas *= 2) {
+    for (int ctas = 1; ctas <= 8 && (ctas == 1 || (!warps && w.words >= (int64_t)ctas * NT)); ctas *= 2) {
         ClusterLaunch l(1, NT, shared, ctas, false, st);
         int fit = 0;
         const cudaError_t e = clusters_held(kernel, l.c, ctas, held[warps], &fit);
         if (e != cudaSuccess) return e;
-        const int64_t groups = (words + (int64_t)ctas * NT * U - 1) / ((int64_t)ctas * NT * U);
+        const int64_t groups = (w.share(ctas) + NT * U - 1) / (NT * U);
         const double cost = (double)((s.rows + fit - 1) / fit) * (double)(groups + 1);
         if (ctas == 1 || cost < 0.97 * least) {
             best = ctas;
@@ -861,9 +888,10 @@ cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int NT = 256, K = 4;
-        const int64_t words = (s.n + Word<T>::N - 1) / Word<T>::N;
-        const bool warps = words <= 32 * 8;
-        const int parts = warps ? 1 : (int)((words + NT * K - 1) / (NT * K));
+        const RowWords<T> w(s);
+        const bool warps = w.share(1) <= 32 * 8;
+        int parts = 1;
+        if (!warps) parts = (int)((w.words + w.before + NT * K - 1) / (NT * K));
         const int64_t ctas = warps ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows * parts;
         ClusterLaunch l(std::min<int64_t>(ctas, 1 << 30), NT, 0, 1, true, st);
         auto* kernel = warps ? score_backward_kernel<T, NT, 32, K> : score_backward_kernel<T, NT, NT, K>;
