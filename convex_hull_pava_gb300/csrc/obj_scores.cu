@@ -107,15 +107,15 @@ template <class T>
 struct RowShape {
     int head, words, tail;   // single scores before the words, words, single scores after
     int first, count, skew;  // this reader's words, and the threads before the first one's
-    // readers: a power of two of which `shift` is the exponent, or any number with shift < 0
-    __device__ __forceinline__ RowShape(const T* x, int n, int rank, int readers, int shift = -1) {
+    // 1 << shift readers, or stretches of `fixed` words (a multiple of 8) if that is not 0.
+    __device__ __forceinline__ RowShape(const T* x, int n, int rank, int shift, int fixed = 0) {
         constexpr int N = Word<T>::N;
         const uintptr_t at = reinterpret_cast<uintptr_t>(x) / sizeof(T);
         head = min(n, (int)(-at & (N - 1)));
         words = (n - head) / N;
         tail = n - head - words * N;
         const int before = (int)((at + head) / N) & 7, total = words + before;
-        const int share = ((shift < 0 ? (total + readers - 1) / readers : (total + readers - 1) >> shift) + 7) & ~7;
+        const int share = fixed ? fixed : (((total + (1 << shift) - 1) >> shift) + 7) & ~7;
         const int from = min(total, rank * share), end = min(total, from + share);
         first = max(from, before) - before;
         skew = max(before - from, 0);
@@ -192,7 +192,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         RowAhead h{row, label < 0 ? -1 : label < n ? (int)label : n, -INFINITY};
         if (label >= 0) {
             const T* x = base + row * sc.stride;
-            const RowShape<T> s(x, n, rank, ctas, shift);
+            const RowShape<T> s(x, n, rank, shift);
             if (!LONG) {
                 const int j = tt - s.skew;
                 const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first + j;
@@ -210,7 +210,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         if (rank == 0 && tt == 0) unlabelled_row(o, row);
         if (!o.out) return;
         T* out = static_cast<T*>(o.out) + row * o.out_stride;
-        const RowShape<T> s(o.out_words ? base + row * sc.stride : out, n, rank, ctas, shift);
+        const RowShape<T> s(o.out_words ? base + row * sc.stride : out, n, rank, shift);
         uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
         for (int j = tt - s.skew; j < s.count; j += TEAM)
             if (j >= 0) store_streaming(dst + j, uint4{0, 0, 0, 0});
@@ -261,7 +261,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             weight = p.weights ? p.weights[r] : inv_count;
         }
         const T* x = base + r * sc.stride;
-        const RowShape<T> s(x, n, rank, ctas, shift);
+        const RowShape<T> s(x, n, rank, shift);
         const int rounds = s.rounds(TEAM), j0 = tt - s.skew;  // rounds: the same in all threads, as is what depends on it
         T* out = static_cast<T*>(o.out) + r * o.out_stride;
         uint4 w[K];
@@ -474,7 +474,7 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
             row = ahead.next();
             if (row >= 0) {
                 const T* x = base + row * sc.stride;
-                const RowShape<T> s(x, n, rank, ctas, shift);
+                const RowShape<T> s(x, n, rank, shift);
                 src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
                 count = s.count;
                 skew = s.skew;
@@ -499,7 +499,7 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     int slot = 0, turn = 0;
     for (int64_t r = here.next(); r >= 0; r = here.next()) {
         const T* x = base + r * sc.stride;
-        const RowShape<T> s(x, n, rank, ctas, shift);
+        const RowShape<T> s(x, n, rank, shift);
         int64_t label = 0;
         float at_label = 0.f, edge = -INFINITY;
         if (edges) {
@@ -570,10 +570,9 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
 // K words a thread of one row, from the last row to the first (the forward has read them in order,
 // so that the last ones are in L2).
 template <class T, int NT, int TEAM, int K>
-__global__ void __launch_bounds__(NT)
+__global__ void __launch_bounds__(NT, 6)
 score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float* __restrict__ coef,
-                      float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o,
-                      int parts) {
+                      float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o) {
     constexpr int N = Word<T>::N;
     wait_for_previous();
     if (grad_scale_dev) {
@@ -583,37 +582,35 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
     }
     const float a = kLog2e * sc.inv_t;
     const int n = sc.n, tt = threadIdx.x & (TEAM - 1);
-    const int64_t teams = (int64_t)gridDim.x * (NT / TEAM);
-    for (int64_t unit = (int64_t)blockIdx.x * (NT / TEAM) + threadIdx.x / TEAM; unit < sc.rows * parts; unit += teams) {
-        const int64_t r = sc.rows - 1 - unit / parts;
-        const int part = (int)(unit % parts);
+    for (int64_t i = (int64_t)blockIdx.y * (NT / TEAM) + threadIdx.x / TEAM; i < sc.rows; i += (int64_t)gridDim.y * (NT / TEAM)) {
+        const int64_t r = sc.rows - 1 - i;
         const T* x = static_cast<const T*>(sc.x) + r * sc.stride;
         T* out = static_cast<T*>(o.out) + r * o.out_stride;
         const int64_t label = sc.labels[r];
-        if (label < 0) {
-            const RowShape<T> s(o.out_words ? x : out, n, part, parts);
-            uint4* dst = reinterpret_cast<uint4*>(out + s.head) + s.first;
-            for (int j = tt - s.skew; j < s.count; j += TEAM)
-                if (j >= 0) store_streaming(dst + j, uint4{0, 0, 0, 0});
-            const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
-            if (e >= 0) out[e] = from_f32<T>(0.f);
-            continue;
-        }
-        const RowShape<T> s(x, n, part, parts);
-        const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
-        T* dst = out + s.head + (int64_t)s.first * N;
-        const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1;
-        const float edge = e >= 0 ? to_f32(x[e]) : 0.f;
-        const bool owner = s.owner(label, TEAM) == tt;
-        const float at_label = owner ? to_f32(x[label]) : 0.f;
-        const float2 ms = *reinterpret_cast<const float2*>(norm + 2 * r);
-        const float g = coef[r] * grad_scale * sc.inv_t;
-        const RowGrad<T> grad{g, -g / ms.y, SoftRef(ms.x, a)};
-        for (int j = tt - s.skew; j < s.count; j += K * TEAM) {
+        const bool live = label >= 0;
+        const float2 ms = live ? *reinterpret_cast<const float2*>(norm + 2 * r) : float2{0.f, 1.f};
+        const float g = live ? coef[r] * grad_scale * sc.inv_t : 0.f;
+        const RowGrad<T> grad{g, __fdividef(-g, ms.y), SoftRef(ms.x, a)};
+        for (int part = blockIdx.x;; part += gridDim.x) {
+            const RowShape<T> s(live || o.out_words ? x : out, n, part, 0, TEAM * K);
+            if (part > 0 && s.count == 0) break;
+            const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
+            T* dst = out + s.head + (int64_t)s.first * N;
+            const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1, j = tt - s.skew;
+            if (!live) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+                    if (s.has(j + k * TEAM)) store_streaming(dst + (int64_t)(j + k * TEAM) * N, uint4{0, 0, 0, 0});
+                if (e >= 0) out[e] = from_f32<T>(0.f);
+                continue;
+            }
             uint4 w[K];
 #pragma unroll
             for (int k = 0; k < K; ++k)
                 if (s.has(j + k * TEAM)) w[k] = load_streaming(src + j + k * TEAM);
+            const float edge = e >= 0 ? to_f32(x[e]) : 0.f;
+            const bool owner = s.owner(label, TEAM) == tt;
+            const float at_label = owner ? to_f32(x[label]) : 0.f;
             auto give = [&](auto far) {
 #pragma unroll
                 for (int k = 0; k < K; ++k)
@@ -621,9 +618,9 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
                         store_word(dst + (int64_t)(j + k * TEAM) * N, grad.template word<decltype(far)::value>(w[k]), o.out_words);
             };
             grad.ref.far ? give(std::true_type()) : give(std::false_type());
+            if (e >= 0) out[e] = grad.one(edge, e == label);
+            if (owner) out[label] = grad.one(at_label, true);
         }
-        if (e >= 0) out[e] = grad.one(edge, e == label);
-        if (owner) out[label] = grad.one(at_label, true);
     }
 }
 
@@ -890,12 +887,12 @@ cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm
         constexpr int NT = 256, K = 4;
         const RowWords<T> w(s);
         const bool warps = w.share(1) <= 32 * 8;
-        int parts = 1;
-        if (!warps) parts = (int)((w.words + w.before + NT * K - 1) / (NT * K));
-        const int64_t ctas = warps ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows * parts;
-        ClusterLaunch l(std::min<int64_t>(ctas, 1 << 30), NT, 0, 1, true, st);
+        const int64_t parts = warps ? 1 : std::min<int64_t>((w.share(1) + NT * K - 1) / (NT * K), 1 << 20);
+        const int64_t row_ctas = warps ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows;
+        ClusterLaunch l(parts, NT, 0, 1, true, st);
+        l.c.gridDim.y = (unsigned)std::min<int64_t>(row_ctas, 65535);
         auto* kernel = warps ? score_backward_kernel<T, NT, 32, K> : score_backward_kernel<T, NT, NT, K>;
-        return l(kernel, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, parts);
+        return l(kernel, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o);
     });
 }
 
