@@ -120,6 +120,18 @@ template <int G>
 __device__ __forceinline__ float group_max(float v) {
     return warp_max(v, group_lanes<G>());
 }
+struct BalanceOuts {
+    float* loss;
+    int64_t *counts, *live;
+};
+
+// The loss, from sum_e n[e] sum_t p[t, e].
+__device__ __forceinline__ void balance_result(const BalanceOuts& o, unsigned long long live, int E, int k, float sum) {
+    const float tokens = (float)live;
+    *o.live = (int64_t)live;
+    *o.loss = live > 0 ? (float)E / ((float)k * tokens) * (sum / tokens) : 0.f;
+}
+
 template <int G>
 __device__ __forceinline__ float group_add(float v) {
 #pragma unroll
@@ -160,8 +172,8 @@ __device__ __forceinline__ bool token_open(SoftState st) { return !(st.m == -INF
 // each.
 template <class T, int G, int EPL>
 __global__ void __launch_bounds__(token_threads<EPL>, token_ctas_an_sm<EPL>)
-balance_tokens_kernel(RouterArgs a, BalanceParts b, int whole, int32_t* __restrict__ chosen,
-                      float* __restrict__ gates) {
+balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
+                      int32_t* __restrict__ chosen, float* __restrict__ gates) {
     constexpr int kTokThreads = token_threads<EPL>, kTokWarps = kTokThreads / 32, TPW = 32 / G;
     static_assert(G == 32 || EPL == 1, "several tokens to a warp hold a score a lane");
     __shared__ __align__(16) float found[EPL == 1 ? 1 : kTokWarps][36];  // scores that may be among the k largest
@@ -333,17 +345,27 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, int whole, int32_t* __restri
     tokens = __reduce_add_sync(~0u, tokens);
     if (lane == 0) atomicAdd(&sh_live, tokens);
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kTokThreads) {
-        b.p[(int64_t)blockIdx.x * E + e] = sh_p[e];
-        b.n[(int64_t)blockIdx.x * E + e] = sh_n[e];
+    if (gridDim.x > 1) {
+        for (int e = threadIdx.x; e < E; e += kTokThreads) {
+            b.p[(int64_t)blockIdx.x * E + e] = sh_p[e];
+            b.n[(int64_t)blockIdx.x * E + e] = sh_n[e];
+        }
+        if (threadIdx.x == 0) b.live[blockIdx.x] = sh_live;
+        return;
     }
-    if (threadIdx.x == 0) b.live[blockIdx.x] = sh_live;
+    // one CTA has had all tokens: the loss
+    for (int e = threadIdx.x; e < E; e += kTokThreads) o.counts[e] = sh_n[e];
+    if (warp == 0) {
+        float sum = 0.f;
+        for (int e = lane; e < E; e += 32) sum = fmaf(sh_p[e], (float)sh_n[e], sum);
+        sum = warp_add(sum);
+        if (lane == 0) balance_result(o, sh_live, E, k, sum);
+    }
 }
 
 // The CTAs' sums, in a fixed order, by one cluster that shares the experts; the loss.
 __global__ void __launch_bounds__(512)
-balance_finish_kernel(BalanceParts b, int grid, int E, int top_k, float* __restrict__ loss,
-                      int64_t* __restrict__ counts, int64_t* __restrict__ live) {
+balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k) {
     __shared__ float sh_p[512];
     __shared__ uint32_t sh_n[512];
     __shared__ float sh_sum[kFinishCtas], sh_warp[16];
@@ -374,7 +396,7 @@ balance_finish_kernel(BalanceParts b, int grid, int E, int top_k, float* __restr
             s.add(sh_p[q * cols + col]);
             total += sh_n[q * cols + col];
         }
-        counts[e] = (int64_t)total;
+        o.counts[e] = (int64_t)total;
         product = s.value() * (float)total;
     }
     product = warp_add(product);
@@ -395,9 +417,7 @@ balance_finish_kernel(BalanceParts b, int grid, int E, int top_k, float* __restr
         if (lane == 0) {
             float s = 0.f;
             for (int c = 0; c < kFinishCtas; ++c) s += sh_sum[c];
-            const float tokens = (float)t;
-            *live = (int64_t)t;
-            *loss = t > 0 ? (float)E / ((float)top_k * tokens) * (s / tokens) : 0.f;
+            balance_result(o, t, E, top_k, s);
         }
     }
 }
@@ -526,6 +546,7 @@ size_t balance_workspace(int64_t tokens, int experts) {
 
 cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* counts,
                          int32_t* chosen, float* gates, int64_t* live, void* ws, cudaStream_t st) {
+    const BalanceOuts o{loss, counts, live};
     BalanceParts b;
     b.live = static_cast<uint32_t*>(ws);
     int grid = 0;
@@ -537,13 +558,13 @@ cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* c
             b.p = reinterpret_cast<float*>(static_cast<char*>(ws) + 2048);
             b.n = reinterpret_cast<uint32_t*>(b.p + (int64_t)grid * a.experts);
             const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, TokenRow<T, G, EPL>::CH, sizeof(T));
-            balance_tokens_kernel<T, G, EPL><<<grid, token_threads<EPL>, 0, st>>>(a, b, whole, chosen, gates);
+            balance_tokens_kernel<T, G, EPL><<<grid, token_threads<EPL>, 0, st>>>(a, b, o, whole, chosen, gates);
             return cudaGetLastError();
         });
     });
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || grid == 1) return e;
     ClusterLaunch l(kFinishCtas, 512, 0, kFinishCtas, true, st);
-    return l(balance_finish_kernel, b, grid, a.experts, a.top_k, loss, counts, live);
+    return l(balance_finish_kernel, b, o, grid, a.experts, a.top_k);
 }
 
 cudaError_t balance_backward(int dtype, const RouterArgs& a, const int64_t* counts,

@@ -362,11 +362,10 @@ def _router(logits, top_k, mask):
     if experts > MAX_EXPERTS or not 1 <= top_k <= min(experts, MAX_TOP_K):
         raise ValueError(f"at most {MAX_EXPERTS} experts, and 1 <= top_k <= min(experts, {MAX_TOP_K})")
     torch = _torch()
-    if mask is not None:
-        if isinstance(mask, torch.Tensor) and mask.dtype == torch.bool:
-            mask = mask.view(torch.uint8)
-        _check(mask, "mask", torch.uint8, logits.shape[:1], dev)
-    return torch, code, tokens, experts, stride, dev, mask
+    if mask is not None:   # (a bool is a byte of 0 or 1)
+        dtype = torch.bool if getattr(mask, "dtype", None) == torch.bool else torch.uint8
+        _check(mask, "mask", dtype, logits.shape[:1], dev)
+    return torch, code, tokens, experts, stride, dev
 
 
 def iso_balance_loss(logits, top_k: int, mask=None, *, renormalize: bool = False, workspace=None,
@@ -376,7 +375,7 @@ def iso_balance_loss(logits, top_k: int, mask=None, *, renormalize: bool = False
     where a token takes no part.  Returns a :class:`BalanceLoss`: ``loss`` (scalar), ``counts``
     (int64 ``[experts]``), ``experts`` (int32 ``[tokens, top_k]``, -1 where none), ``gates``
     (float32), ``live`` (int64 scalar: the tokens that take part), ``mask``, ``renormalize``."""
-    torch, code, tokens, experts, stride, dev, mask = _router(logits, top_k, mask)
+    torch, code, tokens, experts, stride, dev = _router(logits, top_k, mask)
     there = _elsewhere(torch, dev, stream)
     if there is not None:
         with there:
@@ -404,7 +403,8 @@ def iso_balance_loss_backward(logits, result, *, grad_loss: float = 1.0, grad_lo
     if not isinstance(result, BalanceLoss):
         raise ValueError("result must be iso_balance_loss's")
     shape = result.experts.shape
-    torch, code, tokens, experts, stride, dev, mask = _router(logits, shape[1], result.mask)
+    mask = result.mask
+    torch, code, tokens, experts, stride, dev = _router(logits, shape[1], mask)
     if shape[0] != tokens or result.counts.numel() != experts or result.counts.device != dev:
         raise ValueError("logits must have the shape and device that result was made for")
     if grad_gates is not None:

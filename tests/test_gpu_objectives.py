@@ -559,3 +559,17 @@ def test_gradient_over_the_scores(cuda_ok):
         y = x.clone()
         obj.iso_token_logp_backward(adv.nan_to_num(), y, ids(labels), norm, out=y)
         assert bool((y == want).all())
+
+
+def test_example_runs(cuda_ok):
+    """The example that trains on calibrated, ranked rewards."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "post_training.py")
+    spec = importlib.util.spec_from_file_location("post_training", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    history = np.array(example.main(6))
+    assert history.shape == (6, 3) and np.isfinite(history).all()
+    # balance is 1 when even; a sigmoid preference loss is positive
+    assert (history[:, 1] > 0.9).all() and (history[:, 2] > 0).all()
