@@ -30,7 +30,8 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 
 isodev::ScoreRows score_rows(const void* logits, int64_t rows, int64_t n, int64_t stride,
                              const int64_t* labels, float temperature) {
-    return {logits, rows, (int)n, stride, labels, 1.f / temperature};
+    return {logits, rows, (int)n, stride, labels, temperature, 1.f / temperature,
+            (float)(1.4426950408889634074 / temperature)};
 }
 
 }  // namespace
@@ -134,7 +135,7 @@ iso_status iso_preference_loss(const void* logits, int dtype, int64_t rows, int6
     if (!workspace_ok(workspace, workspace_bytes, isodev::preference_workspace(rows, pairs)))
         return ISO_ERR_WORKSPACE;
     isodev::PreferenceArgs p{offsets, pairs,   ref_logp, kind,        average, beta,
-                             label_smoothing, loss,    margins,  seq_logp,    pair_status, nullptr, nullptr};
+                             label_smoothing, loss,    margins,  seq_logp,    pair_status, nullptr, nullptr, nullptr};
     return from_cuda(isodev::preference_loss(
         dtype, score_rows(logits, rows, n, stride, labels, 1.f), p, logp, norm, coef, grad_scale,
         dlogits, out_stride, workspace, row_status, static_cast<cudaStream_t>(stream)));

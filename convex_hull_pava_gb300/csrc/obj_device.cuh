@@ -20,13 +20,6 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-// log2(v) by the hardware's instruction: absolute error about 2^-22 near 1, relative 2^-22 beyond 2.
-__device__ __forceinline__ float log2_of(float v) {
-    float r;
-    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 __device__ __forceinline__ float to_f32(float v) { return v; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
@@ -187,6 +180,45 @@ struct SoftRef {
         return ex2(far ? (top - m) * a : __fmul_rn(top, a) - c);
     }
 };
+
+// A log-probability as the unevaluated sum of two floats, hi the larger.  About 3e-8 off beside the
+// sum's own error, where one float32 of its size would be up to 5e-7: a policy's ratio and a
+// preference's margin are differences of such numbers.
+struct LogP {
+    float hi, lo;
+    __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+    // what value() leaves out
+    __device__ __forceinline__ float rest() const {
+        const float v = value();
+        return isfinite(v) ? (hi - v) + lo : 0.f;
+    }
+    // this minus a float, which is near it
+    __device__ __forceinline__ float minus(float v) const { return isfinite(hi) ? (hi - v) + lo : hi - v; }
+};
+
+// log p of a score x, given the sum of all against `ref`:
+//   (x - m) / T - log sum',   sum' = sum 2^(c - m a): c's rounding put right (to first order: it is
+//   under 2^-24 of c),   log sum' = k high + (k low + log f),  sum' = f 2^k,  1/2 <= f / sqrt(2) < 1,
+// with high + low = log 2 and so few bits in high that k high is exact.
+__device__ __forceinline__ LogP log_p(const SoftRef& ref, float x, float sum, float temperature, float inv_t) {
+    constexpr float kHigh = 2839.f / 4096.f, kLow = (float)(0.693147180559945309417 - 2839.0 / 4096.0);
+    // x - m = d + d_low, d / T = q + q_low
+    const float d = __fsub_rn(x, ref.m), back = __fsub_rn(d, x);
+    const float d_low = __fsub_rn(__fsub_rn(x, __fsub_rn(d, back)), __fadd_rn(ref.m, back));
+    const float q = d * inv_t, q_low = (fmaf(-q, temperature, d) + d_low) * inv_t;
+    const float total = ref.far ? sum : fmaf(sum, -kLn2 * fmaf(ref.m, ref.a, -ref.c), sum);
+    // a sum is at least about 1 and at most n; anything else (0, NaN, infinity) is for logf alone
+    const bool usual = total > 0.5f && total < 1e30f;
+    const int k = usual ? (__float_as_int(total) - 0x3f3504f3) >> 23 : 0;  // 0x3f3504f3: 1 / sqrt(2)
+    const float f = usual ? __int_as_float(__float_as_int(total) - (k << 23)) : total;
+    const float high = (float)k * kHigh, low = fmaf((float)k, kLow, logf(f));
+    // q - high exactly, as hi + err
+    const float hi = __fsub_rn(q, high), b = __fsub_rn(hi, q);
+    const float err = __fsub_rn(__fsub_rn(q, __fsub_rn(hi, b)), __fadd_rn(high, b));
+    LogP lp{hi, err + q_low - low};
+    if (!usual) lp = {q - low, 0.f};
+    return lp;
+}
 
 // A softmax's running state: the largest score m seen so far and the sum s of the exponentials
 // against it.  A state that has seen nothing, or only -inf, is (-inf, 0); a NaN or +inf among the

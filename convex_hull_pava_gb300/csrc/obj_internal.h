@@ -16,7 +16,7 @@ struct ScoreRows {
     int n;
     int64_t stride;
     const int64_t* labels;
-    float inv_t;  // 1 / temperature
+    float t, inv_t, a;  // temperature, 1 / temperature, log2(e) / temperature
 };
 
 // At the front of a call's workspace: the CTAs that have come to the end of a kernel, and the rows
@@ -47,6 +47,7 @@ struct PreferenceArgs {
     float *loss, *margins, *seq_logp;
     uint32_t* pair_status;
     unsigned* ticket;  // workspace
+    float* rest;       // [rows] workspace: what logp's rounding to float32 has left out
     float* each;       // [pairs] workspace
 };
 

@@ -47,9 +47,9 @@ struct PolicyRow {
     float coef, pg, kl, cut;
 };
 
-__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, float logp, float old,
+__device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, LogP logp, float old,
                                                 float adv, float ref, float w) {
-    const float ratio = ex2((logp - old) * kLog2e);
+    const float ratio = expf(logp.minus(old));
     const float free = -adv * ratio;
     const float held = -adv * fminf(fmaxf(ratio, p.low), p.high);
     const bool cut = held > free;
@@ -60,7 +60,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, float logp,
     q.kl = 0.f;
     if (p.ref_logp) {
         // exp(d) - 1 - d without its cancellation at small d
-        const float d = ref - logp, e = expm1f(d);
+        const float d = -logp.minus(ref), e = expm1f(d);
         q.kl = w * (e - d);
         q.coef -= p.kl_coef * w * e;
     }
@@ -91,6 +91,7 @@ __device__ __forceinline__ uint32_t norm_status(SoftState st) {
 
 struct RowOuts {
     float *logp, *norm, *coef;
+    float* rest;  // or NULL: what logp's rounding to float32 has left out
     void* out;
     int64_t out_stride;
     int out_words;  // the gradient's rows are aligned as the scores' rows: words can be stored
@@ -183,7 +184,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     const uint32_t teams = TEAM == 32 ? gridDim.x * W : gridDim.x >> shift;
     const uint32_t team = TEAM == 32 ? blockIdx.x * W + warp : blockIdx.x >> shift;
     uint4* mine = ahead_words + (TEAM == 32 ? warp * 32 * K : 0) + tt;
-    const float a = kLog2e * sc.inv_t;
+    const float a = sc.a;
     const int n = sc.n;
     const bool edges = rank == 0 && tt < 32;
     const T* const base = static_cast<const T*>(sc.x);
@@ -351,8 +352,9 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         }
 
         const SoftRef ref(st.m, a);
-        const float lp = (ref.of(at_label) - log2_of(st.s)) * kLn2;
-        const PolicyRow q = policy_row(p, lp, old, adv, base_lp, weight);
+        const LogP logp = log_p(ref, at_label, st.s, sc.t, sc.inv_t);
+        const float lp = logp.value();
+        const PolicyRow q = policy_row(p, logp, old, adv, base_lp, weight);
         if (rank == 0 && tt == 0) {
             o.logp[r] = lp;
             *reinterpret_cast<float2*>(o.norm + 2 * r) = {st.m, st.s};
@@ -456,7 +458,7 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     const int64_t teams = TEAM == 32 ? (int64_t)gridDim.x * W : gridDim.x >> shift;
     const int64_t team = TEAM == 32 ? (int64_t)blockIdx.x * W + warp : blockIdx.x >> shift;
     uint4* mine = ring + (TEAM == 32 ? warp * 32 * U * D : 0) + tt;
-    const float a = kLog2e * sc.inv_t;
+    const float a = sc.a;
     const int n = sc.n;
     const bool edges = rank == 0 && tt < 32;
     const T* const base = static_cast<const T*>(sc.x);
@@ -548,7 +550,9 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
             st = soft_warp(st, a);
         }
         if (lane == 0) {
-            o.logp[r] = SoftRef(st.m, a).of(at_label) * kLn2 - logf(st.s);
+            const LogP lp = log_p(SoftRef(st.m, a), at_label, st.s, sc.t, sc.inv_t);
+            o.logp[r] = lp.value();
+            if (o.rest) o.rest[r] = lp.rest();
             *reinterpret_cast<float2*>(o.norm + 2 * r) = {st.m, st.s};
             if (o.coef) o.coef[r] = 0.f;
             if (o.status) o.status[r] = norm_status(st) | (label >= n ? ISO_ROW_BAD_LABEL : 0u);
@@ -580,7 +584,7 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
         if (changed_only && g == 1.f) return;
         grad_scale *= g;
     }
-    const float a = kLog2e * sc.inv_t;
+    const float a = sc.a;
     const int n = sc.n, tt = threadIdx.x & (TEAM - 1);
     for (int64_t i = (int64_t)blockIdx.y * (NT / TEAM) + threadIdx.x / TEAM; i < sc.rows; i += (int64_t)gridDim.y * (NT / TEAM)) {
         const int64_t r = sc.rows - 1 - i;
@@ -700,6 +704,7 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
                     const float lp = logp[r];
                     seq.add(lp);
                     gain.add(p.ref_logp ? lp - p.ref_logp[r] : lp);
+                    gain.add(p.rest[r]);
                     count.add(1.f);
                 }
         seq = warp_sum(seq);
@@ -873,7 +878,7 @@ size_t token_logp_workspace(int64_t rows) { return rows <= kNoList ? 0 : list_by
 
 cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, void* ws,
                        uint32_t* row_status, cudaStream_t st) {
-    const RowOuts o{logp, norm, nullptr, nullptr, 0, 0, row_status};
+    const RowOuts o{logp, norm, nullptr, nullptr, nullptr, 0, 0, row_status};
     return by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, ws, false, st); });
 }
 
@@ -881,7 +886,7 @@ cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm
                                 float grad_scale, const float* grad_scale_dev, int changed_only,
                                 void* out, int64_t out_stride, cudaStream_t st) {
     if (s.rows == 0) return cudaSuccess;
-    const RowOuts o{nullptr, nullptr, nullptr, out, out_stride, words_agree(s, out, out_stride, dtype), nullptr};
+    const RowOuts o{nullptr, nullptr, nullptr, nullptr, out, out_stride, words_agree(s, out, out_stride, dtype), nullptr};
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int NT = 256, K = 4;
@@ -906,20 +911,23 @@ cudaError_t policy_loss(int dtype, const ScoreRows& s, const PolicyArgs& p, void
         zero_kernel<<<1, 32, 0, st>>>(p.loss, 1, p.stats, 3);
         return cudaGetLastError();
     }
-    const RowOuts o{p.logp, p.norm, p.coef, out, out_stride, out ? words_agree(s, out, out_stride, dtype) : 0, row_status};
+    const RowOuts o{p.logp, p.norm, p.coef, nullptr, out, out_stride, out ? words_agree(s, out, out_stride, dtype) : 0, row_status};
     return by_type(dtype, [&](auto t) { return run_policy<decltype(t)>(s, p, o, ws, st); });
 }
 
-size_t preference_workspace(int64_t rows, int64_t pairs) { return list_bytes(rows) + align256o((size_t)pairs * 4); }
+size_t preference_workspace(int64_t rows, int64_t pairs) {
+    return list_bytes(rows) + align256o((size_t)rows * 4) + align256o((size_t)pairs * 4);
+}
 
 cudaError_t preference_loss(int dtype, const ScoreRows& s, PreferenceArgs p, float* logp,
                             float* norm, float* coef, float grad_scale, void* out,
                             int64_t out_stride, void* ws, uint32_t* row_status, cudaStream_t st) {
     p.ticket = &list_head(ws)->ticket;
-    p.each = reinterpret_cast<float*>(after_list(ws, s.rows));
+    p.rest = reinterpret_cast<float*>(after_list(ws, s.rows));
+    p.each = p.rest + align256o((size_t)s.rows * 4) / 4;
     cudaError_t e = cudaSuccess;
     if (s.rows > 0) {
-        const RowOuts o{logp, norm, coef, nullptr, 0, 0, row_status};
+        const RowOuts o{logp, norm, coef, p.rest, nullptr, 0, 0, row_status};
         e = by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, ws, true, st); });
     } else {  // pairs of empty sequences: the ticket's zero
         zero_kernel<<<1, 32, 0, st>>>(reinterpret_cast<float*>(p.ticket), 1, nullptr, 0);
