@@ -197,7 +197,7 @@ iso_status backward_impl(const IO* grad, const uint8_t* blocks, const IO* w, con
 
 extern "C" {
 
-int iso_version(void) { return 100; }
+int iso_version(void) { return 200; }
 
 const char* iso_status_string(int status) {
     switch (status) {

@@ -1,6 +1,8 @@
 // C ABI of the training objectives (declared in include/iso.h): argument checks.
 #include "obj_internal.h"
 
+#include "iso_internal.h"
+
 #include <cmath>
 
 namespace {
@@ -51,6 +53,7 @@ iso_status iso_token_logp(const void* logits, int dtype, int64_t rows, int64_t n
     if (!logits || !labels || !logp || !norm) return ISO_ERR_INVALID_ARG;
     if (!workspace_ok(workspace, workspace_bytes, isodev::token_logp_workspace(rows)))
         return ISO_ERR_WORKSPACE;
+    isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::token_logp(dtype, score_rows(logits, rows, n, stride, labels, temperature),
                                         logp, norm, workspace, row_status,
                                         static_cast<cudaStream_t>(stream)));
@@ -66,6 +69,7 @@ iso_status iso_token_logp_backward(const void* logits, int dtype, int64_t rows, 
         return ISO_ERR_INVALID_ARG;
     if (rows == 0) return ISO_OK;
     if (!logits || !labels || !norm || !grad_logp || !dlogits) return ISO_ERR_INVALID_ARG;
+    isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::token_logp_backward(
         dtype, score_rows(logits, rows, n, stride, labels, temperature), norm, grad_logp,
         grad_scale, grad_scale_dev, changed_only, dlogits, out_stride,
@@ -105,6 +109,7 @@ iso_status iso_policy_loss(const void* logits, int dtype, int64_t rows, int64_t 
     p.coef = coef;
     p.loss = loss;
     p.stats = stats;
+    isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::policy_loss(
         dtype, score_rows(logits, rows, n, stride, labels, temperature), p, dlogits, out_stride, workspace, row_status, static_cast<cudaStream_t>(stream)));
 }
@@ -135,7 +140,8 @@ iso_status iso_preference_loss(const void* logits, int dtype, int64_t rows, int6
     if (!workspace_ok(workspace, workspace_bytes, isodev::preference_workspace(rows, pairs)))
         return ISO_ERR_WORKSPACE;
     isodev::PreferenceArgs p{offsets, pairs,   ref_logp, kind,        average, beta,
-                             label_smoothing, loss,    margins,  seq_logp,    pair_status, nullptr, nullptr, nullptr};
+                             label_smoothing, loss,    margins,  seq_logp,    pair_status, 0, nullptr, nullptr, nullptr};
+    isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::preference_loss(
         dtype, score_rows(logits, rows, n, stride, labels, 1.f), p, logp, norm, coef, grad_scale,
         dlogits, out_stride, workspace, row_status, static_cast<cudaStream_t>(stream)));
@@ -164,6 +170,7 @@ iso_status iso_balance_loss(const void* logits, int dtype, int64_t tokens, int64
     if (!workspace_ok(workspace, workspace_bytes, isodev::balance_workspace(tokens, (int)experts)))
         return ISO_ERR_WORKSPACE;
     const isodev::RouterArgs a{logits, tokens, (int)experts, stride, mask, top_k, renormalize};
+    isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::balance_loss(dtype, a, loss, counts, chosen, gates, live, workspace,
                                           static_cast<cudaStream_t>(stream)));
 }
@@ -181,6 +188,7 @@ iso_status iso_balance_loss_backward(const void* logits, int dtype, int64_t toke
     if (tokens == 0) return ISO_OK;
     if (!logits || !counts || !chosen || !gates || !live || !dlogits) return ISO_ERR_INVALID_ARG;
     const isodev::RouterArgs a{logits, tokens, (int)experts, stride, mask, top_k, renormalize};
+    isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::balance_backward(dtype, a, counts, chosen, gates, live, grad_gates,
                                               grad_loss, grad_loss_dev, dlogits, out_stride,
                                               static_cast<cudaStream_t>(stream)));

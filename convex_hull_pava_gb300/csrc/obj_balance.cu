@@ -559,12 +559,16 @@ cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* c
             b.n = reinterpret_cast<uint32_t*>(b.p + (int64_t)grid * a.experts);
             const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, TokenRow<T, G, EPL>::CH, sizeof(T));
             balance_tokens_kernel<T, G, EPL><<<grid, token_threads<EPL>, 0, st>>>(a, b, o, whole, chosen, gates);
-            return cudaGetLastError();
+            const cudaError_t e = cudaGetLastError();
+            prof_mark(st, "balance_tokens");
+            return e;
         });
     });
     if (e != cudaSuccess || grid == 1) return e;
     ClusterLaunch l(kFinishCtas, 512, 0, kFinishCtas, true, st);
-    return l(balance_finish_kernel, b, o, grid, a.experts, a.top_k);
+    e = l(balance_finish_kernel, b, o, grid, a.experts, a.top_k);
+    prof_mark(st, "balance_finish");
+    return e;
 }
 
 cudaError_t balance_backward(int dtype, const RouterArgs& a, const int64_t* counts,
@@ -579,8 +583,10 @@ cudaError_t balance_backward(int dtype, const RouterArgs& a, const int64_t* coun
             const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, CH, sizeof(T)) &&
                               chunks_fit(out, a.tokens, out_stride, a.experts, CH, sizeof(T));
             ClusterLaunch l(token_grid<G, EPL>(a.tokens), token_threads<EPL>, 0, 1, true, st);
-            return l(balance_backward_kernel<T, G, EPL>, a, whole, counts, chosen, gates, live, grad_gates,
-                     grad_loss, grad_loss_dev, static_cast<T*>(out), out_stride);
+            const cudaError_t e = l(balance_backward_kernel<T, G, EPL>, a, whole, counts, chosen, gates, live,
+                                    grad_gates, grad_loss, grad_loss_dev, static_cast<T*>(out), out_stride);
+            prof_mark(st, "balance_backward");
+            return e;
         });
     });
 }

@@ -46,6 +46,7 @@ struct PreferenceArgs {
     float beta, smooth;
     float *loss, *margins, *seq_logp;
     uint32_t* pair_status;
+    int sum_later;     // the gradient's kernel adds up the loss
     unsigned* ticket;  // workspace
     float* rest;       // [rows] workspace: what logp's rounding to float32 has left out
     float* each;       // [pairs] workspace

@@ -89,6 +89,13 @@ __device__ __forceinline__ uint32_t norm_status(SoftState st) {
     return isfinite(st.m) && isfinite(st.s) ? 0u : ISO_ROW_BAD_Y;
 }
 
+// A preference loss that the backward adds up (loss NULL: none).
+struct PairSum {
+    const float* each;
+    int64_t pairs;
+    float* loss;
+};
+
 struct RowOuts {
     float *logp, *norm, *coef;
     float* rest;  // or NULL: what logp's rounding to float32 has left out
@@ -570,62 +577,73 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     if (ctas > 1) cluster_sync();  // the first CTA's shared memory outlives the others' writes
 }
 
+// The pairs' mean loss, by a warp, in a fixed order.
+__device__ __forceinline__ void sum_pairs(const float* each, int64_t pairs, float* loss) {
+    const int lane = threadIdx.x & 31;
+    Sum v;
+    for (int64_t q = lane; q < pairs; q += 32) v.add(__ldcg(each + q));
+    v = warp_sum(v);
+    if (lane == 0) *loss = v.value() / (float)pairs;
+}
+
 // out = g (onehot - p) with g from the rows' coefficients: a CTA (or, of a short row, a warp) takes
 // K words a thread of one row, from the last row to the first (the forward has read them in order,
 // so that the last ones are in L2).
-template <class T, int NT, int TEAM, int K>
-__global__ void __launch_bounds__(NT, 6)
+template <class T, int NT, int TEAM, int K, bool PAIRS>
+__global__ void __launch_bounds__(NT, K == 4 ? 6 : 3)
 score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float* __restrict__ coef,
-                      float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o) {
+                      float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o,
+                      PairSum pairs) {
     constexpr int N = Word<T>::N;
     wait_for_previous();
+    if (PAIRS && blockIdx.x == gridDim.x - 1) {  // a column of CTAs of its own
+        if ((blockIdx.y | blockIdx.z) == 0 && threadIdx.x < 32) sum_pairs(pairs.each, pairs.pairs, pairs.loss);
+        return;
+    }
     if (grad_scale_dev) {
         const float g = *grad_scale_dev;
         if (changed_only && g == 1.f) return;
         grad_scale *= g;
     }
-    const float a = sc.a;
-    const int n = sc.n, tt = threadIdx.x & (TEAM - 1);
-    for (int64_t i = (int64_t)blockIdx.y * (NT / TEAM) + threadIdx.x / TEAM; i < sc.rows; i += (int64_t)gridDim.y * (NT / TEAM)) {
-        const int64_t r = sc.rows - 1 - i;
-        const T* x = static_cast<const T*>(sc.x) + r * sc.stride;
-        T* out = static_cast<T*>(o.out) + r * o.out_stride;
-        const int64_t label = sc.labels[r];
-        const bool live = label >= 0;
-        const float2 ms = live ? *reinterpret_cast<const float2*>(norm + 2 * r) : float2{0.f, 1.f};
-        const float g = live ? coef[r] * grad_scale * sc.inv_t : 0.f;
-        const RowGrad<T> grad{g, __fdividef(-g, ms.y), SoftRef(ms.x, a)};
-        for (int part = blockIdx.x;; part += gridDim.x) {
-            const RowShape<T> s(live || o.out_words ? x : out, n, part, 0, TEAM * K);
-            if (part > 0 && s.count == 0) break;
-            const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
-            T* dst = out + s.head + (int64_t)s.first * N;
-            const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1, j = tt - s.skew;
-            if (!live) {
+    const int n = sc.n, part = blockIdx.x, tt = threadIdx.x & (TEAM - 1);
+    const int64_t r = sc.rows - 1 - ((blockIdx.z * (int64_t)gridDim.y + blockIdx.y) * (NT / TEAM) + threadIdx.x / TEAM);
+    if (r < 0) return;
+    const T* x = static_cast<const T*>(sc.x) + r * sc.stride;
+    T* out = static_cast<T*>(o.out) + r * o.out_stride;
+    const int64_t label = sc.labels[r];
+    if (label < 0) {
+        const RowShape<T> s(o.out_words ? x : out, n, part, 0, TEAM * K);
+        T* dst = out + s.head + (int64_t)s.first * N;
+        const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1, j = tt - s.skew;
 #pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (s.has(j + k * TEAM)) store_streaming(dst + (int64_t)(j + k * TEAM) * N, uint4{0, 0, 0, 0});
-                if (e >= 0) out[e] = from_f32<T>(0.f);
-                continue;
-            }
-            uint4 w[K];
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-                if (s.has(j + k * TEAM)) w[k] = load_streaming(src + j + k * TEAM);
-            const float edge = e >= 0 ? to_f32(x[e]) : 0.f;
-            const bool owner = s.owner(label, TEAM) == tt;
-            const float at_label = owner ? to_f32(x[label]) : 0.f;
-            auto give = [&](auto far) {
-#pragma unroll
-                for (int k = 0; k < K; ++k)
-                    if (s.has(j + k * TEAM))
-                        store_word(dst + (int64_t)(j + k * TEAM) * N, grad.template word<decltype(far)::value>(w[k]), o.out_words);
-            };
-            grad.ref.far ? give(std::true_type()) : give(std::false_type());
-            if (e >= 0) out[e] = grad.one(edge, e == label);
-            if (owner) out[label] = grad.one(at_label, true);
-        }
+        for (int k = 0; k < K; ++k)
+            if (s.has(j + k * TEAM)) store_streaming(dst + (int64_t)(j + k * TEAM) * N, uint4{0, 0, 0, 0});
+        if (e >= 0) out[e] = from_f32<T>(0.f);
+        return;
     }
+    const RowShape<T> s(x, n, part, 0, TEAM * K);
+    const uint4* src = reinterpret_cast<const uint4*>(x + s.head) + s.first;
+    T* dst = out + s.head + (int64_t)s.first * N;
+    const int e = part == 0 && tt < 32 ? s.edge(n, tt) : -1, j = tt - s.skew;
+    uint4 w[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (s.has(j + k * TEAM)) w[k] = load_streaming(src + j + k * TEAM);
+    const float edge = e >= 0 ? to_f32(x[e]) : 0.f;
+    const bool owner = s.owner(label, TEAM) == tt;
+    const float at_label = owner ? to_f32(x[label]) : 0.f;
+    const float2 ms = *reinterpret_cast<const float2*>(norm + 2 * r);
+    const float g = coef[r] * grad_scale * sc.inv_t;
+    const RowGrad<T> grad{g, __fdividef(-g, ms.y), SoftRef(ms.x, sc.a)};
+    auto give = [&](auto far) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (s.has(j + k * TEAM))
+                store_word(dst + (int64_t)(j + k * TEAM) * N, grad.template word<decltype(far)::value>(w[k]), o.out_words);
+    };
+    grad.ref.far ? give(std::true_type()) : give(std::false_type());
+    if (e >= 0) out[e] = grad.one(edge, e == label);
+    if (owner) out[label] = grad.one(at_label, true);
 }
 
 // The list of rows (see RowList), its counts, and a zeroed ticket; with list == NULL the counts
@@ -639,7 +657,12 @@ row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, ListHead* __re
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t share = (rows + ctas - 1) / ctas, first = min(rows, rank * share), end = min(rows, first + share);
     int c = 0;
-    for (int64_t r = first + threadIdx.x; r < end; r += 1024) c += labels[r] >= 0 ? 1 : 0;
+    bool mine_has = false;  // of the stretch's first 1,024 rows
+    for (int64_t r = first + threadIdx.x; r < end; r += 1024) {
+        const bool has = labels[r] >= 0;
+        if (r == first + threadIdx.x) mine_has = has;
+        c += has ? 1 : 0;
+    }
     c = __reduce_add_sync(~0u, c);
     if (lane == 0) of_warp[0][warp] = c;
     __syncthreads();
@@ -661,7 +684,7 @@ row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, ListHead* __re
     int turn = 1;
     for (int64_t from = first; from < end; from += 1024, turn ^= 1) {
         const int64_t r = from + threadIdx.x;
-        const bool has = r < end && labels[r] >= 0;
+        const bool has = from == first ? mine_has : r < end && labels[r] >= 0;
         const unsigned all = __ballot_sync(~0u, has);
         if (lane == 0) of_warp[turn][warp] = __popc(all);
         __syncthreads();  // (of_warp's other half is written after the next one)
@@ -680,7 +703,7 @@ __global__ void zero_kernel(float* a, int na, float* b, int nb) {
 }
 
 // One CTA per pair, half of it for each of the two sequences: their sums, the pair's loss and the
-// coefficient of every labelled token.  The last CTA adds up the loss.
+// coefficient of every labelled token.
 __global__ void __launch_bounds__(512)
 preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
                         const float* logp, float* coef) {
@@ -716,19 +739,26 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
             sh[2][warp] = count;
         }
         __syncthreads();
-        if (threadIdx.x == 0) {
-            float total[3][2], share[2];
-            for (int v = 0; v < 3; ++v)
-                for (int i = 0; i < 2; ++i) {
-                    Sum s;
-                    for (int w = 0; w < W / 2; ++w) s.add(sh[v][i * (W / 2) + w]);
-                    total[v][i] = s.value();
+        if (warp == 0) {
+            // lanes 0 and 8 end up with the two sequences' sums
+            float total[3];
+            for (int v = 0; v < 3; ++v) {
+                Sum s = sh[v][lane & (W - 1)];
+#pragma unroll
+                for (int o = W / 4; o > 0; o >>= 1) {
+                    Sum other;
+                    other.hi = __shfl_down_sync(~0u, s.hi, o);
+                    other.lo = __shfl_down_sync(~0u, s.lo, o);
+                    s.add(other);
                 }
-            for (int i = 0; i < 2; ++i) {
-                share[i] = p.average ? 1.f / fmaxf(total[2][i], 1.f) : 1.f;
-                p.seq_logp[2 * q + i] = bad ? NAN : total[0][i] * share[i];
+                total[v] = s.value();
             }
-            const float h = total[1][0] * share[0] - total[1][1] * share[1], beta = p.beta, z = beta * h;
+            const float own_share = p.average ? 1.f / fmaxf(total[2], 1.f) : 1.f;
+            if (lane == 0 || lane == W / 2) p.seq_logp[2 * q + (lane != 0)] = bad ? NAN : total[0] * own_share;
+            const float gained = total[1] * own_share;
+            const float h = gained - __shfl_down_sync(~0u, gained, W / 2);
+            const float share[2] = {own_share, __shfl_down_sync(~0u, own_share, W / 2)};
+            const float beta = p.beta, z = beta * h;  // lane 0's are meant from here on
             float each, slope;  // the pair's loss and its derivative in h
             if (p.kind == ISO_PREFERENCE_SIGMOID) {
                 const float e = expf(-fabsf(z)), over = log1pf(e);
@@ -745,11 +775,13 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
                 slope = 2.f * d;
             }
             if (bad) each = slope = NAN;
-            p.margins[q] = bad ? NAN : z;
-            p.each[q] = each;
-            if (p.pair_status) p.pair_status[q] = bad ? ISO_ROW_BAD_SHAPE : 0u;
-            sh_coef[0] = slope * share[0] / (float)p.pairs;
-            sh_coef[1] = -slope * share[1] / (float)p.pairs;
+            if (lane == 0) {
+                p.margins[q] = bad ? NAN : z;
+                p.each[q] = each;
+                if (p.pair_status) p.pair_status[q] = bad ? ISO_ROW_BAD_SHAPE : 0u;
+                sh_coef[0] = slope * share[0] / (float)p.pairs;
+                sh_coef[1] = -slope * share[1] / (float)p.pairs;
+            }
         }
         __syncthreads();
         if (ok)
@@ -757,13 +789,9 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
                 if (labels[r] >= 0) coef[r] = sh_coef[side];
     }
     if (!waited) wait_for_previous();
-    if (!last_to_come(p.ticket, gridDim.x)) return;
-    if (warp == 0) {
-        Sum v;
-        for (int64_t q = lane; q < p.pairs; q += 32) v.add(__ldcg(p.each + q));
-        v = warp_sum(v);
-        if (lane == 0) *p.loss = v.value() / (float)p.pairs;
-    }
+    // with a gradient to follow, its kernel adds up the loss, and need not wait for that here
+    if (p.sum_later || !last_to_come(p.ticket, gridDim.x)) return;
+    if (warp == 0) sum_pairs(p.each, p.pairs, p.loss);
 }
 
 // Rows that log-probabilities alone need no list for.
@@ -791,7 +819,9 @@ inline char* after_list(void* ws, int64_t rows) { return static_cast<char*>(ws) 
 cudaError_t make_list(const ScoreRows& s, void* ws, bool list, cudaStream_t st) {
     const int ctas = s.rows > 1024 ? 8 : 1;
     ClusterLaunch l(ctas, 1024, 0, ctas, false, st);
-    return l(row_list_kernel, s.labels, s.rows, list_head(ws), list ? list_rows(ws) : nullptr);
+    const cudaError_t e = l(row_list_kernel, s.labels, s.rows, list_head(ws), list ? list_rows(ws) : nullptr);
+    prof_mark(st, "row_list");
+    return e;
 }
 
 template <class T, int NT, int TEAM, int K, bool LONG>
@@ -809,7 +839,9 @@ cudaError_t launch_policy(const ScoreRows& s, PolicyArgs p, const RowOuts& o, in
     p.head = list_head(ws);
     p.of_team = reinterpret_cast<PolicyTerms*>(after_list(ws, s.rows));
     l.c.gridDim = dim3((unsigned)(grid * ctas));
-    return l(kernel, s, p, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr});
+    e = l(kernel, s, p, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr});
+    prof_mark(st, "policy_rows");
+    return e;
 }
 
 // By a row's bytes: a warp holds up to 4 KB, a CTA 16, 32 or 64 KB and a cluster up to 8 times that;
@@ -861,8 +893,10 @@ cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, void* ws, bool zero_t
         if (e != cudaSuccess) return e;
     }
     ClusterLaunch l(grid * best, NT, shared, best, list, st);
-    return l(kernel, s, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr},
-             zero_ticket && !list ? &list_head(ws)->ticket : nullptr);
+    const cudaError_t e = l(kernel, s, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr},
+                            zero_ticket && !list ? &list_head(ws)->ticket : nullptr);
+    prof_mark(st, "score_stream");
+    return e;
 }
 
 // Whether the gradient's rows start at the same place within 16 bytes as the scores' rows.
@@ -882,23 +916,36 @@ cudaError_t token_logp(int dtype, const ScoreRows& s, float* logp, float* norm, 
     return by_type(dtype, [&](auto t) { return run_logp<decltype(t)>(s, o, ws, false, st); });
 }
 
-cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,
-                                float grad_scale, const float* grad_scale_dev, int changed_only,
-                                void* out, int64_t out_stride, cudaStream_t st) {
-    if (s.rows == 0) return cudaSuccess;
+namespace {
+cudaError_t run_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef, float grad_scale,
+                         const float* grad_scale_dev, int changed_only, void* out, int64_t out_stride,
+                         const PairSum& pairs, cudaStream_t st) {
     const RowOuts o{nullptr, nullptr, nullptr, nullptr, out, out_stride, words_agree(s, out, out_stride, dtype), nullptr};
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int NT = 256, K = 4;
         const RowWords<T> w(s);
         const bool warps = w.share(1) <= 32 * 8;
-        const int64_t parts = warps ? 1 : std::min<int64_t>((w.share(1) + NT * K - 1) / (NT * K), 1 << 20);
+        const int64_t parts = warps ? 1 : (w.share(1) + NT * K - 1) / (NT * K);  // at most 2^19
         const int64_t row_ctas = warps ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows;
-        ClusterLaunch l(parts, NT, 0, 1, true, st);
+        const bool sum = pairs.loss != nullptr;
+        ClusterLaunch l(parts + (sum ? 1 : 0), NT, 0, 1, true, st);
         l.c.gridDim.y = (unsigned)std::min<int64_t>(row_ctas, 65535);
-        auto* kernel = warps ? score_backward_kernel<T, NT, 32, K> : score_backward_kernel<T, NT, NT, K>;
-        return l(kernel, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o);
+        l.c.gridDim.z = (unsigned)((row_ctas + 65534) / 65535);
+        auto* kernel = warps ? (sum ? score_backward_kernel<T, NT, 32, 8, true> : score_backward_kernel<T, NT, 32, 8, false>)
+                             : (sum ? score_backward_kernel<T, NT, NT, K, true> : score_backward_kernel<T, NT, NT, K, false>);
+        const cudaError_t e = l(kernel, s, norm, coef, grad_scale, grad_scale_dev, changed_only, o, pairs);
+        prof_mark(st, "score_backward");
+        return e;
     });
+}
+}  // namespace
+
+cudaError_t token_logp_backward(int dtype, const ScoreRows& s, const float* norm, const float* coef,
+                                float grad_scale, const float* grad_scale_dev, int changed_only,
+                                void* out, int64_t out_stride, cudaStream_t st) {
+    if (s.rows == 0) return cudaSuccess;
+    return run_backward(dtype, s, norm, coef, grad_scale, grad_scale_dev, changed_only, out, out_stride, PairSum{}, st);
 }
 
 size_t policy_workspace(int64_t rows) {
@@ -938,11 +985,14 @@ cudaError_t preference_loss(int dtype, const ScoreRows& s, PreferenceArgs p, flo
         zero_kernel<<<1, 32, 0, st>>>(p.loss, 1, nullptr, 0);
         e = cudaGetLastError();
     } else {
+        p.sum_later = out && s.rows > 0;
         ClusterLaunch l(std::min<int64_t>(p.pairs, 1024), 512, 0, 1, true, st);
         e = l(preference_pairs_kernel, p, s.labels, s.rows, logp, coef);
+        prof_mark(st, "preference_pairs");
     }
-    if (e != cudaSuccess || !out) return e;
-    return token_logp_backward(dtype, s, norm, coef, grad_scale, nullptr, 0, out, out_stride, st);
+    if (e != cudaSuccess || !out || s.rows == 0) return e;
+    return run_backward(dtype, s, norm, coef, grad_scale, nullptr, 0, out, out_stride,
+                        PairSum{p.each, p.pairs, p.pairs > 0 ? p.loss : nullptr}, st);
 }
 
 }  // namespace isodev

@@ -482,8 +482,8 @@ iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t toke
  * Optional per-kernel timing for benchmarks (not part of the fit).
  * iso_profile_enable(1) makes the library create a few CUDA events (once, on
  * first use; the only state the library keeps) and record one before the first
- * kernel of every later iso_fit / iso_backward call and one after each of its
- * kernels, on the call's stream.  iso_profile_enable(0) stops the recording.
+ * kernel of every later call of a computing entry point and one after each of
+ * its kernels, on the call's stream.  iso_profile_enable(0) stops the recording.
  * iso_profile_read waits for the events of the most recent call and writes the
  * duration of each of its kernels in launch order (milliseconds, into ms[0..])
  * and a static name for each (names may be NULL); it returns the number of

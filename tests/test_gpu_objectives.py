@@ -573,3 +573,45 @@ def test_example_runs(cuda_ok):
     assert history.shape == (6, 3) and np.isfinite(history).all()
     # balance is 1 when even; a sigmoid preference loss is positive
     assert (history[:, 1] > 0.9).all() and (history[:, 2] > 0).all()
+
+
+def test_kernel_times_can_be_read(cuda_ok):
+    """The library's per-kernel timing covers these calls."""
+    import torch
+    import convex_hull_pava_gb300 as chp
+    from convex_hull_pava_gb300 import objectives as obj
+    x, xw, labels, rng = make(2000, 700, "f32", 2)
+    li, off = ids(labels), ids([0, 500, 1000, 1700, 2000])
+    zero = torch.zeros(2000, device="cuda")
+    chp.profile_enable(True)
+    try:
+        seen = []
+        for call in (lambda: obj.iso_policy_loss(x, li, zero, zero), lambda: obj.iso_preference_loss(x, li, off),
+                     lambda: obj.iso_balance_loss(x, 4)):
+            call()
+            times = chp.profile_read()
+            seen.append([name for name, _ in times])
+            assert all(ms >= 0 for _, ms in times)
+    finally:
+        chp.profile_enable(False)
+    assert seen[0][-1] == "policy_rows" and seen[1][-1] == "score_backward" and seen[2] == ["balance_tokens", "balance_finish"]
+
+
+def test_more_rows_than_a_grid_dimension(cuda_ok):
+    """Over 65,535 rows, of one CTA and of one warp each."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    for rows, n in ((66000, 2600), (530000, 9)):
+        x = torch.randn((rows, n), device="cuda", dtype=torch.bfloat16)
+        labels = torch.randint(-1, n, (rows,), device="cuda")
+        g = torch.randn(rows, device="cuda")
+        lp, norm, _ = obj.iso_token_logp(x, labels)
+        want = torch.log_softmax(x.double(), 1)
+        at = want.gather(1, labels.clamp(min=0)[:, None])[:, 0].where(labels >= 0, 0)
+        assert bool(((lp - at).abs() <= 4e-6 * (1 + at.abs())).all())
+        d = want.exp_().mul_(-g.double()[:, None])
+        d.scatter_add_(1, labels.clamp(min=0)[:, None], g.double()[:, None])
+        d[labels < 0] = 0
+        got = obj.iso_token_logp_backward(g, x, labels, norm).double()
+        # half a unit of bfloat16 relative, and the probabilities' error
+        assert bool(((got - d).abs() <= 2.0 ** -8 * d.abs() + 5e-6 * g.double().abs()[:, None]).all())
