@@ -178,7 +178,7 @@ __device__ __forceinline__ void unlabelled_row(const RowOuts& o, int64_t r) {
 // row's (maximum, sum); the warps of a cluster write theirs to every CTA and meet once a row.
 // LONG: rows longer than the team's registers are read twice, the second time from L2.
 template <class T, int NT, int TEAM, int K, bool LONG>
-__global__ void __launch_bounds__(NT, NT == 512 ? 2 : NT * K >= 4096 ? 2 : NT == 128 ? 6 : 3)
+__global__ void __launch_bounds__(NT, NT * K > 4096 ? 1 : NT * K == 4096 ? 2 : NT == 128 ? 6 : 3)
 policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     constexpr int N = Word<T>::N, W = NT / 32;
     extern __shared__ uint4 ahead_words[];
@@ -844,20 +844,25 @@ cudaError_t launch_policy(const ScoreRows& s, PolicyArgs p, const RowOuts& o, in
     return e;
 }
 
-// By a row's bytes: a warp holds up to 4 KB, a CTA 16, 32 or 64 KB and a cluster up to 8 times that;
-// longer rows are read twice.
+// By a row's bytes: a warp holds up to 4 KB, a CTA of 128 or 256 threads 16, 32 or 64 KB, a pair of
+// the latter 128 KB, and up to 8 CTAs of 512 threads 128 KB each; rows over 1 MB are read twice.
+// Several small CTAs an SM are better than one (8,192 x 65,536 bf16: 321 us by pairs of 256 threads,
+// 363 by one CTA of 512), but two wide ones better than four: 8,192 x 131,072 bf16 took 615 us on
+// every GPU by pairs of 512 threads, and by fours of 256 between 588 and 705, as the chip's groups
+// of SMs happened to lie.
 template <class T>
 cudaError_t run_policy(const ScoreRows& s, const PolicyArgs& p, const RowOuts& o, void* ws, cudaStream_t st) {
     const RowWords<T> w(s);
     if (w.share(1) <= 32 * 8) return launch_policy<T, 256, 32, 8, false>(s, p, o, 1, ws, st);
-    if (w.share(8) > 256 * 16) return launch_policy<T, 256, 256, 8, true>(s, p, o, 8, ws, st);
-    int ctas = 1;
-    while (w.share(ctas) > 256 * 16) ctas *= 2;
+    if (w.share(8) > 512 * 16) return launch_policy<T, 256, 256, 8, true>(s, p, o, 8, ws, st);
+    int ctas = w.share(1) <= 256 * 16 ? 1 : 2;
+    while (w.share(ctas) > (ctas == 1 ? 256 : 512) * 16) ctas *= 2;
     // few rows: more CTAs for each, down to a word a thread
     while (ctas < 8 && s.rows * ctas < device_sms() && w.share(ctas) > 256) ctas *= 2;
     if (w.share(ctas) <= 128 * 8) return launch_policy<T, 128, 128, 8, false>(s, p, o, ctas, ws, st);
     if (w.share(ctas) <= 256 * 8) return launch_policy<T, 256, 256, 8, false>(s, p, o, ctas, ws, st);
-    return launch_policy<T, 256, 256, 16, false>(s, p, o, ctas, ws, st);
+    if (w.share(ctas) <= 256 * 16) return launch_policy<T, 256, 256, 16, false>(s, p, o, ctas, ws, st);
+    return launch_policy<T, 512, 512, 16, false>(s, p, o, ctas, ws, st);
 }
 
 // Rows of up to 4 KB by warps; longer ones by as many CTAs a row (up to 8) as make the slowest
