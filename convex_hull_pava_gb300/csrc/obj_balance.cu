@@ -165,11 +165,14 @@ __device__ __forceinline__ SoftState token_softmax(const float (&v)[EPL], float 
 // Whether a token takes part, given its mask: some score is above -inf (or NaN, which shows).
 __device__ __forceinline__ bool token_open(SoftState st) { return !(st.m == -INFINITY && st.s == 0.f); }
 
-// A group of G lanes a token, several tokens to a warp where G < 32 (then EPL is 1).  The choice: with EPL = 1 each
-// lane counts the scores above its own.  Otherwise the k-th largest of the lanes' largest scores
-// bounds the k-th largest score from below; the scores that reach it (k and a few more) are
-// collected and each counts those above it.  When more than 32 reach it, k rounds of one maximum
-// each.
+// A group of G lanes a token, several tokens to a warp where G < 32 (then EPL is 1).  The choice:
+// with EPL = 1 each lane counts the scores above its own.  Otherwise the k-th largest of the lanes'
+// largest scores bounds the k-th largest score from below; the scores that reach it (k and a few
+// more) are collected and each counts those above it.  When more than 32 reach it, k rounds of one
+// maximum each.
+// Bound by instructions: 439 a token at 256 experts and k = 8 (61 us for 131,072 tokens of float32,
+// 2.2 TB/s).  k rounds of one maximum each for all took 214 us, collecting by ballots 69, two tokens
+// a warp 80.
 template <class T, int G, int EPL>
 __global__ void __launch_bounds__(token_threads<EPL>, token_ctas_an_sm<EPL>)
 balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
@@ -363,7 +366,8 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
     }
 }
 
-// The CTAs' sums, in a fixed order, by one cluster that shares the experts; the loss.
+// The CTAs' sums, in a fixed order, by one cluster that shares the experts; the loss.  Bound by latency:
+// 6 us after the choice for 304 CTAs' sums of 256 experts (one CTA alone took 50).
 __global__ void __launch_bounds__(512)
 balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k) {
     __shared__ float sh_p[512];
@@ -422,7 +426,8 @@ balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k)
     }
 }
 
-// The last tokens first: what the forward read last is still in L2.
+// The last tokens first: what the forward read last is still in L2.  The softmax is formed again (less
+// work than its bytes).  Bound by HBM: 131,072 x 256 float32 in 45 us, 268 MB, 6.0 TB/s.
 template <class T, int G, int EPL>
 __global__ void __launch_bounds__(token_threads<EPL>, token_ctas_an_sm<EPL>)
 balance_backward_kernel(RouterArgs a, int whole, const int64_t* __restrict__ counts,
