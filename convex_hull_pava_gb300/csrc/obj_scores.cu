@@ -34,12 +34,14 @@ struct PolicyTerms {
 
 namespace {
 
-// Rows with a label, counted and listed before the kernels that take them, so that teams of equal
-// numbers of rows have equal work: the labelled rows in order from the list's front, the others in
-// order from its back.  Without a list (no more rows than teams) a team takes the row of its number.
+// Which rows a team takes: first the row of its own number, whose scores it can ask for at once; then,
+// where there are more rows than teams, of the rows behind those, which another kernel lists
+// meanwhile: the labelled ones in order from the list's front, the others in order from its back, so
+// that teams have equal work.
 struct RowList {
     const ListHead* head;
-    const int32_t* list;
+    const int32_t* list;  // or NULL: no more rows than teams
+    int64_t rows;         // listed, with and without a label
 };
 
 // One row's part of the policy loss, from its log-probability.
@@ -244,28 +246,27 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     }
     bool lost = false;  // a wait for the other CTAs has run out
     let_next_start();
-    if (rl.list) wait_for_previous();
+    auto label_of = [&](int row) { return row >= 0 ? sc.labels[row] : (int64_t)-1; };
+    const int row0 = team < sc.rows ? (int)team : -1;
+    RowAhead cur = start(row0, label_of(row0)), next;
+    wait_for_previous();
     // the team's rows: the current one, the next (its words copied while the current one's turn
     // lasts), the one after (its label known), and the one after that
-    const uint32_t items = rl.list ? (uint32_t)rl.head->labelled : (uint32_t)sc.rows;
-    auto item = [&](uint32_t i) { return i >= items ? -1 : rl.list ? rl.list[i] : (int)i; };
-    auto label_of = [&](int row) { return row >= 0 ? sc.labels[row] : (int64_t)-1; };
+    const uint32_t items = rl.list ? (uint32_t)rl.head->labelled : 0u;
+    auto item = [&](uint32_t i) { return i >= items ? -1 : rl.list[i]; };
     uint32_t at = team;
-    int row1 = item(at + teams), row2 = item(at + 2 * teams), row3;
+    int row1 = item(at), row2 = item(at + teams), row3;
     int64_t label1 = label_of(row1);
-    const int row0 = item(at);
-    RowAhead cur = start(row0, label_of(row0)), next;
-    if (!rl.list) wait_for_previous();
     const float inv_count = p.weights ? 0.f : rl.head->inv_count;
     // rows without a label are spread between the labelled ones, from the last team to the first
     // (those have had fewer labelled ones)
-    uint32_t zeros = (uint32_t)sc.rows - items, zero_at = teams - 1 - team;
+    uint32_t zeros = (uint32_t)rl.rows - items, zero_at = teams - 1 - team;
     int64_t due = (int64_t)items * team / teams;
     PolicyTerms terms;
     for (int turn = 0; cur.row >= 0; row1 = row2, row2 = row3, at += teams, cur = next) {
         const int r = cur.row;
         const int64_t label2 = label_of(row2);
-        row3 = item(at + 3 * teams);
+        row3 = item(at + 2 * teams);
         float at_label = NAN, old = 0.f, adv = 0.f, base_lp = 0.f, weight = 0.f;
         if (cur.label >= 0) {
             if (lane == 0 && cur.label < n) at_label = to_f32(base[r * sc.stride + cur.label]);
@@ -299,7 +300,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
             zero_row(r);
             continue;
         }
-        for (due += zeros; due >= items && zero_at < zeros; due -= items, zero_at += teams) zero_row(rl.list[sc.rows - 1 - zero_at]);
+        for (due += zeros; items > 0 && due >= items && zero_at < zeros; due -= items, zero_at += teams) zero_row(rl.list[rl.rows - 1 - zero_at]);
 
         // the warp's sum, against the warp's maximum
         SoftState st;
@@ -409,7 +410,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
         if (s.owner(cur.label, TEAM) == tt) out[cur.label] = grad.one(at_label, true);
     }
     copy_async_wait_all();
-    for (; zero_at < zeros; zero_at += teams) zero_row(rl.list[sc.rows - 1 - zero_at]);
+    for (; zero_at < zeros; zero_at += teams) zero_row(rl.list[rl.rows - 1 - zero_at]);
 
     // the teams' sums, by the last CTA, in the teams' order
     if (rank == 0 && tt == 0) p.of_team[team] = terms;
@@ -435,22 +436,30 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     }
 }
 
-// A team's rows in turn, for a reader that has only the index: those listed, or the row of the
-// team's number if it has a label.
+// A team's labelled rows in turn (see RowList).
 struct TeamRows {
     RowList rl;
     const int64_t* labels;
-    int64_t items, teams, at, upcoming;
+    int64_t rows, teams, at, items, upcoming;
+    bool begun, listed;
     __device__ __forceinline__ TeamRows(const ScoreRows& sc, const RowList& list, int64_t team, int64_t step)
-        : rl(list), labels(sc.labels), teams(step), at(team) {
-        items = rl.list ? rl.head->labelled : sc.rows;
-        upcoming = at < items ? (rl.list ? rl.list[at] : labels[at] >= 0 ? at : -1) : -1;
-    }
+        : rl(list), labels(sc.labels), rows(sc.rows), teams(step), at(team), items(0), upcoming(-1), begun(false), listed(false) {}
     // The next row, or -1 when there are none left.
     __device__ __forceinline__ int64_t next() {
+        if (!begun) {
+            begun = true;
+            if (at < rows && labels[at] >= 0) return at;
+        }
+        if (!rl.list) return -1;
+        if (!listed) {
+            wait_for_previous();
+            listed = true;
+            items = rl.head->labelled;
+            upcoming = at < items ? rl.list[at] : -1;
+        }
         const int64_t r = upcoming;
         at += teams;
-        upcoming = rl.list && at < items ? rl.list[at] : -1;
+        upcoming = at < items ? rl.list[at] : -1;
         return r;
     }
 };
@@ -478,7 +487,6 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     const bool edges = rank == 0 && tt < 32;
     const T* const base = static_cast<const T*>(sc.x);
     let_next_start();
-    if (rl.list) wait_for_previous();
     if (zero_ticket && blockIdx.x == 0 && threadIdx.x == 0) *zero_ticket = 0u;
 
     // what is copied next: group `at` of row `row`
@@ -576,11 +584,9 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     copy_async_wait_all();
     // the rows without a label
     const int64_t thread = (int64_t)blockIdx.x * NT + threadIdx.x, threads = (int64_t)gridDim.x * NT;
-    if (rl.list) {
-        for (int64_t j = thread; j < sc.rows - rl.head->labelled; j += threads) unlabelled_row(o, rl.list[sc.rows - 1 - j]);
-    } else if (rank == 0 && tt == 0 && team < sc.rows && sc.labels[team] < 0) {
-        unlabelled_row(o, team);
-    }
+    if (rl.list)  // (which next() has waited for)
+        for (int64_t j = thread; j < rl.rows - rl.head->labelled; j += threads) unlabelled_row(o, rl.list[rl.rows - 1 - j]);
+    if (rank == 0 && tt == 0 && team < sc.rows && sc.labels[team] < 0) unlabelled_row(o, team);
     __syncwarp();
     if (ctas > 1) cluster_sync();  // the first CTA's shared memory outlives the others' writes
 }
@@ -656,17 +662,24 @@ score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float*
     if (owner) out[label] = grad.one(at_label, true);
 }
 
-// The list of rows (see RowList), its counts, and a zeroed ticket; with list == NULL the counts
-// alone.  One CTA, or one cluster of which each CTA has a stretch of the rows, so that nothing has
+// The list of the rows behind the first `skip` (see RowList), its counts, 1 / (number of all labelled
+// rows), and a zeroed ticket; with list == NULL the counts alone.  One CTA, or one cluster of which each CTA has a stretch of the rows, so that nothing has
 // to be zeroed first.  Bound by latency: 3.5 us for 8,192 rows.
 __global__ void __launch_bounds__(1024)
-row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, ListHead* __restrict__ head, int32_t* __restrict__ list) {
-    __shared__ int of_cta[8], of_warp[2][32];
+row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, int64_t skip, ListHead* __restrict__ head,
+                int32_t* __restrict__ list) {
+    __shared__ int of_cta[8], of_warp[2][32], skipped[32];
     let_next_start();
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t share = (rows + ctas - 1) / ctas, first = min(rows, rank * share), end = min(rows, first + share);
+    const int64_t behind = rows - skip, share = (behind + ctas - 1) / ctas;
+    const int64_t first = skip + min(behind, rank * share), end = min(rows, first + share);
     int c = 0;
+    if (rank == 0)
+        for (int64_t r = threadIdx.x; r < skip; r += 1024) c += labels[r] >= 0 ? 1 : 0;
+    c = __reduce_add_sync(~0u, c);
+    if (lane == 0) skipped[warp] = c;
+    c = 0;
     bool mine_has = false;  // of the stretch's first 1,024 rows
     for (int64_t r = first + threadIdx.x; r < end; r += 1024) {
         const bool has = labels[r] >= 0;
@@ -685,10 +698,13 @@ row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, ListHead* __re
         if (q < rank) run += of_cta[q];
         labelled += of_cta[q];
     }
-    if (rank == 0 && threadIdx.x == 0) {
-        head->ticket = 0u;
-        head->labelled = labelled;
-        head->inv_count = labelled > 0 ? 1.f / (float)labelled : 0.f;
+    if (rank == 0 && warp == 0) {
+        const int all = labelled + __reduce_add_sync(~0u, skipped[lane]);
+        if (lane == 0) {
+            head->ticket = 0u;
+            head->labelled = labelled;
+            head->inv_count = all > 0 ? 1.f / (float)all : 0.f;
+        }
     }
     if (!list) return;
     int turn = 1;
@@ -701,7 +717,7 @@ row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, ListHead* __re
         const int mine = of_warp[turn][lane];
         const int before = __reduce_add_sync(~0u, lane < warp ? mine : 0) + __popc(all & ((1u << lane) - 1u));
         if (has) list[run + before] = (int32_t)r;
-        else if (r < end) list[rows - 1 - (r - (run + before))] = (int32_t)r;
+        else if (r < end) list[behind - 1 - (r - skip - (run + before))] = (int32_t)r;
         run += __reduce_add_sync(~0u, mine);
     }
 }
@@ -827,10 +843,13 @@ inline ListHead* list_head(void* ws) { return static_cast<ListHead*>(ws); }
 inline int32_t* list_rows(void* ws) { return reinterpret_cast<int32_t*>(static_cast<char*>(ws) + 256); }
 inline char* after_list(void* ws, int64_t rows) { return static_cast<char*>(ws) + list_bytes(rows); }
 
-cudaError_t make_list(const ScoreRows& s, void* ws, bool list, cudaStream_t st) {
+// With `teams` fewer than the rows: the list of those behind the teams' own.
+cudaError_t make_list(const ScoreRows& s, void* ws, int64_t teams, RowList* rl, cudaStream_t st) {
+    const bool list = s.rows > teams;
+    *rl = RowList{list_head(ws), list ? list_rows(ws) : nullptr, list ? s.rows - teams : 0};
     const int ctas = s.rows > 1024 ? 8 : 1;
     ClusterLaunch l(ctas, 1024, 0, ctas, false, st);
-    const cudaError_t e = l(row_list_kernel, s.labels, s.rows, list_head(ws), list ? list_rows(ws) : nullptr);
+    const cudaError_t e = l(row_list_kernel, s.labels, s.rows, list ? teams : 0, list_head(ws), list ? list_rows(ws) : nullptr);
     prof_mark(st, "row_list");
     return e;
 }
@@ -845,12 +864,12 @@ cudaError_t launch_policy(const ScoreRows& s, PolicyArgs p, const RowOuts& o, in
     if (e != cudaSuccess) return e;
     constexpr int per_cta = TEAM == 32 ? NT / 32 : 1;
     const int64_t grid = std::min<int64_t>({(s.rows + per_cta - 1) / per_cta, fit, kMaxTeams / per_cta});
-    const bool list = s.rows > grid * per_cta;
-    if ((e = make_list(s, ws, list, st)) != cudaSuccess) return e;
+    RowList rl;
+    if ((e = make_list(s, ws, grid * per_cta, &rl, st)) != cudaSuccess) return e;
     p.head = list_head(ws);
     p.of_team = reinterpret_cast<PolicyTerms*>(after_list(ws, s.rows));
     l.c.gridDim = dim3((unsigned)(grid * ctas));
-    e = l(kernel, s, p, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr});
+    e = l(kernel, s, p, o, rl);
     prof_mark(st, "policy_rows");
     return e;
 }
@@ -904,12 +923,13 @@ cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, void* ws, bool zero_t
     }
     const int64_t grid = std::min<int64_t>((s.rows + per_cta - 1) / per_cta, std::max<int64_t>(best_fit, kNoList));
     const bool list = s.rows > grid * per_cta;  // (never for up to kNoList rows)
+    RowList rl{};
     if (list) {
-        const cudaError_t e = make_list(s, ws, true, st);
+        const cudaError_t e = make_list(s, ws, grid * per_cta, &rl, st);
         if (e != cudaSuccess) return e;
     }
     ClusterLaunch l(grid * best, NT, shared, best, list, st);
-    const cudaError_t e = l(kernel, s, o, RowList{list_head(ws), list ? list_rows(ws) : nullptr},
+    const cudaError_t e = l(kernel, s, o, rl,
                             zero_ticket && !list ? &list_head(ws)->ticket : nullptr);
     prof_mark(st, "score_stream");
     return e;
