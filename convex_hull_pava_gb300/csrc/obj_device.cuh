@@ -201,7 +201,8 @@ struct LogP {
 //   under 2^-24 of c),   log sum' = k high + (k low + log f),  sum' = f 2^k,  1/2 <= f / sqrt(2) < 1,
 // with high + low = log 2 and so few bits in high that k high is exact.  The exponentials are low by
 // 5.1e-8 of themselves in the mean (ex2 against 64 bits, 2^22 arguments in each of -2..-26's pairs of
-// octaves), and so is their sum; hundreds of tokens' log-probabilities add up in a margin.
+// octaves; not the largest score's, which is 1), and so is the rest of their sum; hundreds of tokens'
+// log-probabilities add up in a margin.
 __device__ __forceinline__ LogP log_p(const SoftRef& ref, float x, float sum, float temperature, float inv_t) {
     constexpr float kHigh = 2839.f / 4096.f, kLow = (float)(0.693147180559945309417 - 2839.0 / 4096.0);
     // x - m = d + d_low, d / T = q + q_low
@@ -213,7 +214,7 @@ __device__ __forceinline__ LogP log_p(const SoftRef& ref, float x, float sum, fl
     const bool usual = total > 0.5f && total < 1e30f;
     const int k = usual ? (__float_as_int(total) - 0x3f3504f3) >> 23 : 0;  // 0x3f3504f3: 1 / sqrt(2)
     const float f = usual ? __int_as_float(__float_as_int(total) - (k << 23)) : total;
-    const float high = (float)k * kHigh, low = fmaf((float)k, kLow, logf(f)) + 5.1e-8f;
+    const float high = (float)k * kHigh, low = fmaf((float)k, kLow, logf(f)) + 5.1e-8f * (1.f - __fdividef(1.f, total));
     // q - high exactly, as hi + err
     const float hi = __fsub_rn(q, high), b = __fsub_rn(hi, q);
     const float err = __fsub_rn(__fsub_rn(q, __fsub_rn(hi, b)), __fadd_rn(high, b));
