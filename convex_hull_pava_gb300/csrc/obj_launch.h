@@ -38,7 +38,9 @@ struct ClusterLaunch {
     ClusterLaunch(const ClusterLaunch&) = delete;
     template <class... P, class... A>
     cudaError_t operator()(void (*kernel)(P...), A... args) {
-        return cudaLaunchKernelEx(&c, kernel, P(args)...);
+        const cudaError_t e = cudaLaunchKernelEx(&c, kernel, P(args)...);
+        if (e != cudaSuccess) cudaGetLastError();  // reported here: not to a later call as well
+        return e;
     }
 };
 
@@ -65,7 +67,10 @@ cudaError_t clusters_held(F* kernel, const cudaLaunchConfig_t& config, int ctas,
             c.gridDim = dim3((unsigned)(device_sms() * ctas));
             e = cudaOccupancyMaxActiveClusters(&n, kernel, &c);
         }
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess) {
+            cudaGetLastError();
+            return e;
+        }
         known = std::max(1, n);
     }
     *fit = known;
