@@ -380,6 +380,7 @@ balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k)
     const int col = tid & (cols - 1), part = tid / cols, parts = 512 / cols;
     const int e = rank * share + col;
     const bool has = col < share && e < E;
+    cluster_started();
     wait_for_previous();
     float p = 0.f;
     uint32_t n = 0u;
@@ -406,6 +407,7 @@ balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k)
     product = warp_add(product);
     if (lane == 0) sh_warp[warp] = product;
     __syncthreads();
+    cluster_wait_started();
     if (tid == 0) {
         float s = 0.f;
         for (int w = 0; w < 16; ++w) s += sh_warp[w];

@@ -156,6 +156,11 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Another CTA's shared memory may be written to once that CTA runs: all CTAs say so as they start,
+// and wait for the others' word before they write.
+__device__ __forceinline__ void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // What scores are taken against in a softmax, a = log2(e) / temperature: exp2(x a - c), with c the
 // float32 product of the largest score m and a.  The one fused operation rounds the difference
 // only, and c's own rounding is the same in every term, in the sum and in the label's, so that it

@@ -192,6 +192,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     extern __shared__ uint4 ahead_words[];
     __shared__ SoftState part[2][TEAM == 32 ? 2 : 8 * W];
     __shared__ uint64_t come[2];
+    __shared__ bool any_lost;
     const int ctas = TEAM == 32 ? 1 : (int)cluster_size(), rank = TEAM == 32 ? 0 : (int)cluster_rank();
     const int shift = 31 - __clz(ctas);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -236,6 +237,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
 
     if (ctas > 1) {
         if (threadIdx.x == 0) {
+            any_lost = false;
             for (int i = 0; i < 2; ++i) {
                 bytes_init(&come[i]);
                 bytes_expect(&come[i], ctas * W * (int)sizeof(SoftState));
@@ -345,8 +347,10 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
                 // Not a barrier of the cluster: that would wait for the last row's gradient to be written.
                 uint64_t* bar = &come[turn & 1];
                 if (lane < ctas) send_remote(&slot[rank * W + warp], bar, lane, st);
-                if (!lost) lost = !bytes_wait(bar, turn >> 1 & 1);
-                if (threadIdx.x == 0) bytes_expect(bar, ctas * W * (int)sizeof(SoftState));  // for the row after next
+                if (!lost) {
+                    if (!bytes_wait(bar, turn >> 1 & 1)) lost = any_lost = true;
+                    else if (threadIdx.x == 0) bytes_expect(bar, ctas * W * (int)sizeof(SoftState));  // for the row after next
+                }
             }
             ++turn;
             constexpr int P = 8 * W / 32;
@@ -414,7 +418,14 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
 
     // the teams' sums, by the last CTA, in the teams' order
     if (rank == 0 && tt == 0) p.of_team[team] = terms;
-    if (!last_to_come(&p.head->ticket, gridDim.x)) return;
+    const bool last = last_to_come(&p.head->ticket, gridDim.x);
+    // This CTA's shared memory outlives what it has stopped waiting for: the others send all they have
+    // to, then end or come here (who has ended counts as here); the last of it is on its way by then.
+    if (ctas > 1 && any_lost) {
+        cluster_sync();
+        __nanosleep(100000);
+    }
+    if (!last) return;
     Sum* const total = reinterpret_cast<Sum*>(part);
     if (warp < 3) {
         Sum v;
@@ -486,6 +497,7 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     const int n = sc.n;
     const bool edges = rank == 0 && tt < 32;
     const T* const base = static_cast<const T*>(sc.x);
+    if (ctas > 1) cluster_started();
     let_next_start();
     if (zero_ticket && blockIdx.x == 0 && threadIdx.x == 0) *zero_ticket = 0u;
 
@@ -519,6 +531,8 @@ score_stream_kernel(ScoreRows sc, RowOuts o, RowList rl, unsigned* zero_ticket) 
     };
 #pragma unroll
     for (int d = 0; d < D; ++d) copy_group(d);
+    __syncwarp();
+    if (ctas > 1) cluster_wait_started();
 
     TeamRows here(sc, rl, team, teams);
     int slot = 0, turn = 0;
@@ -669,8 +683,9 @@ __global__ void __launch_bounds__(1024)
 row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, int64_t skip, ListHead* __restrict__ head,
                 int32_t* __restrict__ list) {
     __shared__ int of_cta[8], of_warp[2][32], skipped[32];
-    let_next_start();
     const int rank = (int)cluster_rank(), ctas = (int)cluster_size();
+    if (ctas > 1) cluster_started();
+    let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t behind = rows - skip, share = (behind + ctas - 1) / ctas;
     const int64_t first = skip + min(behind, rank * share), end = min(rows, first + share);
@@ -690,6 +705,7 @@ row_list_kernel(const int64_t* __restrict__ labels, int64_t rows, int64_t skip, 
     if (lane == 0) of_warp[0][warp] = c;
     __syncthreads();
     c = __reduce_add_sync(~0u, of_warp[0][lane]);
+    if (ctas > 1) cluster_wait_started();
     if (warp == 0 && lane < ctas) store_remote(&of_cta[rank], lane, c);
     __syncwarp();
     cluster_sync();
