@@ -432,11 +432,9 @@ balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k)
 // work than its bytes).  Bound by HBM: 131,072 x 256 float32 in 45 us, 268 MB, 6.0 TB/s.
 template <class T, int G, int EPL>
 __global__ void __launch_bounds__(token_threads<EPL>, token_ctas_an_sm<EPL>)
-balance_backward_kernel(RouterArgs a, int whole, const int64_t* __restrict__ counts,
-                        const int32_t* __restrict__ chosen, const float* __restrict__ gates,
-                        const int64_t* __restrict__ live, const float* __restrict__ grad_gates,
-                        float grad_loss, const float* __restrict__ grad_loss_dev,
-                        T* __restrict__ out, int64_t out_stride) {
+balance_backward_kernel(RouterArgs a, int whole, const int64_t* counts, const int32_t* chosen,
+                        const float* gates, const int64_t* live, const float* grad_gates,
+                        float grad_loss, const float* grad_loss_dev, T* out, int64_t out_stride) {
     constexpr int kTokThreads = token_threads<EPL>, kTokWarps = kTokThreads / 32;
     // the gates' part of u (or of the gradient), at the chosen experts; zero in between
     __shared__ __align__(16) float extra[kTokWarps * (32 / G)][G * EPL];

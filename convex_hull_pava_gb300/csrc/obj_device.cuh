@@ -393,7 +393,9 @@ __device__ __forceinline__ Sum warp_sum(Sum v) {
 }
 
 // The kernel that follows in the stream may be launched (it waits for this one's results where it
-// needs them), and such a wait.
+// needs them), and such a wait.  It runs while those are written: it takes them through pointers
+// that are not const __restrict__ (which would allow loads that assume that nobody writes, also in
+// front of the wait).
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

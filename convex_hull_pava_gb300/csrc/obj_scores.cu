@@ -621,9 +621,8 @@ __device__ __forceinline__ void sum_pairs(const float* each, int64_t pairs, floa
 // more, 7.2 TB/s, beside 6 us of start and end; 8 words a thread 3% slower, 2 words 9%.
 template <class T, int NT, int TEAM, int K, bool PAIRS>
 __global__ void __launch_bounds__(NT, K == 4 ? 6 : 3)
-score_backward_kernel(ScoreRows sc, const float* __restrict__ norm, const float* __restrict__ coef,
-                      float grad_scale, const float* grad_scale_dev, int changed_only, RowOuts o,
-                      PairSum pairs) {
+score_backward_kernel(ScoreRows sc, const float* norm, const float* coef, float grad_scale,
+                      const float* grad_scale_dev, int changed_only, RowOuts o, PairSum pairs) {
     constexpr int N = Word<T>::N;
     wait_for_previous();
     if (PAIRS && blockIdx.x == gridDim.x - 1) {  // a column of CTAs of its own
