@@ -743,8 +743,17 @@ __global__ void zero_kernel(float* a, int na, float* b, int nb) {
     if ((int)threadIdx.x < nb) b[threadIdx.x] = 0.f;
 }
 
+// Whether pair q's own offsets are in order and within the rows; o: its three offsets.
+__device__ __forceinline__ bool pair_in_order(const int64_t* offsets, int64_t q, int64_t rows, int64_t (&o)[3]) {
+    for (int i = 0; i < 3; ++i) o[i] = offsets[2 * q + i];
+    return o[0] >= 0 && o[1] >= o[0] && o[2] >= o[1] && o[2] <= rows;
+}
+
 // One CTA per pair, half of it for each of the two sequences: their sums, the pair's loss and the
-// coefficient of every labelled token.  Bound by latency: 3.2 us after the log-probabilities' end for
+// coefficient of every labelled token.  Each row's coefficient has one writer: a pair out of order
+// writes none, and where some pair is, one that shares rows with an earlier pair in order counts as
+// out of order too (in order throughout, pairs share none; every CTA looks through all offsets, before
+// the log-probabilities are there).  Bound by latency: 3.2 us after the log-probabilities' end for
 // 16 pairs of 300 tokens (in float64, and adding up the loss itself, it was 12.5).
 __global__ void __launch_bounds__(512)
 preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
@@ -754,12 +763,26 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
     __shared__ float sh_coef[2];
     let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, side = threadIdx.x >> 8, tt = threadIdx.x & 255;
+    bool off = false;
+    for (int64_t q = threadIdx.x; q < p.pairs; q += 512) {
+        int64_t o[3];
+        off |= !pair_in_order(p.offsets, q, rows, o);
+    }
+    const bool disorder = __syncthreads_or(off);
     bool waited = false;
     for (int64_t q = blockIdx.x; q < p.pairs; q += gridDim.x) {
-        const int64_t o0 = p.offsets[2 * q], o1 = p.offsets[2 * q + 1], o2 = p.offsets[2 * q + 2];
-        const int64_t a = side ? o1 : o0, b = side ? o2 : o1;
-        const bool ok = a >= 0 && b >= a && b <= rows;
-        const bool bad = !(o0 >= 0 && o1 >= o0 && o2 >= o1 && o2 <= rows);
+        int64_t o[3];
+        bool bad = !pair_in_order(p.offsets, q, rows, o);
+        if (disorder) {
+            bool shares = false;
+            for (int64_t e = threadIdx.x; e < q; e += 512) {
+                int64_t before[3];
+                shares |= pair_in_order(p.offsets, e, rows, before) && max(before[0], o[0]) < min(before[2], o[2]);
+            }
+            bad |= (bool)__syncthreads_or(shares);
+        }
+        const bool ok = !bad;
+        const int64_t a = side ? o[1] : o[0], b = side ? o[2] : o[1];
         if (!waited) wait_for_previous();
         waited = true;
         Sum seq, gain, count;
