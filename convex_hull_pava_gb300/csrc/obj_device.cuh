@@ -163,26 +163,34 @@ __device__ __forceinline__ void cluster_wait_started() { asm volatile("barrier.c
 
 // What scores are taken against in a softmax, a = log2(e) / temperature: exp2(x a - c), with c the
 // float32 product of the largest score m and a.  The one fused operation rounds the difference
-// only, and c's own rounding is the same in every term, in the sum and in the label's, so that it
-// cancels.  Where the product would leave float32's range or come near (a row of the type's lowest
-// value is a softmax as any other) the difference is formed first: exp2((x - m) a).  With nothing
-// but -inf seen, m counts as 0: every -inf then adds 0, and a NaN still shows.
+// only, and c's own rounding, r = m a - c, is the same in every term, in the sum and in the label's:
+// it cancels in a probability, and log_p puts it right to first order.  |r| is at most 2^-24 |c|, so
+// that this holds for |c| < 2^12 (a score of 2,839 at a temperature of 1; the second order is then
+// under 4e-9).  Beyond, "far", the difference is formed first, exp2((x - m) a): no such rest, one more
+// rounding, and no product that could leave float32's range (a row of a mask's large negative number,
+// or of the type's lowest value, is a softmax as any other).  With nothing but -inf seen, m counts as
+// 0: every -inf then adds 0, and a NaN still shows.
 struct SoftRef {
     float m, c, a;
     bool far;
+    static __device__ __forceinline__ bool is_far(float c) { return !(fabsf(c) < 4096.f); }
     __device__ __forceinline__ SoftRef(float top, float scale) {
         m = top == -INFINITY ? 0.f : top;
         a = scale;
         c = __fmul_rn(m, a);
-        far = !(fabsf(c) < 1e30f);
+        far = is_far(c);
     }
     // The exponent of a score.
     __device__ __forceinline__ float of(float x) const { return far ? (x - m) * a : fmaf(x, a, -c); }
     __device__ __forceinline__ float exp(float x) const { return ex2(of(x)); }
-    // What turns a sum that was taken against the score `top` into one against this.
+    // What turns a sum that was taken against the score `top` into one against this.  Near terms are
+    // against c, far ones against m a itself: where one is near and the other far, r counts.
     __device__ __forceinline__ float factor(float top) const {
         if (top == -INFINITY) return 0.f;
-        return ex2(far ? (top - m) * a : __fmul_rn(top, a) - c);
+        const float of_top = __fmul_rn(top, a);
+        const bool top_far = is_far(of_top);
+        if (far == top_far) return ex2(far ? (top - m) * a : of_top - c);
+        return ex2(far ? fmaf(-m, a, of_top) : fmaf(top, a, -c));
     }
 };
 

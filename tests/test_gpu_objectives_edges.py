@@ -77,3 +77,124 @@ def test_many_pairs(cuda_ok):
     off_by = 0.5 * 4 * lp_tol(lp).max() + 1e-6 * np.abs(z).max()
     assert np.abs(wide(r.margins) - z).max() <= off_by
     assert np.abs(wide(r.coef) - coef).max() <= (0.5 / 4 * off_by + 1e-6 * 0.5) / 1500
+
+
+# Sizes of scores between the ordinary ones and the type's lowest value: masks by a large negative
+# number, large positive scores, and ordinary scores at a small temperature.
+FAR = [1e4, -1e4, 1e5, -1e5, 1e7, -1e7, 3e8, -1e9, -1e10, 1e12, -1e12, -1e20, 1e29, -3e30]
+
+
+def far_rows(n, dtype, rng, sizes=FAR):
+    """Two rows for each of the sizes that the type holds: about it throughout, and about it with some
+    entries elsewhere (below a large score, above a mask).  The last entries are closed."""
+    import torch
+    most = torch.finfo(tor(dtype)).max
+    step = {"f32": 2.0 ** -23, "bf16": 2.0 ** -7, "f16": 2.0 ** -10}[dtype]
+    rows = []
+    for size in [v for v in sizes if abs(v) < most / 2]:
+        unit = 2.0 ** np.floor(np.log2(abs(size))) * step     # neighbouring numbers of the type
+        even = size + unit * np.round(3 * rng.random(n)) * (unit < 4)
+        other = even.copy()
+        other[: (n + 1) // 3] = -abs(size) * rng.uniform(0.5, 1.0, (n + 1) // 3) if size > 0 else \
+            3.0 * rng.standard_normal((n + 1) // 3)
+        for row in (even, other):
+            row = row.copy()
+            if n > 4:
+                row[-(n // 8) - 1:] = -np.inf
+            rows.append(row)
+    x = put(np.array(rows), dtype)
+    return x, wide(x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n", [1, 4, 33, 1000, 8191, 40000, 600011])
+def test_scores_of_any_size(cuda_ok, n, dtype):
+    """Log-probabilities, policy and preference losses of rows of large scores, at temperatures that
+    make them larger, and of ordinary rows at a small temperature.
+
+    The exponent of a term is (x - m) / T in base 2 whatever m is, off by 2^-22 of itself; log p is off by
+    that of the label's, within LP as elsewhere."""
+    from convex_hull_pava_gb300 import objectives as obj
+    rng = np.random.default_rng(n)
+    long_ = n > 100000   # (fewer of these)
+    x, xw = far_rows(n, dtype, rng, [1e4, -1e4, -1e9] if long_ else FAR)
+    rows = len(xw)
+    plain = put(3.0 * rng.standard_normal((rows, n)), dtype)
+    for v, w, temperatures in ((x, xw, (0.3,) if long_ else (1.0, 0.3, 50.0)), (plain, wide(plain), (1e-5,) if long_ else (1e-3, 1e-5))):
+        # a label near the top (the others have no probability in 32 bits)
+        labels = np.array([rng.choice(np.flatnonzero(r >= r.max() - 1e-6 * abs(r.max()))) for r in w])
+        li = ids(labels)
+        for t in temperatures:
+            want = ref.token_logp(w, labels, t)
+            lp, norm, st = obj.iso_token_logp(v, li, temperature=t)
+            assert not st.any() and (np.abs(wide(lp) - want) <= lp_tol(want)).all(), (t, wide(lp), want)
+            g = rng.standard_normal(rows).astype(np.float32)
+            d = obj.iso_token_logp_backward(put(g), v, li, norm, temperature=t, grad_scale=t)
+            check_grad(d, w, labels, g.astype(np.float64), np.zeros(rows), dtype, t, t)
+            old, adv, base = policy_inputs(w, labels, rng, t)
+            r = obj.iso_policy_loss(v, li, put(old), put(adv), put(base), clip_high=0.3, kl_coef=0.1, temperature=t,
+                                    grad_scale=t)
+            loss, stats, plp, coef = ref.policy(w, labels, old, adv, base, None, 0.2, 0.3, 0.1, t)
+            assert not r.row_status.any() and (np.abs(wide(r.logp) - plp) <= lp_tol(plp)).all()
+            size = np.abs(adv) * np.exp(plp - old) + 0.1 * np.exp(base - plp)
+            coef_tol = size / rows * (lp_tol(plp) + 1e-6)
+            assert (np.abs(wide(r.coef) - coef) <= coef_tol).all()
+            check_grad(r.dlogits, w, labels, coef, coef_tol, dtype, t, t)
+        # three sequences of one row each and one of all the rest
+        off = np.arange(5).tolist()
+        off[4] = rows
+        want, z, seq, lp, coef = ref.preference(w, labels, off, beta=0.1)
+        r = obj.iso_preference_loss(v, li, ids(off), beta=0.1)
+        z_tol = 0.1 * lp_tol(lp).sum() + 1e-6 * np.abs(z).max()
+        assert np.abs(wide(r.margins) - z).max() <= z_tol and abs(float(r.loss) - want) <= z_tol + 1e-6 * abs(want)
+        check_grad(r.dlogits, w, labels, coef, 0.05 / 4 * z_tol + 1e-6 * np.abs(coef), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_states_of_far_and_near_scores_meet(cuda_ok, dtype):
+    """Rows whose stretches hold scores on both sides of where exponents are formed another way (about
+    2,800 at a temperature of 1): each thread's, warp's and CTA's sums are against a score of their own."""
+    from convex_hull_pava_gb300 import objectives as obj
+    rng = np.random.default_rng(4)
+    for n in (70, 3000, 66000, 600011):
+        for sign in (1, -1):
+            row = sign * 2839.0 + rng.uniform(-6.0, 6.0, (6, n))
+            row[1, : n // 2] -= 8.0
+            row[2, n // 2:] -= 8.0
+            row[3] = np.sort(row[3])
+            row[4] = np.sort(row[4])[::-1]
+            row[5, ::7] = -5000.0
+            x = put(row, dtype)
+            w = wide(x)
+            labels = w.argmax(1)
+            lp, norm, st = obj.iso_token_logp(x, ids(labels))
+            want = ref.token_logp(w, labels)
+            assert not st.any() and (np.abs(wide(lp) - want) <= lp_tol(want)).all()
+            one = put(np.ones(6))
+            zero = put(np.zeros(6))
+            r = obj.iso_policy_loss(x, ids(labels), put(want), one, want_grad=False)
+            assert (np.abs(wide(r.logp) - want) <= lp_tol(want)).all()
+            check_grad(obj.iso_token_logp_backward(one, x, ids(labels), norm), w, labels, np.ones(6), np.zeros(6), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,k", [(4, 2), (16, 3), (32, 1), (64, 8), (256, 8), (300, 32), (1000, 4)])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_router_scores_of_any_size(cuda_ok, n, k, renormalize, dtype):
+    """A router's tokens with large scores beside ordinary ones: choice, gates, loss and gradient."""
+    from convex_hull_pava_gb300 import objectives as obj
+    rng = np.random.default_rng(n)
+    far, fw = far_rows(n, dtype, rng)
+    x = put(np.concatenate([fw, rng.standard_normal((20, n))]), dtype)
+    xw = wide(x)
+    r = obj.iso_balance_loss(x, k, renormalize=renormalize)
+    loss, counts, experts, gates, live = ref.balance(xw, k, None, renormalize)
+    assert int(r.live) == live and np.array_equal(r.counts.cpu().numpy(), counts)
+    assert np.array_equal(r.experts.cpu().numpy(), experts)
+    assert np.abs(wide(r.gates) - gates).max() <= 4e-6
+    assert abs(float(r.loss) - loss) <= 1e-5 * (1 + abs(loss))
+    gg = rng.standard_normal((len(xw), k)).astype(np.float32)
+    d = obj.iso_balance_loss_backward(x, r, grad_loss=0.5, grad_gates=put(gg))
+    want = ref.balance_grad(xw, k, None, renormalize, 0.5, gg.astype(np.float64))
+    top = np.abs(gg).max() + 0.5 * n * counts.max() / (k * live * live)
+    assert np.abs(wide(d) - want).max() <= 1e-5 * top + (HALF[dtype] * np.abs(want)).max() + TINY[dtype]
