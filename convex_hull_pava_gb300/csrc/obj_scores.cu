@@ -998,7 +998,8 @@ cudaError_t run_backward(int dtype, const ScoreRows& s, const float* norm, const
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int NT = 256, K = 4;
-        const RowWords<T> w(s);
+        RowWords<T> w(s);
+        if (!o.out_words) w.before = 7;  // zeros are shared out as the gradient's own rows lie
         const bool warps = w.share(1) <= 32 * 8;
         const int64_t parts = warps ? 1 : (w.share(1) + NT * K - 1) / (NT * K);  // at most 2^19
         const int64_t row_ctas = warps ? (s.rows + NT / 32 - 1) / (NT / 32) : s.rows;

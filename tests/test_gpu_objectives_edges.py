@@ -198,3 +198,50 @@ def test_router_scores_of_any_size(cuda_ok, n, k, renormalize, dtype):
     want = ref.balance_grad(xw, k, None, renormalize, 0.5, gg.astype(np.float64))
     top = np.abs(gg).max() + 0.5 * n * counts.max() / (k * live * live)
     assert np.abs(wide(d) - want).max() <= 1e-5 * top + (HALF[dtype] * np.abs(want)).max() + TINY[dtype]
+
+
+# (scores' width, scores a row, gradient's width, type): the scores' rows start where 128 bytes do, the
+# gradient's do not, and the row's last words are near the end of a CTA's (or a warp's) share.
+LAYOUTS = [(16384, 8191, 8191, "bf16"), (8192, 8192, 8193, "bf16"), (8192, 8185, 8191, "f16"), (131072, 131071, 131071, "bf16"),
+           (4096, 1023, 1023, "f32"), (4096, 4093, 4093, "f32"), (4096, 4096, 4097, "f32"), (2048, 2048, 2049, "bf16"),
+           (64, 17, 19, "f16"), (16384, 16381, 16387, "f16")]
+
+
+@pytest.mark.parametrize("width,n,out_width,dtype", LAYOUTS)
+def test_gradient_aligned_otherwise_than_the_scores(cuda_ok, width, n, out_width, dtype):
+    """A gradient whose rows start at other places within 16 bytes than the scores': all of every row is
+    written, zeros where the row has no label, and nothing else."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    rows = 40
+    rng = np.random.default_rng(n)
+    buf = torch.full((rows, width), float("nan"), dtype=tor(dtype), device="cuda")
+    x = buf[:, :n]
+    x.copy_(put(2.0 * rng.standard_normal((rows, n)), dtype))
+    xw = wide(x)
+    labels = rng.integers(0, n, rows)
+    labels[rng.permutation(rows)[: rows // 2]] = -100
+    li = ids(labels)
+    lp, norm, _ = obj.iso_token_logp(x, li)
+    g = rng.standard_normal(rows).astype(np.float32)
+    lp_ = ref.token_logp(xw, labels)
+    off = ids([0, 10, 20, 30, 40])
+
+    def poisoned():
+        t = torch.full((rows, out_width), float("nan"), dtype=tor(dtype), device="cuda")
+        return t, t[:, :n]
+
+    live = labels >= 0
+    shares = ref.preference(xw, labels, [0, 10, 20, 30, 40])[4]
+    ratio = np.where(live, -g / max(1, live.sum()), 0.0)   # (old is lp: a ratio of 1)
+    for call, coef, coef_tol in (
+            (lambda out: obj.iso_token_logp_backward(put(g), x, li, norm, out=out), g.astype(np.float64), np.zeros(rows)),
+            # a margin's error is beta times those of its tokens, a coefficient's beta / 4 / pairs times that
+            (lambda out: obj.iso_preference_loss(x, li, off, out=out), shares,
+             0.1 / 4 / 2 * 0.1 * lp_tol(lp_)[live].sum() + 1e-6 * np.abs(shares)),
+            (lambda out: obj.iso_policy_loss(x, li, put(lp_), put(g), out=out), ratio, np.abs(ratio) * (lp_tol(lp_) + 1e-6))):
+        whole, out = poisoned()
+        call(out)
+        assert bool((out[li < 0] == 0).all())
+        assert bool(whole[:, n:].isnan().all())
+        check_grad(out, xw, labels, coef, coef_tol, dtype)
