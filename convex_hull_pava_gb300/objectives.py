@@ -45,17 +45,21 @@ class _Result:
         return len(self._fields)
 
     # the buffer's tail, in 4-byte words: norm [rows, 2], coef [rows], row_status [rows]
+    def _tail(self, first, end):
+        at = self._buf.numel() - 4 * self._rows
+        return self._buf[at + first * self._rows:at + end * self._rows]
+
     @property
     def norm(self):
-        return self._buf[-4 * self._rows:][:2 * self._rows].view(self._rows, 2)
+        return self._tail(0, 2).view(self._rows, 2)
 
     @property
     def coef(self):
-        return self._buf[-4 * self._rows:][2 * self._rows:3 * self._rows].view(self._shape)
+        return self._tail(2, 3).view(self._shape)
 
     @property
     def row_status(self):
-        return self._buf[-4 * self._rows:][3 * self._rows:].view(_torch().int32)
+        return self._tail(3, 4).view(_torch().int32)
 
 
 class PolicyLoss(_Result):

@@ -245,3 +245,17 @@ def test_gradient_aligned_otherwise_than_the_scores(cuda_ok, width, n, out_width
         assert bool((out[li < 0] == 0).all())
         assert bool(whole[:, n:].isnan().all())
         check_grad(out, xw, labels, coef, coef_tol, dtype)
+
+
+def test_outputs_of_no_rows(cuda_ok):
+    """Of an empty batch every output is empty."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    e = torch.empty((0, 77), device="cuda")
+    z = torch.empty(0, device="cuda")
+    zi = torch.empty(0, dtype=torch.int64, device="cuda")
+    for r in (obj.iso_policy_loss(e, zi, z, z), obj.iso_preference_loss(e, zi, ids([0])),
+              obj.iso_preference_loss(e, zi, ids([0, 0, 0]))):
+        assert r.norm.shape == (0, 2) and r.coef.shape == (0,) and r.row_status.shape == (0,) and r.logp.shape == (0,)
+        assert not r.row_status.any() and len(list(r)) == len(r)
+    assert r.pair_status.tolist() == [0] and r.margins.tolist() == [0.0]
