@@ -36,7 +36,7 @@ __device__ __forceinline__ float choice_score(uint32_t key) {
 }
 
 struct BalanceParts {
-    float* p;        // [grid][experts] sums of probabilities
+    float2* p;       // [grid][experts] sums of probabilities (Sum's hi and lo)
     uint32_t* n;     // [grid][experts] tokens that chose each
     uint32_t* live;  // [grid]
 };
@@ -132,6 +132,13 @@ __device__ __forceinline__ void balance_result(const BalanceOuts& o, unsigned lo
     *o.loss = live > 0 ? (float)E / ((float)k * tokens) * (sum / tokens) : 0.f;
 }
 
+__device__ __forceinline__ Sum as_sum(float2 v) {
+    Sum s;
+    s.hi = v.x;
+    s.lo = v.y;
+    return s;
+}
+
 template <int G>
 __device__ __forceinline__ float group_add(float v) {
 #pragma unroll
@@ -166,10 +173,13 @@ __device__ __forceinline__ SoftState token_softmax(const float (&v)[EPL], float 
 __device__ __forceinline__ bool token_open(SoftState st) { return !(st.m == -INFINITY && st.s == 0.f); }
 
 // A group of G lanes a token, several tokens to a warp where G < 32 (then EPL is 1).  The choice:
-// with EPL = 1 each lane counts the scores above its own.  Otherwise the k-th largest of the lanes'
+// with EPL = 1 each lane counts the scores above its own, four to a read.  Otherwise the k-th largest of the lanes'
 // largest scores bounds the k-th largest score from below; the scores that reach it (k and a few
 // more) are collected and each counts those above it.  When more than 32 reach it, k rounds of one
 // maximum each.
+// The probabilities of an expert are added in float32 over up to 64 tokens of a lane, those sums to one
+// of the warp that keeps what it rounds off (in float32 throughout, the loss of 2^26 equal tokens was
+// 1.4e-5 off; the same times).
 // Bound by instructions: 439 a token at 256 experts and k = 8 (61 us for 131,072 tokens of float32,
 // 2.2 TB/s).  k rounds of one maximum each for all took 214 us, collecting by ballots 69, two tokens
 // a warp 80.
@@ -182,21 +192,36 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
     __shared__ __align__(16) float found[EPL == 1 ? 1 : kTokWarps][36];  // scores that may be among the k largest
     __shared__ int found_at[EPL == 1 ? 1 : kTokWarps][32];               // their experts
     __shared__ int found_n[EPL == 1 ? 1 : kTokWarps];
-    __shared__ float sh_p[G * EPL];
+    __shared__ __align__(16) uint32_t keys[EPL == 1 ? kTokWarps : 1][32];
+    extern __shared__ float2 warp_sums[];  // [kTokWarps][G * EPL], Sum's hi and lo
     __shared__ uint32_t sh_n[G * EPL];
     __shared__ uint32_t sh_live;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane & (G - 1), E = a.experts, k = a.top_k;
     const unsigned group = group_lanes<G>(), before = group & ((1u << lane) - 1u);
-    for (int e = threadIdx.x; e < G * EPL; e += kTokThreads) {
-        sh_n[e] = 0u;
-        sh_p[e] = 0.f;
-    }
+    for (int e = threadIdx.x; e < G * EPL; e += kTokThreads) sh_n[e] = 0u;
     if (threadIdx.x == 0) sh_live = 0u;
     __syncthreads();
     let_next_start();
     float psum[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) psum[i] = 0.f;
+    // takes the lanes' sums to the warp's
+    auto gather = [&](bool begun) {
+        float2* const mine = warp_sums + warp * G * EPL;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+            float p = psum[i];
+#pragma unroll
+            for (int o = 16; o >= G; o >>= 1) p += __shfl_xor_sync(~0u, p, o);
+            if (lane < G) {
+                float2& at = mine[TokenRow<T, G, EPL>::expert(gl, i)];
+                Sum s = begun ? as_sum(at) : Sum();
+                s.add(p);
+                at = {s.hi, s.lo};
+            }
+            psum[i] = 0.f;
+        }
+    };
     uint32_t tokens = 0;
     const int64_t step = (int64_t)gridDim.x * kTokWarps * TPW;
     const int64_t warp_first = ((int64_t)blockIdx.x * kTokWarps + warp) * TPW;
@@ -208,161 +233,167 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
         if (on) row.load(base + t * a.stride, gl, E, whole);
     };
     fetch(warp_first + lane / G);
-    for (int64_t first = warp_first; first < a.tokens; first += step) {
-        const int64_t t = first + lane / G;
-        float v[EPL], e[EPL];
-        row.scores(v, on);
-        const bool was_on = on;
-        fetch(t + step);
-        const SoftState st = token_softmax<G, EPL>(v, e);
-        const bool open = was_on && token_open(st);
-        const float inv = open ? __frcp_rn(st.s) : 0.f;
-        if (gl == 0 && open) ++tokens;
-        if (open) {
+    int64_t first = warp_first;
+    bool begun = false;
+    do {
+        const int64_t end = min(a.tokens, first + 64 * step);
+        for (; first < end; first += step) {
+            const int64_t t = first + lane / G;
+            float v[EPL], e[EPL];
+            row.scores(v, on);
+            const bool was_on = on;
+            fetch(t + step);
+            const SoftState st = token_softmax<G, EPL>(v, e);
+            const bool open = was_on && token_open(st);
+            const float inv = open ? __frcp_rn(st.s) : 0.f;
+            if (gl == 0 && open) ++tokens;
+            if (open) {
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) psum[i] = fmaf(e[i], inv, psum[i]);
-        }
-        int32_t* const to = chosen + t * k;
-        float* const gate_to = gates + t * k;
-        int taken = 0;  // places filled
-        if constexpr (EPL == 1) {
-            const uint32_t key = choice_key(v[0]);
-            int rank = 0;
-#pragma unroll 8
-            for (int j = 0; j < G; ++j) {
-                const uint32_t other = __shfl_sync(~0u, key, (lane & ~(G - 1)) | j);
-                rank += other > key || (other == key && j < gl) ? 1 : 0;
+                for (int i = 0; i < EPL; ++i) psum[i] = fmaf(e[i], inv, psum[i]);
             }
-            const bool mine = open && key != 0u && rank < k;
-            float gate = mine ? e[0] : 0.f;
-            gate *= a.renormalize ? 1.f / group_add<G>(gate) : inv;
-            if (mine) {
-                to[rank] = gl;
-                gate_to[rank] = gate;
-                atomicAdd(&sh_n[gl], 1u);
-            }
-            taken = __popc(__ballot_sync(~0u, mine) & group);
-        } else {
-            const SoftRef ref(st.m, kLog2e);
-            float most = v[0];
-#pragma unroll
-            for (int i = 1; i < EPL; ++i) most = fmaxf(most, v[i]);
-            float least = 0.f;
-#pragma unroll 4
-            for (int c = 0; c < k; ++c) {
-                least = group_max<G>(most);
-                if (most == least) most = -INFINITY;
-            }
-            least = !open ? INFINITY : least > -INFINITY ? least : __uint_as_float(0xff7fffffu);  // (lowest)
-            float* const list = found[warp];
-            int* const list_at = found_at[warp];
-            if (lane == 0) found_n[warp] = 0;
-            __syncwarp();
-            // in whatever order: the ranks below do not depend on it
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-                if (v[i] >= least) {
-                    const int at = atomicAdd(&found_n[warp], 1);
-                    if (at < 32) {
-                        list[at] = v[i];
-                        list_at[at] = row.expert(lane, i);
-                    }
-                }
-            __syncwarp();
-            const int n = found_n[warp];
-            if (n <= 32) {
-                if (lane < 4) list[n + lane] = -INFINITY;  // four are read at a time
+            int32_t* const to = chosen + t * k;
+            float* const gate_to = gates + t * k;
+            int taken = 0;  // places filled
+            if constexpr (EPL == 1) {
+                const uint32_t key = choice_key(v[0]);
+                keys[warp][lane] = key;
                 __syncwarp();
-                const float own = lane < n ? list[lane] : 0.f;
-                const int own_at = lane < n ? list_at[lane] : 0;
-                int rank = -1;  // the score itself is counted too
-                for (int j = 0; j < n; j += 4) {
-                    const float4 q = *reinterpret_cast<const float4*>(&list[j]);
-                    rank += (q.x >= own) + (q.y >= own) + (q.z >= own) + (q.w >= own);
-                }
-                // without equal scores the ranks are 0 .. n - 1
-                if (__reduce_add_sync(~0u, lane < n ? rank : 0) != n * (n - 1) / 2) {
-                    rank = 0;
-                    for (int j = 0; j < n; ++j) rank += list[j] > own || (list[j] == own && list_at[j] < own_at) ? 1 : 0;
-                }
-                if (lane < n && rank < k) {
-                    to[rank] = own_at;
-                    gate_to[rank] = ref.exp(own) * inv;
-                    atomicAdd(&sh_n[own_at], 1u);
-                }
-                taken = min(n, k);
-            } else {
-                unsigned gone = 0u;  // of this lane's scores
-                for (; taken < k; ++taken) {
-                    uint32_t key = 0u;
-                    int at = -1;
+                int rank = 0;
 #pragma unroll
-                    for (int i = 0; i < EPL; ++i) {
-                        const uint32_t q = choice_key(v[i]);
-                        if (!(gone >> i & 1u) && (q > key || (q == key && q != 0u && row.expert(gl, i) < row.expert(gl, at)))) {
-                            key = q;
-                            at = i;
+                for (int j = 0; j < G; j += 4) {
+                    const uint4 q = *reinterpret_cast<const uint4*>(&keys[warp][(lane & ~(G - 1)) + j]);
+                    const uint32_t other[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) rank += other[i] > key || (other[i] == key && j + i < gl) ? 1 : 0;
+                }
+                __syncwarp();
+                const bool mine = open && key != 0u && rank < k;
+                float gate = mine ? e[0] : 0.f;
+                gate *= a.renormalize ? 1.f / group_add<G>(gate) : inv;
+                if (mine) {
+                    to[rank] = gl;
+                    gate_to[rank] = gate;
+                    atomicAdd(&sh_n[gl], 1u);
+                }
+                taken = __popc(__ballot_sync(~0u, mine) & group);
+            } else {
+                const SoftRef ref(st.m, kLog2e);
+                float most = v[0];
+#pragma unroll
+                for (int i = 1; i < EPL; ++i) most = fmaxf(most, v[i]);
+                float least = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < k; ++c) {
+                    least = group_max<G>(most);
+                    if (most == least) most = -INFINITY;
+                }
+                least = !open ? INFINITY : least > -INFINITY ? least : __uint_as_float(0xff7fffffu);  // (lowest)
+                float* const list = found[warp];
+                int* const list_at = found_at[warp];
+                if (lane == 0) found_n[warp] = 0;
+                __syncwarp();
+                // in whatever order: the ranks below do not depend on it
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (v[i] >= least) {
+                        const int at = atomicAdd(&found_n[warp], 1);
+                        if (at < 32) {
+                            list[at] = v[i];
+                            list_at[at] = row.expert(lane, i);
                         }
                     }
-                    const uint32_t best = __reduce_max_sync(group, key);
-                    if (best == 0u) break;
-                    const unsigned which = key == best ? (unsigned)row.expert(gl, at) : ~0u;
-                    const unsigned winner = __reduce_min_sync(group, which);
-                    if (which == winner) {
-                        gone |= 1u << at;
-                        to[taken] = (int)winner;
-                        gate_to[taken] = ref.exp(choice_score(best)) * inv;
-                        atomicAdd(&sh_n[winner], 1u);
+                __syncwarp();
+                const int n = found_n[warp];
+                if (n <= 32) {
+                    if (lane < 4) list[n + lane] = -INFINITY;  // four are read at a time
+                    __syncwarp();
+                    const float own = lane < n ? list[lane] : 0.f;
+                    const int own_at = lane < n ? list_at[lane] : 0;
+                    int rank = -1;  // the score itself is counted too
+                    for (int j = 0; j < n; j += 4) {
+                        const float4 q = *reinterpret_cast<const float4*>(&list[j]);
+                        rank += (q.x >= own) + (q.y >= own) + (q.z >= own) + (q.w >= own);
+                    }
+                    // without equal scores the ranks are 0 .. n - 1
+                    if (__reduce_add_sync(~0u, lane < n ? rank : 0) != n * (n - 1) / 2) {
+                        rank = 0;
+                        for (int j = 0; j < n; ++j) rank += list[j] > own || (list[j] == own && list_at[j] < own_at) ? 1 : 0;
+                    }
+                    if (lane < n && rank < k) {
+                        to[rank] = own_at;
+                        gate_to[rank] = ref.exp(own) * inv;
+                        atomicAdd(&sh_n[own_at], 1u);
+                    }
+                    taken = min(n, k);
+                } else {
+                    unsigned gone = 0u;  // of this lane's scores
+                    for (; taken < k; ++taken) {
+                        uint32_t key = 0u;
+                        int at = -1;
+#pragma unroll
+                        for (int i = 0; i < EPL; ++i) {
+                            const uint32_t q = choice_key(v[i]);
+                            if (!(gone >> i & 1u) && (q > key || (q == key && q != 0u && row.expert(gl, i) < row.expert(gl, at)))) {
+                                key = q;
+                                at = i;
+                            }
+                        }
+                        const uint32_t best = __reduce_max_sync(group, key);
+                        if (best == 0u) break;
+                        const unsigned which = key == best ? (unsigned)row.expert(gl, at) : ~0u;
+                        const unsigned winner = __reduce_min_sync(group, which);
+                        if (which == winner) {
+                            gone |= 1u << at;
+                            to[taken] = (int)winner;
+                            gate_to[taken] = ref.exp(choice_score(best)) * inv;
+                            atomicAdd(&sh_n[winner], 1u);
+                        }
                     }
                 }
+                __syncwarp();
+                if (a.renormalize) {  // the gates over their sum
+                    float mine = 0.f;
+                    for (int c = gl; c < taken; c += G) mine += gate_to[c];
+                    const float scale = 1.f / group_add<G>(mine);
+                    for (int c = gl; c < taken; c += G) gate_to[c] *= scale;
+                }
             }
-            __syncwarp();
-            if (a.renormalize) {  // the gates over their sum
-                float mine = 0.f;
-                for (int c = gl; c < taken; c += G) mine += gate_to[c];
-                const float scale = 1.f / group_add<G>(mine);
-                for (int c = gl; c < taken; c += G) gate_to[c] *= scale;
-            }
+            // the places that no open expert takes
+            if (t < a.tokens)
+                for (int c = taken + gl; c < k; c += G) {
+                    to[c] = -1;
+                    gate_to[c] = 0.f;
+                }
         }
-        // the places that no open expert takes
-        if (t < a.tokens)
-            for (int c = taken + gl; c < k; c += G) {
-                to[c] = -1;
-                gate_to[c] = 0.f;
-            }
-    }
-    // the CTA's sums, in the order of its warps
-    if constexpr (G < 32) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-#pragma unroll
-            for (int o = 16; o >= G; o >>= 1) psum[i] += __shfl_xor_sync(~0u, psum[i], o);
-    }
-    for (int w = 0; w < kTokWarps; ++w) {
-        if (warp == w && lane < G) {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) sh_p[row.expert(gl, i)] += psum[i];
-        }
-        __syncthreads();
-    }
+        gather(begun);
+        begun = true;
+    } while (first < a.tokens);
     tokens = __reduce_add_sync(~0u, tokens);
     if (lane == 0) atomicAdd(&sh_live, tokens);
     __syncthreads();
-    if (gridDim.x > 1) {
-        for (int e = threadIdx.x; e < E; e += kTokThreads) {
-            b.p[(int64_t)blockIdx.x * E + e] = sh_p[e];
+    // the CTA's sums, in the order of its warps
+    for (int e = threadIdx.x; e < E; e += kTokThreads) {
+        Sum s;
+        for (int w = 0; w < kTokWarps; ++w) s.add(as_sum(warp_sums[w * G * EPL + e]));
+        if (gridDim.x > 1) {
+            b.p[(int64_t)blockIdx.x * E + e] = {s.hi, s.lo};
             b.n[(int64_t)blockIdx.x * E + e] = sh_n[e];
+        } else {
+            o.counts[e] = sh_n[e];
+            warp_sums[e].x = s.value() * (float)sh_n[e];  // (no other thread reads this place before)
         }
+    }
+    if (gridDim.x > 1) {
         if (threadIdx.x == 0) b.live[blockIdx.x] = sh_live;
         return;
     }
     // one CTA has had all tokens: the loss
-    for (int e = threadIdx.x; e < E; e += kTokThreads) o.counts[e] = sh_n[e];
+    __syncthreads();
     if (warp == 0) {
-        float sum = 0.f;
-        for (int e = lane; e < E; e += 32) sum = fmaf(sh_p[e], (float)sh_n[e], sum);
-        sum = warp_add(sum);
-        if (lane == 0) balance_result(o, sh_live, E, k, sum);
+        Sum sum;
+        for (int e = lane; e < E; e += 32) sum.add(warp_sums[e].x);
+        sum = warp_sum(sum);
+        if (lane == 0) balance_result(o, sh_live, E, k, sum.value());
     }
 }
 
@@ -370,48 +401,46 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
 // 6 us after the choice for 304 CTAs' sums of 256 experts (one CTA alone took 50).
 __global__ void __launch_bounds__(512)
 balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k) {
-    __shared__ float sh_p[512];
+    __shared__ float2 sh_p[512], sh_sum[kFinishCtas], sh_warp[16];
     __shared__ uint32_t sh_n[512];
-    __shared__ float sh_sum[kFinishCtas], sh_warp[16];
     const int rank = (int)cluster_rank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int share = (E + kFinishCtas - 1) / kFinishCtas;  // at most 128
     int cols = 1;
     while (cols < share) cols *= 2;
-    const int col = tid & (cols - 1), part = tid / cols, parts = 512 / cols;
+    const int col = tid & (cols - 1), part = tid / cols, parts = min(512 / cols, 32);
     const int e = rank * share + col;
-    const bool has = col < share && e < E;
+    const bool has = col < share && e < E && part < parts;
     cluster_started();
     wait_for_previous();
-    float p = 0.f;
+    Sum p;
     uint32_t n = 0u;
     if (has)
         for (int g = part; g < grid; g += parts) {
-            p += b.p[(int64_t)g * E + e];
+            p.add(as_sum(b.p[(int64_t)g * E + e]));
             n += b.n[(int64_t)g * E + e];
         }
-    sh_p[tid] = p;
+    sh_p[tid] = {p.hi, p.lo};
     sh_n[tid] = n;
     __syncthreads();
-    float product = 0.f;
+    Sum products;
     if (part == 0 && has) {
         uint64_t total = n;
-        Sum s;
-        s.add(p);
         for (int q = 1; q < parts; ++q) {
-            s.add(sh_p[q * cols + col]);
+            p.add(as_sum(sh_p[q * cols + col]));
             total += sh_n[q * cols + col];
         }
         o.counts[e] = (int64_t)total;
-        product = s.value() * (float)total;
+        products.add(p.value() * (float)total);
     }
-    product = warp_add(product);
-    if (lane == 0) sh_warp[warp] = product;
+    products = warp_sum(products);
+    if (lane == 0) sh_warp[warp] = {products.hi, products.lo};
     __syncthreads();
     cluster_wait_started();
     if (tid == 0) {
-        float s = 0.f;
-        for (int w = 0; w < 16; ++w) s += sh_warp[w];
-        store_remote(&sh_sum[rank], 0, s);
+        Sum s;
+        for (int w = 0; w < 16; ++w) s.add(as_sum(sh_warp[w]));
+        store_remote(&sh_sum[rank].x, 0, s.hi);
+        store_remote(&sh_sum[rank].y, 0, s.lo);
     }
     __syncwarp();
     cluster_sync();
@@ -421,9 +450,9 @@ balance_finish_kernel(BalanceParts b, BalanceOuts o, int grid, int E, int top_k)
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
         if (lane == 0) {
-            float s = 0.f;
-            for (int c = 0; c < kFinishCtas; ++c) s += sh_sum[c];
-            balance_result(o, t, E, top_k, s);
+            Sum s;
+            for (int c = 0; c < kFinishCtas; ++c) s.add(as_sum(sh_sum[c]));
+            balance_result(o, t, E, top_k, s.value());
         }
     }
 }
@@ -546,7 +575,7 @@ inline bool chunks_fit(const void* x, int64_t rows, int64_t stride, int experts,
 }  // namespace
 
 size_t balance_workspace(int64_t tokens, int experts) {
-    return 2048 + (size_t)token_grid(tokens, 8, kMaxCtas) * experts * 8;
+    return (2048 + (size_t)token_grid(tokens, 8, kMaxCtas) * experts * 12 + 255) & ~size_t(255);
 }
 
 cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* counts,
@@ -560,10 +589,15 @@ cudaError_t balance_loss(int dtype, const RouterArgs& a, float* loss, int64_t* c
             using T = decltype(t);
             constexpr int G = decltype(g)::value, EPL = decltype(epl)::value;
             grid = token_grid<G, EPL>(a.tokens);
-            b.p = reinterpret_cast<float*>(static_cast<char*>(ws) + 2048);
+            b.p = reinterpret_cast<float2*>(static_cast<char*>(ws) + 2048);
             b.n = reinterpret_cast<uint32_t*>(b.p + (int64_t)grid * a.experts);
             const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, TokenRow<T, G, EPL>::CH, sizeof(T));
-            balance_tokens_kernel<T, G, EPL><<<grid, token_threads<EPL>, 0, st>>>(a, b, o, whole, chosen, gates);
+            constexpr int shared = token_threads<EPL> / 32 * G * EPL * (int)sizeof(float2);
+            if (shared > 40 * 1024) {  // (what the kernel has besides is within 48 KB of it)
+                const cudaError_t e = cudaFuncSetAttribute(balance_tokens_kernel<T, G, EPL>, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
+                if (e != cudaSuccess) return e;
+            }
+            balance_tokens_kernel<T, G, EPL><<<grid, token_threads<EPL>, shared, st>>>(a, b, o, whole, chosen, gates);
             const cudaError_t e = cudaGetLastError();
             prof_mark(st, "balance_tokens");
             return e;

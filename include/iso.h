@@ -311,9 +311,11 @@ iso_status iso_backward_noalloc(const float *grad, const uint8_t *blocks, const 
  * Conventions, beside those at the top of this file:
  *  - Scores and their gradients are float32, bfloat16 or float16 (`dtype`);
  *    everything else is float32 unless said otherwise.  Sums and softmax
- *    statistics are float32 within a row and float64 across rows; a gradient
- *    is rounded once, to the scores' type.  Results do not depend on timing:
- *    the same call gives the same bits.
+ *    statistics are float32 within a row (and over up to 64 tokens of a router);
+ *    sums over rows, tokens and pairs are two float32 each, of which the second
+ *    holds what the first has rounded off.  A gradient is rounded once, to the
+ *    scores' type.  Results do not depend on timing: the same call gives the
+ *    same bits.
  *  - Row r of the scores starts at element r * stride, of the gradient at
  *    r * out_stride (strides in elements; the gradient's at least n).  1 <= n <=
  *    2^31 - 1, 0 <= rows <= 2^31 - 1, rows * stride <= 2^40.  Element alignment is enough.

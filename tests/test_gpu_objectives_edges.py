@@ -259,3 +259,19 @@ def test_outputs_of_no_rows(cuda_ok):
         assert r.norm.shape == (0, 2) and r.coef.shape == (0,) and r.row_status.shape == (0,) and r.logp.shape == (0,)
         assert not r.row_status.any() and len(list(r)) == len(r)
     assert r.pair_status.tolist() == [0] and r.margins.tolist() == [0.0]
+
+
+def test_router_sums_over_many_tokens(cuda_ok):
+    """The probabilities of 2^26 equal tokens: their sum is exact up to 64 additions in float32 (2^-25
+    each, 1.9e-6 in all), a probability's error (4e-7) and the loss's last roundings (2e-7)."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    row = torch.tensor([0.3, -0.2, 0.75, -1.0], device="cuda", dtype=torch.bfloat16)
+    x = row.repeat(1 << 26, 1)
+    r = obj.iso_balance_loss(x, 1)
+    p = float(torch.softmax(row.double(), 0)[2])
+    assert r.counts.tolist() == [0, 0, 1 << 26, 0] and int(r.live) == 1 << 26
+    assert abs(float(r.loss) - 4 * p) <= 3e-6 * 4 * p
+    # and of tokens that one CTA takes alone
+    r = obj.iso_balance_loss(x[:7], 1)
+    assert abs(float(r.loss) - 4 * p) <= 3e-6 * 4 * p
