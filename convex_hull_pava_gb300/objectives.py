@@ -106,10 +106,11 @@ _raw_stream = None
 def _setup():
     global _abi, _dtypes, _raw_stream
     torch = _torch()
-    _dtypes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _abi = load_library()
+    _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    # last: calls, of other threads too, take this one for all three
+    _dtypes = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
     return torch
 
 
