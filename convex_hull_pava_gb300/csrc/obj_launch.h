@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include "iso_internal.h"
@@ -45,20 +46,22 @@ struct ClusterLaunch {
 };
 
 // The clusters of `ctas` CTAs of a kernel that the GPU holds at once (a cluster's CTAs share a
-// group of SMs, so that they are fewer than its SMs alone would take); asked once for each `held`.
+// group of SMs, so that they are fewer than its SMs alone would take); asked once for each `held`
+// (by several threads at first, if they call at once: they find the same).
+using Held = std::atomic<int>[64][4];
 template <class F>
-cudaError_t clusters_held(F* kernel, const cudaLaunchConfig_t& config, int ctas, int (&held)[64][4], int* fit) {
+cudaError_t clusters_held(F* kernel, const cudaLaunchConfig_t& config, int ctas, Held& held, int* fit) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    int& known = held[dev][ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3];
-    if (known == 0) {
+    std::atomic<int>& known = held[dev][ctas == 1 ? 0 : ctas == 2 ? 1 : ctas == 4 ? 2 : 3];
+    int n = known.load(std::memory_order_acquire);
+    if (n == 0) {
         const int shared = (int)config.dynamicSmemBytes;
         if (shared > 48 * 1024 &&
             (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared)) != cudaSuccess)
             return e;
-        int n = 0;
         if (ctas == 1) {
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, (int)config.blockDim.x, shared);
             n *= device_sms();
@@ -71,9 +74,10 @@ cudaError_t clusters_held(F* kernel, const cudaLaunchConfig_t& config, int ctas,
             cudaGetLastError();
             return e;
         }
-        known = std::max(1, n);
+        n = std::max(1, n);
+        known.store(n, std::memory_order_release);
     }
-    *fit = known;
+    *fit = n;
     return cudaSuccess;
 }
 

@@ -896,7 +896,7 @@ template <class T, int NT, int TEAM, int K, bool LONG>
 cudaError_t launch_policy(const ScoreRows& s, PolicyArgs p, const RowOuts& o, int ctas, void* ws, cudaStream_t st) {
     auto* kernel = policy_rows_kernel<T, NT, TEAM, K, LONG>;
     ClusterLaunch l(1, NT, LONG ? 0 : (size_t)NT * K * 16, ctas, true, st);
-    static int held[64][4];
+    static Held held;
     int fit = 0;
     cudaError_t e = clusters_held(kernel, l.c, ctas, held, &fit);
     if (e != cudaSuccess) return e;
@@ -943,7 +943,7 @@ cudaError_t run_logp(const ScoreRows& s, const RowOuts& o, void* ws, bool zero_t
     const bool warps = w.share(1) <= 32 * 8;
     const int per_cta = warps ? NT / 32 : 1;
     auto* kernel = warps ? score_stream_kernel<T, NT, 32, U, D> : score_stream_kernel<T, NT, NT, U, D>;
-    static int held[2][64][4];
+    static Held held[2];
     int best = 1, best_fit = 1;
     double least = 0.0;
     for (int ctas = 1; ctas <= 8 && (ctas == 1 || (!warps && w.words >= (int64_t)ctas * NT)); ctas *= 2) {

@@ -275,3 +275,37 @@ def test_router_sums_over_many_tokens(cuda_ok):
     # and of tokens that one CTA takes alone
     r = obj.iso_balance_loss(x[:7], 1)
     assert abs(float(r.loss) - 4 * p) <= 3e-6 * 4 * p
+
+
+def test_first_calls_from_several_threads(cuda_ok):
+    """A process's first calls, from several threads at once, each on a stream of its own."""
+    import os
+    import subprocess
+    import sys
+    program = """
+import threading
+import torch
+from convex_hull_pava_gb300 import objectives as obj
+g = torch.Generator(device="cuda").manual_seed(1)
+x = [torch.randn((n, v), device="cuda", generator=g) for n, v in ((70, 900), (90, 9000), (30, 70000), (5, 300001))]
+labels = [torch.arange(len(v), device="cuda") % 7 for v in x]
+zero = [torch.zeros(len(v), device="cuda") for v in x]
+torch.cuda.synchronize()
+got, at = [None] * 8, threading.Barrier(8)
+
+def run(i):
+    at.wait()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got[i] = [t for v, l, z in zip(x, labels, zero)
+                  for t in (obj.iso_token_logp(v, l)[0], obj.iso_policy_loss(v, l, z, z + 1).dlogits, obj.iso_balance_loss(v[:, :64], 4).loss)]
+        torch.cuda.current_stream().synchronize()
+
+threads = [threading.Thread(target=run, args=(i,)) for i in range(8)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+assert all(torch.equal(a, b) for other in got[1:] for a, b in zip(got[0], other))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
