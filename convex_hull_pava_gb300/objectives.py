@@ -17,7 +17,7 @@ which states the formulas, the masks and the errors in full):
 * :func:`iso_balance_loss`, :func:`iso_balance_loss_backward`
 
 Differentiable in the scores (autograd): :func:`token_logp`, :func:`policy_loss`,
-:func:`preference_loss`, :func:`balance_loss`.
+:func:`preference_loss`, :func:`balance_loss` (first derivatives only).
 
 Scores are float32, bfloat16 or float16 CUDA tensors, ``[rows, n]`` or ``[n]``,
 contiguous within a row (rows may be strided); gradients have their type.
@@ -438,6 +438,20 @@ def iso_balance_loss_backward(logits, result, *, grad_loss: float = 1.0, grad_lo
 def _make():
     torch = _torch()
 
+    class _FirstOnly(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, d, logits):
+            return d.detach()
+
+        @staticmethod
+        def backward(ctx, g):
+            raise RuntimeError("the objectives have first derivatives only")
+
+    def first_only(d, logits):
+        # A gradient is a kernel's output, without a graph of its own: where one is asked for
+        # (create_graph), its derivative is refused and not taken for 0.
+        return _FirstOnly.apply(d, logits) if torch.is_grad_enabled() and logits.requires_grad else d
+
     class _TokenLogp(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, labels, temperature):
@@ -449,17 +463,17 @@ def _make():
         @staticmethod
         def backward(ctx, g):
             logits, labels, norm = ctx.saved_tensors
-            return iso_token_logp_backward(g.contiguous(), logits, labels, norm,
-                                           temperature=ctx.temperature), None, None
+            d = iso_token_logp_backward(g.contiguous(), logits, labels, norm, temperature=ctx.temperature)
+            return first_only(d, logits), None, None
 
     def hand_over(ctx, g):
         # The forward left the gradient for an upstream gradient of 1.  It is handed out once
         # (rewritten when g is not 1); a further backward through the same graph forms it anew.
         logits, labels, norm, coef = ctx.saved_tensors
         held, ctx.dlogits = ctx.dlogits, None
-        return iso_token_logp_backward(coef, logits, labels, norm, temperature=ctx.temperature,
-                                       grad_scale_dev=g.contiguous(),
-                                       changed_only=held is not None, out=held)
+        d = iso_token_logp_backward(coef, logits, labels, norm, temperature=ctx.temperature,
+                                    grad_scale_dev=g.contiguous(), changed_only=held is not None, out=held)
+        return first_only(d, logits)
 
     class _PolicyLoss(torch.autograd.Function):
         @staticmethod
@@ -505,10 +519,11 @@ def _make():
             if g_loss is None and g_gates is None:
                 return (None,) * 4
             r = BalanceLoss(None, counts, experts, gates, buf, mask, ctx.renormalize)
-            return iso_balance_loss_backward(
+            d = iso_balance_loss_backward(
                 logits, r, grad_loss=0.0 if g_loss is None else 1.0,
                 grad_loss_dev=None if g_loss is None else g_loss.contiguous(),
-                grad_gates=None if g_gates is None else g_gates.contiguous()), None, None, None
+                grad_gates=None if g_gates is None else g_gates.contiguous())
+            return first_only(d, logits), None, None, None
 
     return {"token": _TokenLogp, "policy": _PolicyLoss, "preference": _PreferenceLoss,
             "balance": _BalanceLoss}

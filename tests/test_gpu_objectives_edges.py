@@ -309,3 +309,18 @@ print("same")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", program], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]
+
+
+def test_no_second_derivatives(cuda_ok):
+    """The gradients carry no graph of their own: a second derivative is refused, not left out."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    x = torch.randn((6, 9), device="cuda", requires_grad=True)
+    labels, zero = ids([0, 1, 2, 3, 4, 5]), torch.zeros(6, device="cuda")
+    for loss in (lambda: obj.token_logp(x, labels).square().sum(), lambda: obj.policy_loss(x, labels, zero, zero + 1)[0],
+                 lambda: obj.preference_loss(x, labels, ids([0, 3, 6]))[0], lambda: obj.balance_loss(x, 2)[1].square().sum()):
+        first, = torch.autograd.grad(loss(), x)
+        again, = torch.autograd.grad(loss(), x, create_graph=True)
+        assert torch.equal(first, again)
+        with pytest.raises(RuntimeError):
+            torch.autograd.grad(again.square().sum() + x.square().sum(), x)
