@@ -829,7 +829,8 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
                 const float e = expf(-fabsf(z)), over = log1pf(e);
                 const float up = (z >= 0.f ? 1.f : e) / (1.f + e);  // sigmoid(z)
                 const float down = (z >= 0.f ? e : 1.f) / (1.f + e);  // sigmoid(-z)
-                each = over + (1.f - p.smooth) * (z < 0.f ? -z : 0.f) + p.smooth * (z > 0.f ? z : 0.f);
+                // (a side without weight has no part, also where z is infinite)
+                each = over + (z < 0.f && p.smooth < 1.f ? (1.f - p.smooth) * -z : 0.f) + (z > 0.f && p.smooth > 0.f ? p.smooth * z : 0.f);
                 slope = beta * (p.smooth * up - (1.f - p.smooth) * down);
             } else if (p.kind == ISO_PREFERENCE_HINGE) {
                 each = z < 1.f ? 1.f - z : z >= 1.f ? 0.f : z;

@@ -407,6 +407,7 @@ iso_status iso_policy_loss(const void *logits, int dtype, int64_t rows, int64_t 
  *
  *   h_q = (S_2q - R_2q) - (S_2q+1 - R_2q+1),   z_q = beta h_q
  *   sigmoid: -(1 - label_smoothing) log sigmoid(z) - label_smoothing log sigmoid(-z)
+ *            (a term of weight 0 is 0, also where z is infinite: a closed label)
  *   hinge:   max(0, 1 - z)
  *   squared: (h - 1 / (2 beta))^2
  *   loss = mean over the pairs.

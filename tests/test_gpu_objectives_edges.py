@@ -324,3 +324,23 @@ def test_no_second_derivatives(cuda_ok):
         assert torch.equal(first, again)
         with pytest.raises(RuntimeError):
             torch.autograd.grad(again.square().sum() + x.square().sum(), x)
+
+
+def test_infinite_margins(cuda_ok):
+    """A sequence with a token of probability 0: the pair's loss is its formula's limit, in which a term
+    that the smoothing gives no weight has no part."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    x = torch.zeros((4, 8), device="cuda")
+    x[:, 5] = -float("inf")
+    for rejected, chosen in ((5, 1), (1, 5)):
+        labels, off = ids([chosen, rejected, 2, 3]), ids([0, 1, 2, 3, 4])
+        sign = 1.0 if rejected == 5 else -1.0
+        for smooth, want in ((0.0, 0.0 if sign > 0 else np.inf), (1.0, np.inf if sign > 0 else 0.0), (0.1, np.inf)):
+            r = obj.iso_preference_loss(x, labels, off, beta=0.5, label_smoothing=smooth)
+            assert r.margins.tolist() == [sign * np.inf, 0.0]
+            got = float(r.loss)
+            assert got == np.inf if want == np.inf else abs(got - np.log(2) / 2) <= 1e-6
+            # the slope: -(1 - smooth) sigmoid(-z) + smooth sigmoid(z), halved over the pairs, times beta
+            slope = 0.25 * (smooth if sign > 0 else smooth - 1.0)
+            assert np.abs(wide(r.coef)[:2] - [slope, -slope]).max() <= 1e-6
