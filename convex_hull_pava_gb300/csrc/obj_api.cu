@@ -24,7 +24,11 @@ bool rows_ok(int dtype, int64_t rows, int64_t n, int64_t stride, int64_t least) 
            (rows <= 1 || stride >= least);
 }
 
-bool temperature_ok(float t) { return std::isfinite(t) && t > 0.f && std::isfinite(1.f / t); }
+float exponent_scale(float t) { return (float)(1.4426950408889634074 / t); }  // log2(e) / t
+
+bool temperature_ok(float t) {
+    return std::isfinite(t) && t > 0.f && std::isfinite(1.f / t) && std::isfinite(exponent_scale(t));
+}
 
 bool workspace_ok(const void* ws, size_t bytes, size_t need) {
     return need == 0 || (ws && bytes >= need && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0);
@@ -32,8 +36,7 @@ bool workspace_ok(const void* ws, size_t bytes, size_t need) {
 
 isodev::ScoreRows score_rows(const void* logits, int64_t rows, int64_t n, int64_t stride,
                              const int64_t* labels, float temperature) {
-    return {logits, rows, (int)n, stride, labels, temperature, 1.f / temperature,
-            (float)(1.4426950408889634074 / temperature)};
+    return {logits, rows, (int)n, stride, labels, temperature, 1.f / temperature, exponent_scale(temperature)};
 }
 
 }  // namespace

@@ -327,6 +327,7 @@ iso_status iso_backward_noalloc(const float *grad, const uint8_t *blocks, const 
  *    value is an ordinary, very small score.  A row with a NaN or +inf, or
  *    with nothing but -inf, has no probabilities: its log-probability and
  *    gradient are NaN and its row_status has ISO_ROW_BAD_Y.
+ *  - temperature > 0, with 1 / T and log2(e) / T in float32's range.
  *  - norm [rows, 2], 8-byte aligned: the row's softmax statistics (its largest score and the sum
  *    of exponentials against it), from which the backward forms p without another pass.
  *  - The gradient may be written over the scores (dlogits == logits, out_stride == stride).
