@@ -64,7 +64,7 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, LogP logp, 
         // exp(d) - 1 - d without its cancellation at small d
         const float d = -logp.minus(ref), e = expm1f(d);
         q.kl = w * (e - d);
-        q.coef -= p.kl_coef * w * e;
+        if (p.kl_coef != 0.f) q.coef -= p.kl_coef * w * e;  // (0 of an exponential past float32's range is 0)
     }
     return q;
 }
@@ -443,7 +443,7 @@ policy_rows_kernel(ScoreRows sc, PolicyArgs p, RowOuts o, RowList rl) {
     if (threadIdx.x == 0) {
         for (int i = 0; i < 3; ++i) p.stats[i] = total[i].value();
         // the KL term's product rounds once
-        *p.loss = p.ref_logp ? fmaf(p.kl_coef, total[1].value(), total[0].value()) : total[0].value();
+        *p.loss = p.kl_coef != 0.f ? fmaf(p.kl_coef, total[1].value(), total[0].value()) : total[0].value();
     }
 }
 

@@ -344,3 +344,15 @@ def test_infinite_margins(cuda_ok):
             # the slope: -(1 - smooth) sigmoid(-z) + smooth sigmoid(z), halved over the pairs, times beta
             slope = 0.25 * (smooth if sign > 0 else smooth - 1.0)
             assert np.abs(wide(r.coef)[:2] - [slope, -slope]).max() <= 1e-6
+
+
+def test_kl_term_without_weight(cuda_ok):
+    """A KL weight of 0 leaves no KL term, however far the reference's log-probability is (its
+    exponential leaves float32's range)."""
+    from convex_hull_pava_gb300 import objectives as obj
+    x, labels, lp = put(np.zeros((4, 6))), ids([0, 1, 2, 3]), float(-np.log(6.0))
+    base = put([lp, lp + 150.0, lp, lp])
+    r = obj.iso_policy_loss(x, labels, put([lp] * 4), put([1.0] * 4), base, kl_coef=0.0)
+    # a ratio of 1: off by the log-probability's 1e-5
+    assert abs(float(r.loss) + 1.0) <= 2e-5 and np.abs(wide(r.coef) + 0.25).max() <= 0.25 * 2e-5
+    assert float(r.stats[1]) == np.inf and bool(r.dlogits.isfinite().all())
