@@ -52,7 +52,8 @@ struct PolicyRow {
 __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, LogP logp, float old,
                                                 float adv, float ref, float w) {
     const float ratio = expf(logp.minus(old));
-    const float free = -adv * ratio;
+    // (an advantage of 0 leaves nothing, also of a ratio past float32's range)
+    const float free = adv == 0.f && ratio == INFINITY ? 0.f : -adv * ratio;
     const float held = -adv * fminf(fmaxf(ratio, p.low), p.high);
     const bool cut = held > free;
     PolicyRow q;

@@ -356,3 +356,13 @@ def test_kl_term_without_weight(cuda_ok):
     # a ratio of 1: off by the log-probability's 1e-5
     assert abs(float(r.loss) + 1.0) <= 2e-5 and np.abs(wide(r.coef) + 0.25).max() <= 0.25 * 2e-5
     assert float(r.stats[1]) == np.inf and bool(r.dlogits.isfinite().all())
+
+
+def test_advantage_of_zero(cuda_ok):
+    """An advantage of 0 leaves no policy term, however small the old probability is (the ratio leaves
+    float32's range)."""
+    from convex_hull_pava_gb300 import objectives as obj
+    x, labels, lp = put(np.zeros((4, 6))), ids([0, 1, 2, 3]), float(-np.log(6.0))
+    r = obj.iso_policy_loss(x, labels, put([lp, lp - 200.0, lp, lp - 200.0]), put([1.0, 0.0, -1.0, -0.0]))
+    assert abs(float(r.loss)) <= 1e-5 and wide(r.coef).tolist()[1::2] == [0.0, 0.0]
+    assert np.abs(wide(r.coef)[[0, 2]] - [-0.25, 0.25]).max() <= 1e-5 and not wide(r.dlogits)[1::2].any()
