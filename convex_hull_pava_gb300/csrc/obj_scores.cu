@@ -663,7 +663,7 @@ score_backward_kernel(ScoreRows sc, const float* norm, const float* coef, float 
     const bool owner = s.owner(label, TEAM) == tt;
     const float at_label = owner ? to_f32(x[label]) : 0.f;
     const float2 ms = *reinterpret_cast<const float2*>(norm + 2 * r);
-    const float g = coef[r] * grad_scale * sc.inv_t;
+    const float g = label < n ? coef[r] * grad_scale * sc.inv_t : NAN;  // (no log-probability, no gradient)
     const RowGrad<T> grad{g, __fdividef(-g, ms.y), SoftRef(ms.x, sc.a)};
     auto give = [&](auto far) {
 #pragma unroll

@@ -322,7 +322,7 @@ iso_status iso_backward_noalloc(const float *grad, const uint8_t *blocks, const 
  *  - labels [rows] int64: a negative label marks a row that takes no part; its
  *    scores (and its other inputs) are not used, its log-probability is 0 and
  *    its gradient 0.  A label >= n is an error in the data: the row's
- *    log-probability is NaN and its row_status has ISO_ROW_BAD_LABEL.
+ *    log-probability and gradient are NaN and its row_status has ISO_ROW_BAD_LABEL.
  *  - A score of -inf is a closed entry of probability 0.  The type's lowest
  *    value is an ordinary, very small score.  A row with a NaN or +inf, or
  *    with nothing but -inf, has no probabilities: its log-probability and

@@ -366,3 +366,24 @@ def test_advantage_of_zero(cuda_ok):
     r = obj.iso_policy_loss(x, labels, put([lp, lp - 200.0, lp, lp - 200.0]), put([1.0, 0.0, -1.0, -0.0]))
     assert abs(float(r.loss)) <= 1e-5 and wide(r.coef).tolist()[1::2] == [0.0, 0.0]
     assert np.abs(wide(r.coef)[[0, 2]] - [-0.25, 0.25]).max() <= 1e-5 and not wide(r.dlogits)[1::2].any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_labels_past_the_end(cuda_ok, dtype):
+    """A label that is not below n: no log-probability and no gradient, in every call."""
+    from convex_hull_pava_gb300 import objectives as obj
+    for n in (7, 900, 9000):
+        x, xw, labels, rng = make(9, n, dtype, seed=n, ignored=0.0)
+        good = ids(labels)
+        labels[[1, 4, 8]] = [n, n + 7, 1 << 40]
+        bad = np.isin(np.arange(9), [1, 4, 8])
+        li, one = ids(labels), put(np.ones(9))
+        lp, norm, st = obj.iso_token_logp(x, li)
+        assert np.array_equal(np.isnan(wide(lp)), bad) and np.array_equal(st.cpu().numpy(), 8 * bad)
+        d = wide(obj.iso_token_logp_backward(one, x, li, norm))
+        want = wide(obj.iso_token_logp_backward(one, x, good, norm))
+        assert np.isnan(d[bad]).all() and np.array_equal(d[~bad], want[~bad])
+        r = obj.iso_policy_loss(x, li, one, one)
+        assert np.isnan(wide(r.dlogits)[bad]).all() and np.isfinite(wide(r.dlogits)[~bad]).all()
+        r = obj.iso_preference_loss(x, li, ids([0, 1, 2, 3, 4, 5, 6, 7, 8]))
+        assert r.margins.isnan().tolist() == [True, False, True, False]
