@@ -269,7 +269,8 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
                 __syncwarp();
                 const bool mine = open && key != 0u && rank < k;
                 float gate = mine ? e[0] : 0.f;
-                gate *= a.renormalize ? 1.f / group_add<G>(gate) : inv;
+                // (0 inv: a token without probabilities has no gates)
+                gate *= a.renormalize ? fmaf(0.f, inv, 1.f / group_add<G>(gate)) : inv;
                 if (mine) {
                     to[rank] = gl;
                     gate_to[rank] = gate;

@@ -459,6 +459,8 @@ iso_status iso_preference_loss(const void *logits, int dtype, int64_t rows, int6
  *             score of -inf or NaN is never chosen) or the token takes no part.
  *  gates      [tokens, top_k] float32, written: 0 where chosen is -1.
  *  live       one int64, written: T.
+ *             A NaN or +inf among the scores of a token that takes part makes its
+ *             gates, its gradient and the loss NaN.
  *  workspace  iso_balance_loss_workspace_bytes(tokens, experts) bytes, 256-byte aligned.
  *
  * iso_balance_loss_backward -- the gradient of grad_loss * (*grad_loss_dev) * loss

@@ -387,3 +387,40 @@ def test_labels_past_the_end(cuda_ok, dtype):
         assert np.isnan(wide(r.dlogits)[bad]).all() and np.isfinite(wide(r.dlogits)[~bad]).all()
         r = obj.iso_preference_loss(x, li, ids([0, 1, 2, 3, 4, 5, 6, 7, 8]))
         assert r.margins.isnan().tolist() == [True, False, True, False]
+
+
+@pytest.mark.parametrize("n", [4, 8, 16, 30, 64, 256, 600])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_router_scores_of_nan(cuda_ok, n, renormalize):
+    """A NaN or +inf makes the gates and the gradient of its token NaN, at any number of experts, and the
+    loss; the other tokens are as they are alone."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    x = torch.randn((40, n), device="cuda", generator=torch.Generator(device="cuda").manual_seed(n))
+    want = obj.iso_balance_loss(x, 3, renormalize=renormalize)
+    x[5, 1], x[17, n - 1] = float("nan"), float("inf")
+    r = obj.iso_balance_loss(x, 3, renormalize=renormalize)
+    bad = torch.zeros(40, dtype=torch.bool, device="cuda")
+    bad[[5, 17]] = True
+    assert bool(r.gates[bad].isnan().all()) and torch.equal(r.gates[~bad], want.gates[~bad])
+    assert torch.equal(r.experts[~bad], want.experts[~bad]) and bool((r.experts[5] != 1).all()) and int(r.experts[17, 0]) == n - 1
+    assert bool(r.loss.isnan())
+    d = obj.iso_balance_loss_backward(x, r, grad_gates=torch.ones_like(r.gates))
+    assert bool(d[bad].isnan().all()) and bool(d[~bad].isfinite().all())
+
+
+def test_router_of_many_experts_in_a_graph(cuda_ok):
+    """More than 512 experts, whose sums take more shared memory than a kernel has by itself, captured."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    x = torch.randn((3000, 1000), device="cuda")
+    held = torch.zeros_like(x)
+    obj.iso_balance_loss(held, 4)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = obj.iso_balance_loss(held, 4)
+    held.copy_(x)
+    graph.replay()
+    want = obj.iso_balance_loss(x, 4)
+    assert torch.equal(r.loss, want.loss) and torch.equal(r.experts, want.experts) and torch.equal(r.counts, want.counts)
