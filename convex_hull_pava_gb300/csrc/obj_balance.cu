@@ -173,14 +173,14 @@ __device__ __forceinline__ SoftState token_softmax(const float (&v)[EPL], float 
 __device__ __forceinline__ bool token_open(SoftState st) { return !(st.m == -INFINITY && st.s == 0.f); }
 
 // A group of G lanes a token, several tokens to a warp where G < 32 (then EPL is 1).  The choice:
-// with EPL = 1 each lane counts the scores above its own, four to a read.  Otherwise the k-th largest of the lanes'
-// largest scores bounds the k-th largest score from below; the scores that reach it (k and a few
-// more) are collected and each counts those above it.  When more than 32 reach it, k rounds of one
-// maximum each.
+// with EPL = 1 each lane counts the scores above its own, four to a read of shared memory (by shuffles
+// 32 experts took 57 us and not 55).  Otherwise the k-th largest of the lanes' largest scores bounds
+// the k-th largest score from below; the scores that reach it (k and a few more) are collected and
+// each counts those above it.  When more than 32 reach it, k rounds of one maximum each.
 // The probabilities of an expert are added in float32 over up to 64 tokens of a lane, those sums to one
 // of the warp that keeps what it rounds off (in float32 throughout, the loss of 2^26 equal tokens was
 // 1.4e-5 off; the same times).
-// Bound by instructions: 439 a token at 256 experts and k = 8 (61 us for 131,072 tokens of float32,
+// Bound by instructions: 443 a token at 256 experts and k = 8 (62 us for 131,072 tokens of float32,
 // 2.2 TB/s).  k rounds of one maximum each for all took 214 us, collecting by ballots 69, two tokens
 // a warp 80.
 template <class T, int G, int EPL>

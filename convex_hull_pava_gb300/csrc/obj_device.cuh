@@ -215,7 +215,8 @@ struct LogP {
 // with high + low = log 2 and so few bits in high that k high is exact.  The exponentials are low by
 // 5.1e-8 of themselves in the mean (ex2 against 64 bits, 2^22 arguments in each of -2..-26's pairs of
 // octaves; not the largest score's, which is 1), and so is the rest of their sum; hundreds of tokens'
-// log-probabilities add up in a margin.
+// log-probabilities add up in a margin.  (A mean: a row of a few equal scores, whose exponentials are
+// exact, is put off by up to that much.)
 __device__ __forceinline__ LogP log_p(const SoftRef& ref, float x, float sum, float temperature, float inv_t) {
     constexpr float kHigh = 2839.f / 4096.f, kLow = (float)(0.693147180559945309417 - 2839.0 / 4096.0);
     // x - m = d + d_low, d / T = q + q_low

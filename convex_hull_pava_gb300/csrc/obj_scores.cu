@@ -13,7 +13,6 @@
 #include "obj_launch.h"
 
 #include <type_traits>
-#define MINB 3
 
 namespace isodev {
 
@@ -70,7 +69,8 @@ __device__ __forceinline__ PolicyRow policy_row(const PolicyArgs& p, LogP logp, 
     return q;
 }
 
-// The gradient of a row: h exp(...) throughout, and g more at the label.
+// The gradient of a row: h exp(...) throughout, and g more at the label; h = -g / s by __fdividef (2
+// units in the last place, beside ex2's; s is far from where that instruction gives 0).
 template <class T>
 struct RowGrad {
     float g, h;
@@ -180,9 +180,9 @@ __device__ __forceinline__ void unlabelled_row(const RowOuts& o, int64_t r) {
 // read once.  A thread reads only what it has copied, so the one thing that a team shares is the
 // row's (maximum, sum); the warps of a cluster write theirs to every CTA and meet once a row.
 // LONG: rows longer than the team's registers are read twice, the second time from L2.
-// Bound by HBM where rows are long (8,192 x 131,072 bf16, 3.65 GB: 602 us, 6.1 TB/s; 8,192 x 65,536:
+// Bound by HBM where rows are long (8,192 x 131,072 bf16, 3.65 GB: 605 us, 6.0 TB/s; 8,192 x 65,536:
 // 321 us, 6.4 TB/s), by a row's chain of steps where its stretch is short: a turn of a 50 KB stretch
-// takes 6.3 us with two CTAs an SM, of which the exponentials are a third (2,047 x 50,021: 84 us,
+// takes 6.3 us with two CTAs an SM, of which the exponentials are a third (2,047 x 50,021: 85 us,
 // 4.5 TB/s).  Registers hold the row because shared memory holds the next one: together they keep
 // 256 KB an SM on the chip.  16 words a thread and not 8: what a row costs each warp beside its
 // words, some 600 instructions, is then half as much a score (21.6 instructions a score became 13.4).

@@ -424,3 +424,20 @@ def test_router_of_many_experts_in_a_graph(cuda_ok):
     graph.replay()
     want = obj.iso_balance_loss(x, 4)
     assert torch.equal(r.loss, want.loss) and torch.equal(r.experts, want.experts) and torch.equal(r.counts, want.counts)
+
+
+@pytest.mark.parametrize("n", [5, 1000, 50021])
+def test_one_row_without_a_rows_dimension(cuda_ok, n):
+    """Scores [n] with a label of no dimension: as the one row [1, n]."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    x, xw, labels, rng = make(1, n, "bf16", seed=n)
+    li, one = ids(labels), put(np.ones(1))
+    lp, norm, st = obj.iso_token_logp(x[0], li[0])
+    assert lp.shape == () and torch.equal(lp, obj.iso_token_logp(x, li)[0][0])
+    d = obj.iso_token_logp_backward(one[0], x[0], li[0], norm)
+    assert d.shape == (n,) and torch.equal(d, obj.iso_token_logp_backward(one, x, li, norm)[0])
+    r, want = obj.iso_policy_loss(x[0], li[0], lp, one[0]), obj.iso_policy_loss(x, li, lp[None], one)
+    assert r.coef.shape == () and torch.equal(r.dlogits, want.dlogits[0]) and torch.equal(r.loss, want.loss)
+    r, want = obj.iso_preference_loss(x[0], li[0], ids([0, 1, 1])), obj.iso_preference_loss(x, li, ids([0, 1, 1]))
+    assert torch.equal(r.dlogits, want.dlogits[0]) and torch.equal(r.loss, want.loss)
