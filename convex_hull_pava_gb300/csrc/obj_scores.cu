@@ -744,6 +744,10 @@ __global__ void zero_kernel(float* a, int na, float* b, int nb) {
     if ((int)threadIdx.x < nb) b[threadIdx.x] = 0.f;
 }
 
+// CTAs an SM of the kernel below: one wave of them, since each looks through all offsets (4,096 pairs of
+// single tokens 43 us, with as many CTAs as pairs up to 1,024 47; without looking 43).
+constexpr int kPairCtas = 3;
+
 // Whether pair q's own offsets are in order and within the rows; o: its three offsets.
 __device__ __forceinline__ bool pair_in_order(const int64_t* offsets, int64_t q, int64_t rows, int64_t (&o)[3]) {
     for (int i = 0; i < 3; ++i) o[i] = offsets[2 * q + i];
@@ -756,7 +760,7 @@ __device__ __forceinline__ bool pair_in_order(const int64_t* offsets, int64_t q,
 // out of order too (in order throughout, pairs share none; every CTA looks through all offsets, before
 // the log-probabilities are there).  Bound by latency: 3.2 us after the log-probabilities' end for
 // 16 pairs of 300 tokens (in float64, and adding up the loss itself, it was 12.5).
-__global__ void __launch_bounds__(512)
+__global__ void __launch_bounds__(512, kPairCtas)
 preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
                         const float* logp, float* coef) {
     constexpr int W = 16;
@@ -764,11 +768,9 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
     __shared__ float sh_coef[2];
     let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, side = threadIdx.x >> 8, tt = threadIdx.x & 255;
-    bool off = false;
-    for (int64_t q = threadIdx.x; q < p.pairs; q += 512) {
-        int64_t o[3];
-        off |= !pair_in_order(p.offsets, q, rows, o);
-    }
+    bool off = threadIdx.x == 0 && (p.offsets[0] < 0 || p.offsets[2 * p.pairs] > rows);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < 2 * p.pairs; i += 512) off |= p.offsets[i] > p.offsets[i + 1];
     const bool disorder = __syncthreads_or(off);
     bool waited = false;
     for (int64_t q = blockIdx.x; q < p.pairs; q += gridDim.x) {
@@ -1063,7 +1065,7 @@ cudaError_t preference_loss(int dtype, const ScoreRows& s, PreferenceArgs p, flo
         e = cudaGetLastError();
     } else {
         p.sum_later = out && s.rows > 0;
-        ClusterLaunch l(std::min<int64_t>(p.pairs, 1024), 512, 0, 1, true, st);
+        ClusterLaunch l(std::min<int64_t>(p.pairs, kPairCtas * device_sms()), 512, 0, 1, true, st);
         e = l(preference_pairs_kernel, p, s.labels, s.rows, logp, coef);
         prof_mark(st, "preference_pairs");
     }
