@@ -756,9 +756,9 @@ __device__ __forceinline__ bool pair_in_order(const int64_t* offsets, int64_t q,
 
 // One CTA per pair, half of it for each of the two sequences: their sums, the pair's loss and the
 // coefficient of every labelled token.  Each row's coefficient has one writer: a pair out of order
-// writes none, and where some pair is, one that shares rows with an earlier pair in order counts as
-// out of order too (in order throughout, pairs share none; every CTA looks through all offsets, before
-// the log-probabilities are there).  Bound by latency: 3.2 us after the log-probabilities' end for
+// writes none, and where some pair is, one that starts before the end of an earlier pair in order
+// counts as out of order too (in order throughout, pairs share no rows; every CTA looks through all
+// offsets, before the log-probabilities are there, and at most once more).  Bound by latency: 3.2 us after the log-probabilities' end for
 // 16 pairs of 300 tokens (in float64, and adding up the loss itself, it was 12.5).
 __global__ void __launch_bounds__(512, kPairCtas)
 preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
@@ -766,6 +766,7 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
     constexpr int W = 16;
     __shared__ Sum sh[3][W];
     __shared__ float sh_coef[2];
+    __shared__ int sh_end[W];
     let_next_start();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, side = threadIdx.x >> 8, tt = threadIdx.x & 255;
     bool off = threadIdx.x == 0 && (p.offsets[0] < 0 || p.offsets[2 * p.pairs] > rows);
@@ -773,16 +774,21 @@ preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, in
     for (int64_t i = threadIdx.x; i < 2 * p.pairs; i += 512) off |= p.offsets[i] > p.offsets[i + 1];
     const bool disorder = __syncthreads_or(off);
     bool waited = false;
+    int64_t looked = 0;  // pairs that `end` has taken in: this thread's part of the largest end of one in order
+    int end = 0;
     for (int64_t q = blockIdx.x; q < p.pairs; q += gridDim.x) {
         int64_t o[3];
         bool bad = !pair_in_order(p.offsets, q, rows, o);
         if (disorder) {
-            bool shares = false;
-            for (int64_t e = threadIdx.x; e < q; e += 512) {
+            for (int64_t e = looked + threadIdx.x; e < q; e += 512) {
                 int64_t before[3];
-                shares |= pair_in_order(p.offsets, e, rows, before) && max(before[0], o[0]) < min(before[2], o[2]);
+                if (pair_in_order(p.offsets, e, rows, before) && before[0] < before[2]) end = max(end, (int)before[2]);
             }
-            bad |= (bool)__syncthreads_or(shares);
+            looked = q;
+            const int most = __reduce_max_sync(~0u, end);
+            if (lane == 0) sh_end[warp] = most;
+            __syncthreads();  // (read before the next one, written behind it)
+            bad |= o[0] < o[2] && o[0] < __reduce_max_sync(~0u, sh_end[lane & (W - 1)]);
         }
         const bool ok = !bad;
         const int64_t a = side ? o[1] : o[0], b = side ? o[2] : o[1];

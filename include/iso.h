@@ -414,10 +414,10 @@ iso_status iso_policy_loss(const void *logits, int dtype, int64_t rows, int64_t 
  *   loss = mean over the pairs.
  *
  *  offsets    [2 pairs + 1] int64, not read by the host.  A pair with offsets
- *             out of order or out of [0, rows], or that shares rows with an earlier
- *             pair in order, gets ISO_ROW_BAD_SHAPE in pair_status, a margin and
- *             sums of NaN, and adds nothing to a gradient; the loss is NaN.  Rows of
- *             no other sequence get a gradient of 0.
+ *             out of order or out of [0, rows], or that has rows and starts before
+ *             the end of an earlier such pair in order, gets ISO_ROW_BAD_SHAPE in
+ *             pair_status, a margin and sums of NaN, and adds nothing to a gradient;
+ *             the loss is NaN.  Rows of no other sequence get a gradient of 0.
  *  ref_logp   [rows], or NULL: R = 0.
  *  loss       one float, written (0 for no pairs).
  *  margins    [pairs], written: z.       seq_logp [2 pairs], written: S.

@@ -43,7 +43,9 @@ def test_preference_gradient_over_the_scores(cuda_ok, rows, n, dtype):
 @pytest.mark.parametrize("offsets,status,as_if", [
     ([0, 6, 3, 6, 9], [4, 0], [3, 3, 3, 6, 9]),                     # a pair out of order over a good one's rows
     ([0, 3, 6, 9, 3, 5, 9], [0, 4, 4], [0, 3, 6, 6, 6, 6, 6]),      # two in order about one that is not
-    ([5, 2, 5, 7, 9, 1 << 40, 0, 3, 5], [4, 0, 4, 0], [0, 0, 0, 3, 5, 5, 5, 7, 9]),
+    ([5, 2, 5, 7, 9, 1 << 40, 0, 3, 5], [4, 0, 4, 4], [5, 5, 5, 7, 9, 9, 9, 9, 9]),   # the last starts before the second
+    ([9, 9, 9, 3, 3, 6, 9], [0, 4, 0], [3, 3, 3, 3, 3, 6, 9]),      # an empty one holds no rows
+    ([0, 3, 6, 9, 4, 4, 4], [0, 4, 0], [0, 3, 6, 6, 6, 6, 6]),
     ([0, 3, 6, 9, 6, 6, 6, 8, 12], [0, 4, 0, 0], [0, 3, 6, 6, 6, 6, 6, 8, 12]),
 ])
 def test_pairs_that_share_rows(cuda_ok, offsets, status, as_if):
@@ -61,6 +63,40 @@ def test_pairs_that_share_rows(cuda_ok, offsets, status, as_if):
         assert r.margins.isnan().tolist() == [s != 0 for s in status] and bool(r.loss.isnan())
         assert r.seq_logp.isnan().tolist() == [s != 0 for s in status for _ in range(2)]
         assert torch.equal(r.coef, want.coef) and torch.equal(r.dlogits, want.dlogits)
+
+
+def test_many_pairs_out_of_order(cuda_ok):
+    """More pairs than the GPU takes at once, of which some are out of order: whatever CTA has a pair, it
+    knows the rows before it."""
+    import torch
+    from convex_hull_pava_gb300 import objectives as obj
+    rng = np.random.default_rng(9)
+    pairs, rows = 3000, 9000
+    off = np.sort(rng.integers(0, rows + 1, 2 * pairs + 1))
+    off[rng.integers(0, 2 * pairs, 300)] += rng.integers(-12, 13, 300)
+    off[77], off[5000] = -5, rows + 1
+    x, xw, labels, _ = make(rows, 20, "f32", 6)
+    status, last = [], 0
+    for q in range(pairs):
+        a, b, c = off[2 * q:2 * q + 3]
+        order = 0 <= a <= b <= c <= rows
+        status.append(0 if order and (a == c or a >= last) else 4)
+        if order and a < c:
+            last = max(last, c)
+    r = obj.iso_preference_loss(x, ids(labels), ids(off), beta=0.5)
+    assert r.pair_status.tolist() == status and 10 < np.count_nonzero(status) < pairs
+    assert torch.equal(r.margins.isnan().cpu(), torch.tensor(status) != 0) and bool(r.loss.isnan())
+    # the coefficients that are left: each row's of the pair that holds it
+    want = np.zeros(rows)
+    lp = ref.token_logp(xw, labels)
+    for q in np.flatnonzero(np.array(status) == 0):
+        a, b, c = off[2 * q:2 * q + 3]
+        z = 0.5 * (lp[a:b].sum() - lp[b:c].sum())
+        slope = -0.5 / (1 + np.exp(z)) / pairs
+        want[a:b], want[b:c] = slope, -slope
+    want[labels < 0] = 0
+    # a margin is beta times its tokens' log-probabilities (at most 40), a coefficient's slope in it beta / 4
+    assert np.abs(wide(r.coef) - want).max() <= (0.5 / 4 * 0.5 * 40 * lp_tol(lp).max() + 1e-6) / pairs
 
 
 def test_many_pairs(cuda_ok):
