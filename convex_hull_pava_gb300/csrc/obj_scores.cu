@@ -758,8 +758,9 @@ __device__ __forceinline__ bool pair_in_order(const int64_t* offsets, int64_t q,
 // coefficient of every labelled token.  Each row's coefficient has one writer: a pair out of order
 // writes none, and where some pair is, one that starts before the end of an earlier pair in order
 // counts as out of order too (in order throughout, pairs share no rows; every CTA looks through all
-// offsets, before the log-probabilities are there, and at most once more).  Bound by latency: 3.2 us after the log-probabilities' end for
-// 16 pairs of 300 tokens (in float64, and adding up the loss itself, it was 12.5).
+// offsets, before the log-probabilities are there, and at most once more).  Bound by latency: 3.2 us
+// after the log-probabilities' end for 16 pairs of 300 tokens (in float64, and adding up the loss
+// itself, it was 12.5).
 __global__ void __launch_bounds__(512, kPairCtas)
 preference_pairs_kernel(PreferenceArgs p, const int64_t* __restrict__ labels, int64_t rows,
                         const float* logp, float* coef) {
