@@ -21,7 +21,8 @@ Entry points (same names as the C ABI):
 
 :mod:`.soft_rank` holds the differentiable soft rank, :mod:`.objectives` the
 training objectives (token log-probabilities, policy, preference and balance
-losses).
+losses), :mod:`.choices` the choices over rows of scores (a router's experts, beam
+search's continuations) and the states that follow them.
 """
 from __future__ import annotations
 
@@ -51,7 +52,9 @@ EXPORTS = ("iso_version", "iso_status_string", "iso_fit_workspace_bytes", "iso_f
            "iso_token_logp_backward",
            "iso_policy_loss_workspace_bytes", "iso_policy_loss",
            "iso_preference_loss_workspace_bytes", "iso_preference_loss",
-           "iso_balance_loss_workspace_bytes", "iso_balance_loss", "iso_balance_loss_backward")
+           "iso_balance_loss_workspace_bytes", "iso_balance_loss", "iso_balance_loss_backward",
+           "iso_route", "iso_route_backward", "iso_beam_choose_workspace_bytes",
+           "iso_beam_choose", "iso_beam_reorder")
 
 _lib = None
 _lock = threading.Lock()
@@ -132,6 +135,15 @@ def load_library(path: str | None = None):
             getattr(lib, f"iso_{name}_loss_workspace_bytes").restype = sz
             getattr(lib, f"iso_{name}_loss").restype = ci
         for name in ("iso_token_logp", "iso_token_logp_backward", "iso_balance_loss_backward"):
+            getattr(lib, name).restype = ci
+        lib.iso_route.argtypes = scores + [ci, vp, vp] + [ci] * 5 + [cf] + [vp] * 4
+        lib.iso_route_backward.argtypes = scores + [ci, ci, ci, cf] + [vp] * 4 + [i64, vp]
+        lib.iso_beam_choose_workspace_bytes.argtypes = [i64, i64, i64, ci, ci]
+        lib.iso_beam_choose_workspace_bytes.restype = sz
+        lib.iso_beam_choose.argtypes = [vp, ci] + [i64] * 4 + [vp, vp, i64, ctypes.c_double, ci,
+                                                              vp, vp, vp, vp, sz, vp, vp]
+        lib.iso_beam_reorder.argtypes = [vp, i64, i64, i64, vp, vp]
+        for name in ("iso_route", "iso_route_backward", "iso_beam_choose", "iso_beam_reorder"):
             getattr(lib, name).restype = ci
         _lib = lib
         return lib

@@ -486,6 +486,121 @@ iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t toke
                                      float grad_loss, const float *grad_loss_dev, void *dlogits,
                                      int64_t out_stride, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Choices over rows of scores, and the states that follow them.
+ *
+ * Beside the objectives: the experts that a router gives its tokens to, the
+ * continuations that beam search keeps (the answers of preference pairs), and
+ * the states of the beams that they continue.
+ *
+ * Conventions, beside those of the objectives (types, strides and limits of the
+ * scores are theirs):
+ *  - A choice is that of the exact values: where rounding could change an order,
+ *    the values are formed again with about 2^-50 (route) or 2^-36 (beams) of
+ *    relative error.  Equal values go to the lowest index (beam first, then token).
+ *  - A score of -inf is closed and never chosen, nor is a NaN.  Places for which
+ *    nothing is left hold -1.
+ *  - Results do not depend on timing: the same call gives the same bits.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * iso_route -- a router's choice of top_k experts for each token.  With x a
+ * token's scores,
+ *
+ *   s_e = exp(x_e) / sum_f exp(x_f)  (score 0)   or   1 / (1 + exp(-x_e))  (score 1)
+ *   c_e = s_e + bias_e
+ *   chosen: the top_k largest c of the open experts (of the groups that stay)
+ *   gate_i = scale s_i   or, renormalize = 1,   scale s_i / sum_j s_j   (j: the chosen)
+ *
+ *  logits     [tokens, experts] of dtype, row t at element t * stride;
+ *             1 <= experts <= ISO_MAX_EXPERTS.
+ *  top_k      1 <= top_k <= ISO_MAX_TOP_K, and not more than the experts of top_groups groups.
+ *  mask       [tokens] uint8, or NULL: 0 marks a token that takes no part.
+ *  bias       [experts] float32, or NULL: 0.  It moves the choice, not the gates.  -inf or NaN
+ *             closes an expert to all tokens.
+ *  groups     1 <= groups <= ISO_MAX_GROUPS, a divisor of experts: experts g * size .. (g + 1) * size - 1
+ *             are group g.  A group's score is the sum of its group_best (1 or 2) largest c of
+ *             open experts (of one, where only one is open); the top_groups groups of the
+ *             largest scores stay.  groups = 1: group_best is not used.
+ *  scale      finite and above 0.
+ *  counts     [experts] int64, written: the tokens that chose each expert.
+ *  chosen     [tokens, top_k] int32, written: the experts by decreasing c; -1 where no open
+ *             expert is left or the token takes no part.
+ *  gates      [tokens, top_k] float32, written: 0 where chosen is -1.
+ *             With score 0, a NaN or +inf among the scores of a token makes its gates and its
+ *             gradient NaN; its experts are then the open ones by bias and index (c = bias_e).
+ *             With score 1 a NaN closes its own expert only.
+ *
+ * iso_route_backward -- the gradient of sum grad_gates * gates in the scores (counts, choice and
+ * bias carry none).
+ *
+ *  chosen, gates  as the forward wrote them for the same logits.
+ *  grad_gates     [tokens, top_k] float32.
+ *  dlogits        [tokens, experts] of dtype, row t at t * out_stride, written; it may be the
+ *                 logits themselves (out_stride == stride).
+ */
+#define ISO_MAX_GROUPS 32
+#define ISO_ROUTE_SOFTMAX 0
+#define ISO_ROUTE_SIGMOID 1
+iso_status iso_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride,
+                     int top_k, const uint8_t *mask, const float *bias, int score, int groups,
+                     int top_groups, int group_best, int renormalize, float scale, int64_t *counts,
+                     int32_t *chosen, float *gates, void *stream);
+iso_status iso_route_backward(const void *logits, int dtype, int64_t tokens, int64_t experts,
+                              int64_t stride, int top_k, int score, int renormalize, float scale,
+                              const int32_t *chosen, const float *gates, const float *grad_gates,
+                              void *dlogits, int64_t out_stride, void *stream);
+
+/*
+ * iso_beam_choose -- a step of beam search: of all continuations of a batch item's beams, the
+ * `keep` of the largest
+ *
+ *   total(b, v) = scores_b + x_v / T - log sum_u exp(x_u / T)
+ *
+ * over its beams b and tokens v, with x the beam's row of scores.  A beam that is done offers
+ * one continuation only, the token `end` at total = scores_b, and its row is not read.
+ *
+ *  logits     [batch * beams, n] of dtype, row (item * beams + b) at that times stride;
+ *             1 <= beams <= ISO_MAX_BEAMS, batch * beams <= 2^31 - 1.
+ *  scores     [batch, beams] float32.  A beam whose score is not finite offers nothing, and its
+ *             row is not read.
+ *  done       [batch, beams] uint8, or NULL: none is done.
+ *  end        0 <= end < n (not used where done is NULL).
+ *  temperature  T: finite, above 0, 1 / T and log2(e) / T in float32's range.
+ *  keep       1 <= keep <= ISO_MAX_KEEP.
+ *  out_scores [batch, keep] float32, written: the totals in decreasing order; -inf where nothing is left.
+ *  parents    [batch, keep] int32, written: the beam of each.    tokens [batch, keep] int64, written.
+ *  workspace  iso_beam_choose_workspace_bytes(...) bytes, 256-byte aligned.
+ *  row_status [batch * beams] uint32, written, or NULL: ISO_ROW_BAD_Y for a row with a NaN or
+ *             +inf, or with nothing but -inf: its beam offers nothing.
+ */
+#define ISO_MAX_BEAMS 32
+#define ISO_MAX_KEEP 64
+size_t iso_beam_choose_workspace_bytes(int64_t batch, int64_t beams, int64_t n, int dtype, int keep);
+iso_status iso_beam_choose(const void *logits, int dtype, int64_t batch, int64_t beams, int64_t n,
+                           int64_t stride, const float *scores, const uint8_t *done, int64_t end,
+                           double temperature, int keep, float *out_scores, int32_t *parents,
+                           int64_t *tokens, void *workspace, size_t workspace_bytes,
+                           uint32_t *row_status, void *stream);
+
+/*
+ * iso_beam_reorder -- the states of beams put, in place, where their continuations are: in each
+ * state, row (item * beams + b) becomes what row (item * beams + parents[item, b]) was.  Rows of beams
+ * that keep their own state (parents[item, b] == b) are neither read for themselves nor written.
+ *
+ *  states     `count` descriptions, read by the host during the call: `base`, and in bytes:
+ *             row r is `runs` runs of `run_bytes`, the first at base + r * row_stride, then one
+ *             each run_stride.  Rows and runs may not overlap, nor may states.
+ *  batch * beams <= 2^31 - 1; 1 <= beams <= ISO_MAX_BEAMS.
+ *  parents    [batch, beams] int32 on the device.  A parent out of [0, beams) leaves its row as it is.
+ */
+typedef struct {
+    void *base;
+    int64_t row_stride, runs, run_stride, run_bytes;
+} iso_state;
+iso_status iso_beam_reorder(const iso_state *states, int64_t count, int64_t batch, int64_t beams,
+                            const int32_t *parents, void *stream);
+
 /*
  * Optional per-kernel timing for benchmarks (not part of the fit).
  * iso_profile_enable(1) makes the library create a few CUDA events (once, on
