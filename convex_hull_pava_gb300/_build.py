@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libiso.so")
 SOURCES = ("iso_api.cu", "iso_rows.cu", "iso_rows_f64.cu", "iso_long.cu", "iso_long_f64.cu",
            "iso_backward.cu", "iso_noalloc.cu", "iso_ragged.cu",
            "obj_api.cu", "obj_scores.cu", "obj_balance.cu",
-           "choice_api.cu", "choice_route.cu", "choice_beam.cu", "choice_reorder.cu")
+           "choice_api.cu", "choice_route.cu", "choice_route_bf16.cu", "choice_route_f16.cu",
+           "choice_beam.cu", "choice_reorder.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-Xptxas", "-warn-spills"]
