@@ -8,65 +8,131 @@ extern template cudaError_t route_rows<__half>(const RouteArgs&, int64_t*, int32
 
 namespace {
 
-// The gates' part of each gradient element is put together in shared memory, a warp's tokens beside one
-// another.  DENSE: softmax without renormalisation, whose gradient has all elements; otherwise only
-// the chosen ones' scores are read.
-template <class T, int G, int EPL, bool DENSE>
+// Softmax without renormalisation: all elements have a gradient.  The gates' part of each is put together in
+// shared memory, a warp's tokens beside one another; the next tokens' scores are on their way meanwhile.
+template <class T, int G, int EPL>
 __global__ void __launch_bounds__(256)
-route_backward_kernel(RouteArgs a, int whole, const int32_t* chosen, const float* gates, const float* grad_gates,
-                      T* out, int64_t out_stride) {
+route_dense_backward_kernel(RouteArgs a, int whole, const int32_t* chosen, const float* gates, const float* grad_gates,
+                            T* out, int64_t out_stride) {
     constexpr int W = 256 / 32, TPW = 32 / G;
     __shared__ __align__(16) float extra[W * TPW][G * EPL];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane & (G - 1), E = a.experts, k = a.top_k;
+    const unsigned group = group_lanes<G>();
     float* const mine = extra[warp * TPW + lane / G];
     for (int e = gl; e < G * EPL; e += G) mine[e] = 0.f;
     __syncwarp();
     const int64_t step = (int64_t)gridDim.x * W * TPW;
     const T* const base = static_cast<const T*>(a.x);
-    for (int64_t first = ((int64_t)blockIdx.x * W + warp) * TPW; first < a.tokens; first += step) {
+    TokenRow<T, G, EPL> row;
+    int slot = -1;
+    float g = 0.f, gate = 0.f;
+    bool on = false;
+    auto fetch = [&](int64_t t) {
+        on = t < a.tokens;
+        slot = -1;
+        if (!on) return;
+        row.load(base + t * a.stride, gl, E, whole);
+        if (gl < k) {
+            slot = chosen[t * k + gl];
+            gate = gates[t * k + gl];
+            g = grad_gates[t * k + gl];
+        }
+    };
+    int64_t first = ((int64_t)blockIdx.x * W + warp) * TPW;
+    fetch(first + lane / G);
+    for (; first < a.tokens; first += step) {
         const int64_t t = first + lane / G;
-        const bool on = t < a.tokens;
-        TokenRow<T, G, EPL> row;
-        int slot = -1;
-        float g = 0.f, gate = 0.f, x = 0.f;
-        if (on) {
-            if (DENSE) row.load(base + t * a.stride, gl, E, whole);
-            if (gl < k) {
-                slot = chosen[t * k + gl];
-                gate = gates[t * k + gl];
-                g = grad_gates[t * k + gl];
-            }
-        }
-        const bool has = slot >= 0 && slot < E;
-        if (!DENSE && has && a.score == ISO_ROUTE_SIGMOID) x = to_f32(base[t * a.stride + slot]);
-        const unsigned group = group_lanes<G>();
+        float v[EPL], p[EPL];
+        row.scores(v, on);
+        const int at = slot;
+        const bool has = at >= 0 && at < E, write = on;
+        const float dot = group_add<G>(has ? gate * g : 0.f), put = a.scale * g;
+        fetch(t + step);
+        if (has) mine[at] = put;
+        __syncwarp();
         const bool any = __ballot_sync(~0u, has) & group;
-        const bool bad = __ballot_sync(~0u, has && gate != gate) & group;
-        const float dot = group_add<G>(has ? gate * g : 0.f);
-        float put;
-        if (DENSE) {
-            put = a.scale * g;
-        } else {
-            put = gate * (a.renormalize ? g - dot / a.scale : g);
-            if (a.score == ISO_ROUTE_SIGMOID) put *= 1.f / (1.f + expf(x));  // 1 - s
-        }
-        if (has) mine[slot] = put;
-        __syncwarp();
+        const SoftState st = token_softmax<G, EPL>(v, p);
+        const float inv = 1.f / st.s;
         TokenRow<T, G, EPL> d;
-        if (DENSE) {
-            float v[EPL], p[EPL];
-            row.scores(v, on);
-            const SoftState st = token_softmax<G, EPL>(v, p);
-            const float inv = 1.f / st.s;
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) d.v[i] = from_f32<T>(any ? p[i] * inv * (mine[row.expert(gl, i)] - dot) : 0.f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPL; ++i) d.v[i] = from_f32<T>(bad && a.score == ISO_ROUTE_SOFTMAX ? NAN : mine[row.expert(gl, i)]);
-        }
-        if (on) d.store(out + t * out_stride, gl, E, whole);
+        for (int i = 0; i < EPL; ++i) d.v[i] = from_f32<T>(any ? p[i] * inv * (mine[row.expert(gl, i)] - dot) : 0.f);
+        if (write) d.store(out + t * out_stride, gl, E, whole);
         __syncwarp();
-        if (has) mine[slot] = 0.f;
+        if (has) mine[at] = 0.f;
+    }
+}
+
+// The others: the chosen alone have a gradient.  A warp has as many tokens at a time as its lanes have
+// places (`places` lanes a token, a power of two); their rows, zero but for the chosen, lie in shared memory
+// in the output's type and are stored from there, 16 bytes a lane.  The next tokens' choice is asked
+// for one turn ahead, and its scores as soon as that is there.  `chunk`: bytes of a store.
+template <class T>
+__global__ void __launch_bounds__(256)
+route_sparse_backward_kernel(RouteArgs a, int places, int tokens, int chunk, const int32_t* chosen, const float* gates,
+                             const float* grad_gates, T* out, int64_t out_stride) {
+    extern __shared__ __align__(16) char rows[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts, k = a.top_k;
+    const int place = lane & (places - 1), tw = lane / places;
+    const int pitch = (E * (int)sizeof(T) + 15) / 16 * 16;  // bytes of a row in shared memory
+    char* const mine = rows + warp * tokens * pitch;
+    for (int i = lane * 16; i < tokens * pitch; i += 512) *reinterpret_cast<uint4*>(mine + i) = uint4{0, 0, 0, 0};
+    const T* const base = static_cast<const T*>(a.x);
+    const bool sigmoid = a.score == ISO_ROUTE_SIGMOID;
+    const int64_t step = (int64_t)gridDim.x * 8 * tokens;
+    int slot = -1;
+    float gate = 0.f, g = 0.f, x = 0.f;
+    auto fetch = [&](int64_t first) {
+        const int64_t t = first + tw;
+        slot = -1;
+        if (tw < tokens && place < k && t < a.tokens) {
+            slot = chosen[t * k + place];
+            gate = gates[t * k + place];
+            g = grad_gates[t * k + place];
+            if (slot < 0 || slot >= E) slot = -1;
+        }
+    };
+    auto score = [&](int64_t first) {
+        if (sigmoid && slot >= 0) x = to_f32(base[(first + tw) * a.stride + slot]);
+    };
+    int64_t first = ((int64_t)blockIdx.x * 8 + warp) * tokens;
+    fetch(first);
+    score(first);
+    __syncwarp();
+    for (; first < a.tokens; first += step) {
+        const int at = slot;
+        const float own = gate, of = g, own_x = x;
+        fetch(first + step);
+        float dot = at >= 0 ? own * of : 0.f;
+        for (int o = places / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+        float put = own * (a.renormalize ? of - dot / a.scale : of);
+        if (sigmoid) put *= 1.f / (1.f + expf(own_x));  // 1 - s
+        T* const row = reinterpret_cast<T*>(mine + tw * pitch);
+        if (at >= 0) row[at] = from_f32<T>(put);
+        // without probabilities nothing has a gradient
+        unsigned bad = __ballot_sync(~0u, at >= 0 && own != own);
+        if (sigmoid) bad = 0u;
+        __syncwarp();
+        const int live = (int)min((int64_t)tokens, a.tokens - first);
+        const int chunks = E * (int)sizeof(T) / chunk;  // of a row
+        if (chunk == 16) {
+            for (int r = lane / chunks, c = lane % chunks; r < live;) {
+                store_streaming(reinterpret_cast<char*>(out + (first + r) * out_stride) + c * 16,
+                                *reinterpret_cast<const uint4*>(mine + r * pitch + c * 16));
+                for (c += 32; c >= chunks; c -= chunks) ++r;
+            }
+        } else {
+            for (int r = 0; r < live; ++r)
+                for (int e = lane; e < E; e += 32)
+                    out[(first + r) * out_stride + e] = reinterpret_cast<const T*>(mine + r * pitch)[e];
+        }
+        __syncwarp();
+        if (bad) {
+            for (int r = 0; r < live; ++r)
+                if (bad >> (r * places) & (places == 32 ? ~0u : (1u << places) - 1u))
+                    for (int e = lane; e < E; e += 32) out[(first + r) * out_stride + e] = from_f32<T>(NAN);
+        }
+        if (at >= 0) row[at] = from_f32<T>(0.f);
+        score(first + step);
         __syncwarp();
     }
 }
@@ -80,19 +146,30 @@ cudaError_t route(int dtype, const RouteArgs& a, int64_t* counts, int32_t* chose
 cudaError_t route_backward(int dtype, const RouteArgs& a, const int32_t* chosen, const float* gates,
                            const float* grad_gates, void* out, int64_t out_stride, cudaStream_t st) {
     return by_type(dtype, [&](auto t) {
-        return by_experts(a.experts, [&](auto g, auto epl) {
-            using T = decltype(t);
-            constexpr int G = decltype(g)::value, EPL = decltype(epl)::value, CH = TokenRow<T, G, EPL>::CH;
-            const bool dense = a.score == ISO_ROUTE_SOFTMAX && !a.renormalize;
-            const int whole = (!dense || chunks_fit(a.x, a.tokens, a.stride, a.experts, CH, sizeof(T))) &&
-                              chunks_fit(out, a.tokens, out_stride, a.experts, CH, sizeof(T));
-            const int64_t grid = std::min<int64_t>((a.tokens + 256 / G - 1) / (256 / G), 152 * 4);
-            auto kernel = dense ? route_backward_kernel<T, G, EPL, true> : route_backward_kernel<T, G, EPL, false>;
-            kernel<<<(unsigned)grid, 256, 0, st>>>(a, whole, chosen, gates, grad_gates, static_cast<T*>(out), out_stride);
-            const cudaError_t e = cudaGetLastError();
-            prof_mark(st, "route_backward");
-            return e;
-        });
+        using T = decltype(t);
+        constexpr int N = Word<T>::N;
+        T* const to = static_cast<T*>(out);
+        if (a.score == ISO_ROUTE_SOFTMAX && !a.renormalize)
+            return by_experts(a.experts, [&](auto g, auto epl) {
+                constexpr int G = decltype(g)::value, EPL = decltype(epl)::value, CH = TokenRow<T, G, EPL>::CH;
+                const int whole = chunks_fit(a.x, a.tokens, a.stride, a.experts, CH, sizeof(T)) &&
+                                  chunks_fit(out, a.tokens, out_stride, a.experts, CH, sizeof(T));
+                const int64_t grid = std::min<int64_t>((a.tokens + 256 / G - 1) / (256 / G), 152 * 4);
+                route_dense_backward_kernel<T, G, EPL><<<(unsigned)grid, 256, 0, st>>>(a, whole, chosen, gates, grad_gates, to, out_stride);
+                const cudaError_t e = cudaGetLastError();
+                prof_mark(st, "route_backward");
+                return e;
+            });
+        int places = 1;
+        while (places < a.top_k) places *= 2;
+        const int pitch = (a.experts * (int)sizeof(T) + 15) / 16 * 16;
+        const int tokens = std::max(1, std::min(32 / places, 4096 / pitch));  // of a warp at a time: up to 4 KB
+        const int chunk = chunks_fit(out, a.tokens, out_stride, a.experts, N, sizeof(T)) ? 16 : (int)sizeof(T);
+        const int64_t grid = std::min<int64_t>((a.tokens + 8 * tokens - 1) / (8 * tokens), 152 * 6);
+        route_sparse_backward_kernel<T><<<(unsigned)grid, 256, 8 * tokens * pitch, st>>>(a, places, tokens, chunk, chosen, gates, grad_gates, to, out_stride);
+        const cudaError_t e = cudaGetLastError();
+        prof_mark(st, "route_backward");
+        return e;
     });
 }
 

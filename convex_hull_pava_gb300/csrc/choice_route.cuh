@@ -141,11 +141,40 @@ __device__ __forceinline__ float rcp(float v) {
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+    float r;
+    asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // NaN if one is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+template <int K>
+__device__ __forceinline__ float max_nan(const float (&v)[K]) {
+    float top = v[0];
+#pragma unroll
+    for (int i = 1; i + 1 < K; i += 2) top = max_nan(top, v[i], v[i + 1]);
+    return K % 2 ? top : max_nan(top, v[K - 1]);
+}
+template <int K>
+__device__ __forceinline__ float min_of(const float (&v)[K]) {
+    float low = v[0];
+#pragma unroll
+    for (int i = 1; i + 1 < K; i += 2) low = min3(low, v[i], v[i + 1]);
+    return K % 2 ? low : fminf(low, v[K - 1]);
 }
 __device__ __forceinline__ void order(float& a, float& b) {  // a the larger
     const float t = fmaxf(a, b);
@@ -171,56 +200,74 @@ __device__ __forceinline__ void sort8(float (&v)[8]) {
 
 // How far apart two ranked values have to be for their float32 order to be that of the exact
 // ones: twice what one may be off.  Sigmoid: s is off by s (1 - s) times its exponential's error, 2^-22
-// and 2^-24 |x| (s (1 - s) |x| < 0.23), a sum's and a quotient's rounding (2^-24, 2^-23), together under
-// 2.7e-7.  Softmax: p times the exponential's 2^-22, a sum's 15 roundings and a quotient's (1.5e-6),
-// and p |x - m| < 0.37 times 2^-23.  Adding the bias rounds by 2^-24 of the result.
-__device__ __forceinline__ float unsure(int mode, float c, float share) {
-    return (mode == kSigmoid ? 6e-7f : fmaf(fabsf(share), 3.2e-6f, 1e-7f)) + 1.3e-7f * fabsf(c);
+// and 2^-24 |x| (s (1 - s) |x| < 0.23), a sum's, a product's and a quotient's rounding (2 of 2^-24, 2^-23),
+// together under 3.2e-7.  Softmax: p times the exponential's 2^-22, a sum's 15 roundings and a quotient's
+// (1.5e-6), and p |x - m| < 0.37 times 2^-23.  Adding the bias rounds by 2^-24 of the result.
+__device__ __forceinline__ float unsure(bool sigmoid, float c, float share) {
+    return (sigmoid ? 7e-7f : fmaf(fabsf(share), 3.2e-6f, 1e-7f)) + 1.3e-7f * fabsf(c);
+}
+
+// What is ranked, in 64 bits; of softmax with float32's sum (inv its reciprocal, m the largest score).
+__device__ __noinline__ double ranked_value(bool sigmoid, float x, float b, float m, float inv) {
+    return (sigmoid ? 1. / (1. + exp(-(double)x)) : exp((double)x - (double)m) * (double)inv) + (double)b;
 }
 
 constexpr int kFound = 32;  // candidates of a token
+constexpr int kTeamWarps = 6, kTeamThreads = 32 * kTeamWarps;
+template <class T>
+constexpr int team_ctas = sizeof(T) == 4 ? 3 : 4;  // an SM, by shared memory and registers
 
 // Candidates: experts whose ranked value reaches a bound that top_k of them reach, the top_k-th largest of
-// the lanes' 8 partial maxima, which the lanes sort and merge (LIST of them).  VALUES: what is ranked is
-// formed from the scores; otherwise it is the scores themselves, which nothing rounds.  Tokens whose choice float32 does not
-// settle, with NaN or infinities, or with too many candidates are chosen by choose_exact.
+// the lanes' partial maxima (8 a lane), which the lanes sort and merge (LIST of them).  VALUES: what is
+// ranked is formed from the scores; otherwise it is the scores themselves, which nothing rounds.  Where
+// candidates' values or groups' sums are nearer to each other than float32 tells they are formed again in
+// 64 bits; tokens with NaN, without probabilities, with too many candidates, or whose order hangs on
+// the softmax's sum are chosen by choose_exact.
 template <class T, int L, int EPL, bool VALUES, int LIST>
-__global__ void __launch_bounds__(kRouteThreads, 3)
+__global__ void __launch_bounds__(kTeamThreads, team_ctas<T>)
 route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float* gates) {
     constexpr int N = 16 / (int)sizeof(T), TPW = 32 / L, WORDS = EPL / N, LANE = (WORDS | 1) * 16, BIAS = (EPL / 4 | 1) * 4;
     constexpr int PER = EPL / 8;  // experts of a partial maximum
     extern __shared__ __align__(16) char memory[];
     __shared__ uint32_t sh_n[L * EPL];
+    __shared__ int sh_base[L];  // the first expert of a lane
     __shared__ __align__(16) float sh_bias[VALUES ? L * BIAS : 4];
-    __shared__ __align__(16) float found[kRouteWarps][TPW][kFound + 4];
-    __shared__ uint16_t found_at[kRouteWarps][TPW][kFound], first_at[kRouteWarps][TPW][kFound + 1];
-    __shared__ float first[kRouteWarps][TPW][kFound + 1];
+    __shared__ __align__(16) float sh_found[kTeamWarps][TPW][kFound + 4];
+    __shared__ float sh_first[kTeamWarps][TPW][kFound];
+    __shared__ uint16_t sh_found_at[kTeamWarps][TPW][kFound], sh_first_at[kTeamWarps][TPW][kFound];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane & (L - 1), tw = lane / L;
     const int E = a.experts, k = a.top_k;
     const unsigned team = group_lanes<L>();
     char* const stages = memory + warp * 2 * pl.stage;
+    // a token's candidates: values and places (lane EPL + expert of the lane), then those by rank
+    float* const found = sh_found[warp][tw];
+    float* const first = sh_first[warp][tw];
+    uint16_t* const found_at = sh_found_at[warp][tw];
+    uint16_t* const first_at = sh_first_at[warp][tw];
     auto base_of = [&](int l) { return l / pl.per_group * pl.size + l % pl.per_group * pl.sub; };
-    auto held_by = [&](int l) { return min(pl.sub, pl.size - l % pl.per_group * pl.sub); };  // may be negative
+    auto held_by = [&](int l) {
+        return l < a.groups * pl.per_group ? max(0, min(pl.sub, pl.size - l % pl.per_group * pl.sub)) : 0;
+    };
     const bool has_group = gl < a.groups * pl.per_group;
-    const int own_base = base_of(gl), own_count = has_group ? max(0, held_by(gl)) : 0;
+    const int own_count = held_by(gl);
     const bool sigmoid = VALUES && pl.mode == kSigmoid;
     const T closed = from_f32<T>(sigmoid ? 0.f : -INFINITY);  // places without an expert (their bias is -inf)
     auto fill = [&](char* stage) {
         for (int i = own_count; i < EPL; ++i) *reinterpret_cast<T*>(stage + (tw * L + gl) * LANE + i * sizeof(T)) = closed;
     };
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) sh_n[e] = 0u;
+    for (int e = threadIdx.x; e < E; e += kTeamThreads) sh_n[e] = 0u;
+    if (threadIdx.x < L) sh_base[threadIdx.x] = base_of(threadIdx.x);
     if (VALUES)
-        for (int i = threadIdx.x; i < L * BIAS; i += kRouteThreads) {
+        for (int i = threadIdx.x; i < L * BIAS; i += kTeamThreads) {
             const int l = i / BIAS, o = i % BIAS;
-            const bool some = l < a.groups * pl.per_group && o < held_by(l);
-            const float b = !some ? -INFINITY : a.bias ? a.bias[base_of(l) + o] : 0.f;
+            const float b = o >= held_by(l) ? -INFINITY : a.bias ? a.bias[base_of(l) + o] : 0.f;
             sh_bias[i] = b > -INFINITY ? b : -INFINITY;
         }
     fill(stages);
     fill(stages + pl.stage);
     __syncthreads();
     const T* const base = static_cast<const T*>(a.x);
-    const int64_t tiles = (a.tokens + TPW - 1) / TPW, step = (int64_t)gridDim.x * kRouteWarps;
+    const int64_t tiles = (a.tokens + TPW - 1) / TPW, step = (int64_t)gridDim.x * kTeamWarps;
     // where this lane's words of a row go
     int to[WORDS];
     if (pl.vector) {
@@ -252,42 +299,45 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
         copy_async_commit();
         return on;
     };
-    const int64_t tile0 = (int64_t)blockIdx.x * kRouteWarps + warp;
+    const int64_t tile0 = (int64_t)blockIdx.x * kTeamWarps + warp;
     bool on = fetch(tile0, stages), next_on = fetch(tile0 + step, stages + pl.stage);
     int turn = 0;
     for (int64_t tile = tile0; tile < tiles; tile += step, turn ^= 1) {
         char* const stage = stages + turn * pl.stage;
+        const char* const token = stage + tw * L * LANE;
         const int64_t t = tile * TPW + tw;
         copy_async_wait<1>();
         __syncwarp();
-        const char* const mine = stage + (tw * L + gl) * LANE;
-        const float* const own_bias = sh_bias + gl * BIAS;
+        auto score_of = [&](int place) {
+            return to_f32(*reinterpret_cast<const T*>(token + place / EPL * LANE + place % EPL * (int)sizeof(T)));
+        };
+        auto bias_of = [&](int place) { return sh_bias[place / EPL * BIAS + place % EPL]; };
         float v[EPL];
+        auto load = [&]() {
 #pragma unroll
-        for (int i = 0; i < WORDS; ++i) {
-            float2 f[N / 2];
-            unpack(*reinterpret_cast<const uint4*>(mine + i * 16), f, T());
+            for (int i = 0; i < WORDS; ++i) {
+                float2 f[N / 2];
+                unpack(*reinterpret_cast<const uint4*>(token + gl * LANE + i * 16), f, T());
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-                v[i * N + 2 * j] = f[j].x;
-                v[i * N + 2 * j + 1] = f[j].y;
+                for (int j = 0; j < N / 2; ++j) {
+                    v[i * N + 2 * j] = f[j].x;
+                    v[i * N + 2 * j + 1] = f[j].y;
+                }
             }
-        }
-        float top = v[0], low = v[0];
-#pragma unroll
-        for (int i = 1; i < EPL; ++i) top = max_nan(top, v[i]);
-        if (VALUES) {
-#pragma unroll
-            for (int i = 1; i < EPL; ++i) low = fminf(low, v[i]);
-        }
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
-        // left to choose_exact: NaN; no probabilities; scores so large that their products lose what counts
+        };
+        load();
         const bool summed = a.score == ISO_ROUTE_SOFTMAX && (VALUES || !a.renormalize);
-        bool exact = on && (top != top || (a.score == ISO_ROUTE_SOFTMAX && top == INFINITY) ||
-                            (summed && fabsf(top) >= 2000.f && top != -INFINITY));
-        const float ref = top == -INFINITY ? 0.f : top * kLog2e;
-        float inv = 0.f;
+        float top = 0.f, ref = 0.f, inv = 0.f;
+        if (!sigmoid) {  // the largest score: NaN shows in it
+            top = max_nan(v);
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(~0u, top, o));
+            ref = top == -INFINITY ? 0.f : top * kLog2e;
+        }
+        // left to choose_exact: NaN; no probabilities; scores so large that their products lose what counts
+        bool exact = top != top || (a.score == ISO_ROUTE_SOFTMAX && top == INFINITY) ||
+                     (summed && fabsf(top) >= 2000.f && top != -INFINITY);
+        const float low = VALUES ? min_of(v) : 0.f;
         if (summed) {
             float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -299,86 +349,116 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
             inv = 1.f / group_add<L>((part[0] + part[1]) + (part[2] + part[3]));
         }
         if (VALUES) {
-            unsigned shut = 0u;
-            if (__any_sync(~0u, low == -INFINITY)) {
+            const float* const bias = sh_bias + gl * BIAS;
+            // (the product of two must not overflow)
+            const bool apart = sigmoid && __any_sync(~0u, low < -40.f);
 #pragma unroll
-                for (int i = 0; i < WORDS; ++i) {
-                    float2 f[N / 2];
-                    unpack(*reinterpret_cast<const uint4*>(mine + i * 16), f, T());
-#pragma unroll
-                    for (int j = 0; j < N / 2; ++j) {
-                        shut |= (f[j].x == -INFINITY ? 1u : 0u) << (i * N + 2 * j);
-                        shut |= (f[j].y == -INFINITY ? 1u : 0u) << (i * N + 2 * j + 1);
+            for (int i = 0; i < EPL; i += 4) {
+                const float4 b = *reinterpret_cast<const float4*>(bias + i);
+                if (!sigmoid) {
+                    v[i] = fmaf(v[i], inv, b.x);
+                    v[i + 1] = fmaf(v[i + 1], inv, b.y);
+                    v[i + 2] = fmaf(v[i + 2], inv, b.z);
+                    v[i + 3] = fmaf(v[i + 3], inv, b.w);
+                } else {
+                    float2 p = mul2({v[i], v[i + 1]}, {-kLog2e, -kLog2e}), q = mul2({v[i + 2], v[i + 3]}, {-kLog2e, -kLog2e});
+                    p = add2({ex2(p.x), ex2(p.y)}, {1.f, 1.f});
+                    q = add2({ex2(q.x), ex2(q.y)}, {1.f, 1.f});
+                    if (!apart) {  // two quotients from one
+                        const float r = rcp(p.x * p.y), s = rcp(q.x * q.y);
+                        v[i] = fmaf(r, p.y, b.x);
+                        v[i + 1] = fmaf(r, p.x, b.y);
+                        v[i + 2] = fmaf(s, q.y, b.z);
+                        v[i + 3] = fmaf(s, q.x, b.w);
+                    } else {
+                        v[i] = rcp(p.x) + b.x;
+                        v[i + 1] = rcp(p.y) + b.y;
+                        v[i + 2] = rcp(q.x) + b.z;
+                        v[i + 3] = rcp(q.y) + b.w;
                     }
                 }
             }
-#pragma unroll
-            for (int i = 0; i < EPL; i += 4) {
-                const float4 b = *reinterpret_cast<const float4*>(own_bias + i);
-                const float bias[4] = {b.x, b.y, b.z, b.w};
-                if (sigmoid) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i + j] = rcp(1.f + ex2(v[i + j] * -kLog2e)) + bias[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i + j] = fmaf(v[i + j], inv, bias[j]);
-                }
-            }
-            if (shut) {
+            if (__any_sync(~0u, low == -INFINITY)) {
 #pragma unroll
                 for (int i = 0; i < EPL; ++i)
-                    if (shut >> i & 1u) v[i] = -INFINITY;
+                    if (to_f32(*reinterpret_cast<const T*>(token + gl * LANE + i * (int)sizeof(T))) == -INFINITY) v[i] = -INFINITY;
             }
         }
-        float part[8];  // the partial maxima
+        // the partial maxima, and the largest of what is second in its part
+        float part[8], second = -INFINITY;
+        const bool pairs = VALUES && a.groups > 1 && a.group_best == 2;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            part[i] = v[i * PER];
-#pragma unroll
-            for (int j = 1; j < PER; ++j) part[i] = fmaxf(part[i], v[i * PER + j]);
+            const float* const q = v + i * PER;
+            if (PER == 1) {
+                part[i] = q[0];
+            } else if (PER == 2) {
+                part[i] = max_nan(q[0], q[1]);
+                if (pairs) second = fmaxf(second, fminf(q[0], q[1]));
+            } else {
+                const float p = max_nan(q[0], q[1]), r = max_nan(q[2 % PER], q[3 % PER]);
+                part[i] = max_nan(p, r);
+                if (pairs) second = max3(second, fminf(p, r), fmaxf(fminf(q[0], q[1]), fminf(q[2 % PER], q[3 % PER])));
+            }
         }
+        static_assert(PER == 1 || PER == 2 || PER == 4, "the parts above");
+        if (VALUES) exact |= max_nan(part) != max_nan(part);
         sort8(part);
         bool kept = has_group;
         if (a.groups > 1) {
-            float one = part[0], two = -INFINITY;
-            if (a.group_best == 2) {
-                // the second largest: of the largest's maximum, or another one
-                float at_most = part[1];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float hi = v[i * PER], second = -INFINITY;
-#pragma unroll
-                    for (int j = 1; j < PER; ++j) {
-                        second = fmaxf(second, fminf(hi, v[i * PER + j]));
-                        hi = fmaxf(hi, v[i * PER + j]);
-                    }
-                    at_most = fmaxf(at_most, second);
-                }
-                two = at_most;
-            }
+            float one = part[0], two = pairs ? fmaxf(second, part[1]) : -INFINITY;
             for (int o = 1; o < pl.per_group; o <<= 1) {
                 const float p = __shfl_xor_sync(~0u, one, o), q = __shfl_xor_sync(~0u, two, o);
-                two = fmaxf(fminf(one, p), fmaxf(two, q));
+                two = max3(fminf(one, p), two, q);
                 one = fmaxf(one, p);
             }
-            const float value = a.group_best == 2 && two > -INFINITY ? one + two : one;
-            const int group = gl / pl.per_group;
+            const float value = pairs && two > -INFINITY ? one + two : one;
+            const int own = gl / pl.per_group;
             int rank = 0;
-            float above = -INFINITY, below = INFINITY;
             for (int g = 0; g < a.groups; ++g) {
-                const float other = __shfl_sync(~0u, value, (lane & ~(L - 1)) + g * pl.per_group);
-                rank += other > value || (other == value && g < group) ? 1 : 0;
+                const float other = __shfl_sync(~0u, value, g * pl.per_group, L);
+                rank += other > value || (other == value && g < own) ? 1 : 0;
             }
             kept = has_group && rank < a.top_groups;
             if (VALUES && a.top_groups < a.groups) {
-                below = has_group && kept ? value : INFINITY;
-                above = has_group && !kept ? value : -INFINITY;
+                float below = kept ? value : INFINITY, above = has_group && !kept ? value : -INFINITY;
 #pragma unroll
                 for (int o = L / 2; o > 0; o >>= 1) {
                     below = fminf(below, __shfl_xor_sync(~0u, below, o));
                     above = fmaxf(above, __shfl_xor_sync(~0u, above, o));
                 }
-                if (above > -INFINITY && !(below - above > 2.f * unsure(pl.mode, fmaxf(fabsf(one), fabsf(below)), 1.f))) exact |= on;
+                const float least = 2.f * unsure(sigmoid, below, 1.f);
+                bool near = on && !exact && above > -INFINITY && !(below - above > least);
+                near = (__ballot_sync(~0u, near) & team) != 0u;
+                if (!sigmoid) {
+                    exact |= near;
+                } else if (__any_sync(~0u, near)) {
+                    // the groups' sums in 64 bits, of what may be among their largest
+                    double p = -INFINITY, q = -INFINITY;
+                    unsigned may = 0u;
+                    const float from = pairs && two > -INFINITY ? two : one;
+#pragma unroll
+                    for (int i = 0; i < EPL; ++i) may |= (v[i] >= from - unsure(true, from, 1.f) && v[i] > -INFINITY ? 1u : 0u) << i;
+                    for (; may; may &= may - 1u) {
+                        const int place = gl * EPL + __ffs(may) - 1;
+                        const double c = ranked_value(true, score_of(place), bias_of(place), 0.f, 0.f);
+                        q = fmax(q, fmin(p, c));
+                        p = fmax(p, c);
+                    }
+                    __syncwarp();
+                    for (int o = 1; o < pl.per_group; o <<= 1) {
+                        const double r = __shfl_xor_sync(~0u, p, o), s = __shfl_xor_sync(~0u, q, o);
+                        q = fmax(fmin(p, r), fmax(q, s));
+                        p = fmax(p, r);
+                    }
+                    const double sum = pairs && q > -INFINITY ? p + q : p;
+                    rank = 0;
+                    for (int g = 0; g < a.groups; ++g) {
+                        const double other = __shfl_sync(~0u, sum, g * pl.per_group, L);
+                        rank += other > sum || (other == sum && g < own) ? 1 : 0;
+                    }
+                    if (near) kept = has_group && rank < a.top_groups;
+                }
             }
             if (!kept) {
 #pragma unroll
@@ -386,29 +466,52 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
             }
         }
         // the lanes' maxima merged: the LIST largest of a sub-team's
-        float list[LIST];
+        float bound;
+        if (LIST == 8 && k == 8) {
+            // (the most common one.)  4 of each lane, 8 of two; of the last 8 only the least counts
+            float list[8];
 #pragma unroll
-        for (int i = 0; i < LIST; ++i) list[i] = i < 8 ? part[i] : -INFINITY;
-        for (int o = 1; o < L / pl.halves; o <<= 1) {
-            float other[LIST];
-#pragma unroll
-            for (int i = 0; i < LIST; ++i) other[i] = __shfl_xor_sync(~0u, list[LIST - 1 - i], o);
-#pragma unroll
-            for (int i = 0; i < LIST; ++i) list[i] = fmaxf(list[i], other[i]);
+            for (int i = 0; i < 4; ++i) {
+                list[i] = part[i];
+                list[7 - i] = __shfl_xor_sync(~0u, part[i], 1);
+            }
             merge(list);
-        }
-        const int place = (k + pl.halves - 1) / pl.halves - 1;
-        float bound = list[0];
 #pragma unroll
-        for (int i = 1; i < LIST; ++i)
-            if (i == place) bound = list[i];
-        if (pl.halves == 2) bound = fminf(bound, __shfl_xor_sync(~0u, bound, L / 2));
-        if (VALUES) bound -= unsure(pl.mode, bound, 1.f);
+            for (int o = 2; o < L; o <<= 1) {
+                float other[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) other[i] = __shfl_xor_sync(~0u, list[7 - i], o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) list[i] = fmaxf(list[i], other[i]);
+                if (2 * o < L) merge(list);
+            }
+            bound = min_of(list);
+        } else {
+            float list[LIST];
+#pragma unroll
+            for (int i = 0; i < LIST; ++i) list[i] = i < 8 ? part[i & 7] : -INFINITY;
+            for (int o = 1; o < L / pl.halves; o <<= 1) {
+                float other[LIST];
+#pragma unroll
+                for (int i = 0; i < LIST; ++i) other[i] = __shfl_xor_sync(~0u, list[LIST - 1 - i], o);
+#pragma unroll
+                for (int i = 0; i < LIST; ++i) list[i] = fmaxf(list[i], other[i]);
+                merge(list);
+            }
+            const int place = (k + pl.halves - 1) / pl.halves - 1;
+            bound = list[0];
+#pragma unroll
+            for (int i = 1; i < LIST; ++i)
+                if (i == place) bound = list[i];
+            if (pl.halves == 2) bound = fminf(bound, __shfl_xor_sync(~0u, bound, L / 2));
+        }
+        if (VALUES) bound -= unsure(sigmoid, bound, 1.f);
         bound = fmaxf(bound, __uint_as_float(0xff7fffffu));  // (the lowest)
         unsigned mask = 0u;
 #pragma unroll
         for (int i = 0; i < EPL; ++i) mask |= (v[i] >= bound ? 1u : 0u) << i;
-        if (!kept || !on) mask = 0u;
+        exact &= on;
+        if (!kept || !on || exact) mask = 0u;
         // the candidates in the order of the experts
         int at = __popc(mask), n;
 #pragma unroll
@@ -416,72 +519,117 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
             const int q = __shfl_up_sync(~0u, at, o, L);
             if (gl >= o) at += q;
         }
-        n = __shfl_sync(~0u, at, (lane & ~(L - 1)) + L - 1);
+        n = __shfl_sync(~0u, at, L - 1, L);
         at -= __popc(mask);
         if (n > kFound) {
             exact = true;
             mask = 0u;
             n = 0;
         }
-        for (; mask; mask &= mask - 1u) found_at[warp][tw][at++] = (uint16_t)(gl * EPL + __ffs(mask) - 1);
+        for (; mask; mask &= mask - 1u) found_at[at++] = (uint16_t)(gl * EPL + __ffs(mask) - 1);
         __syncwarp();
-        auto score_of = [&](int code) {
-            return to_f32(*reinterpret_cast<const T*>(stage + (tw * L + code / EPL) * LANE + code % EPL * (int)sizeof(T)));
-        };
         for (int j = gl; j < ((n + 3) & ~3); j += L) {
             float c = -INFINITY;
             if (j < n) {
-                const int code = found_at[warp][tw][j];
-                c = score_of(code);
-                if (VALUES) {
-                    const float b = sh_bias[code / EPL * BIAS + code % EPL];
-                    c = sigmoid ? rcp(1.f + ex2(c * -kLog2e)) + b : fmaf(ex2(fmaf(c, kLog2e, -ref)), inv, b);
-                }
+                const int place = found_at[j];
+                c = score_of(place);
+                if (VALUES) c = (sigmoid ? rcp(1.f + ex2(c * -kLog2e)) : ex2(fmaf(c, kLog2e, -ref)) * inv) + bias_of(place);
             }
-            found[warp][tw][j] = c;
+            found[j] = c;
         }
         __syncwarp();
+        int ranks = 0;
         for (int j = gl; j < n; j += L) {
-            const float c = found[warp][tw][j];
-            int rank = 0;
+            const float c = found[j];
+            int rank = -1;  // the value itself is counted too
             for (int q = 0; q < n; q += 4) {
-                const float4 f = *reinterpret_cast<const float4*>(&found[warp][tw][q]);
-                rank += (f.x > c || (f.x == c && q < j)) + (f.y > c || (f.y == c && q + 1 < j)) +
-                        (f.z > c || (f.z == c && q + 2 < j)) + (f.w > c || (f.w == c && q + 3 < j));
+                const float4 f = *reinterpret_cast<const float4*>(&found[q]);
+                rank += (f.x >= c) + (f.y >= c) + (f.z >= c) + (f.w >= c);
             }
-            first[warp][tw][rank] = c;
-            first_at[warp][tw][rank] = found_at[warp][tw][j];
+            ranks += rank;
+            rank = max(rank, 0);  // (no candidate is NaN)
+            first[rank] = c;
+            first_at[rank] = found_at[j];
+        }
+        // without equal values the ranks are 0 .. n - 1
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) ranks += __shfl_xor_sync(~0u, ranks, o);
+        __syncwarp();
+        if (ranks != n * (n - 1) / 2) {
+            for (int j = gl; j < n; j += L) {
+                const float c = found[j];
+                int rank = 0;
+                for (int q = 0; q < n; ++q) rank += found[q] > c || (found[q] == c && q < j) ? 1 : 0;
+                first[rank] = c;
+                first_at[rank] = found_at[j];
+            }
         }
         __syncwarp();
-        float most = -INFINITY;  // of the chosen's scores
-        bool near = false;
-        for (int i = gl; i < min(k, n); i += L) {
-            const int code = first_at[warp][tw][i];
-            const float x = score_of(code);
-            most = fmaxf(most, x);
-            if (VALUES && i + 1 < n) {
-                const float c = first[warp][tw][i], d = first[warp][tw][i + 1];
-                const float b = sh_bias[code / EPL * BIAS + code % EPL];
-                if (!(c - d > unsure(pl.mode, fmaxf(fabsf(c), fabsf(d)), fmaxf(c - b, 0.f) + 1e-6f))) {
-                    const int other = first_at[warp][tw][i + 1];
-                    near |= score_of(other) != x || sh_bias[other / EPL * BIAS + other % EPL] != b;
+        const int filled = min(k, n);
+        if (VALUES) {
+            bool near = false;
+            for (int i = gl; i < filled && i + 1 < n; i += L) {
+                const float c = first[i], gap = c - first[i + 1];
+                if (!(gap > unsure(sigmoid, c, 1.f))) {
+                    const int p = first_at[i], q = first_at[i + 1];
+                    const float b = bias_of(p), d = bias_of(q), share = fmaxf(c - b, c - gap - d) + 1e-6f;
+                    near |= !(gap > unsure(sigmoid, c, share)) && (b != d || score_of(p) != score_of(q));
                 }
             }
+            near = (__ballot_sync(~0u, near) & team) != 0u;
+            if (__any_sync(~0u, near)) {
+                // the candidates in 64 bits, as two floats
+                if (near) {
+                    for (int j = gl; j < n; j += L) {
+                        const int place = found_at[j];
+                        const double c = ranked_value(sigmoid, score_of(place), bias_of(place), top, inv);
+                        found[j] = (float)c;
+                        first[j] = isfinite(c) ? (float)(c - (double)(float)c) : 0.f;
+                    }
+                }
+                __syncwarp();
+                if (near) {
+                    for (int j = gl; j < n; j += L) {
+                        const float c = found[j], d = first[j];
+                        int rank = 0;
+                        bool open = false;
+                        for (int q = 0; q < n; ++q) {
+                            const float e = found[q], f = first[q];
+                            rank += e > c || (e == c && (f > d || (f == d && q < j))) ? 1 : 0;
+                            if (!sigmoid && q != j) {  // what the sum's own error may turn round
+                                const int p = found_at[j], r = found_at[q];
+                                const float apart = fabsf(bias_of(p) - bias_of(r));
+                                open |= !(fabsf((c - e) + (d - f)) > fmaf(apart, 3e-6f, 1e-12f)) &&
+                                        (score_of(p) != score_of(r) || apart != 0.f);
+                            }
+                        }
+                        first_at[rank] = found_at[j];
+                        exact |= open && rank <= k;
+                    }
+                }
+                __syncwarp();
+            }
         }
-#pragma unroll
-        for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-        exact |= (__ballot_sync(~0u, near) & team) != 0u;
         // the gates
-        auto share_of = [&](float x) {
-            if (a.score == ISO_ROUTE_SIGMOID) return rcp(1.f + ex2(x * -kLog2e));
-            return a.renormalize ? ex2((x - most) * kLog2e) : ex2(fmaf(x, kLog2e, -ref)) * inv;
-        };
-        float factor = a.scale;
+        float most = 0.f;
+        if (a.renormalize && a.score == ISO_ROUTE_SOFTMAX) {  // against the largest score of the chosen
+            most = -INFINITY;
+            for (int i = gl; i < filled; i += L) most = fmaxf(most, score_of(first_at[i]));
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+        }
+        float factor = a.scale, sum = 0.f;
+        for (int i = gl; i < filled; i += L) {
+            const float x = score_of(first_at[i]);
+            const float s = a.score == ISO_ROUTE_SIGMOID ? rcp(1.f + ex2(x * -kLog2e))
+                            : a.renormalize              ? ex2((x - most) * kLog2e)
+                                                         : ex2(fmaf(x, kLog2e, -ref)) * inv;
+            first[i] = s;
+            sum += s;
+        }
         if (a.renormalize) {
-            float sum = 0.f;
-            for (int i = gl; i < min(k, n); i += L) sum += share_of(score_of(first_at[warp][tw][i]));
             sum = group_add<L>(sum);
-            if (n > 0 && !(sum > 1e-30f)) exact |= on;  // sigmoids that are 0 in float32
+            if (n > 0 && !(sum > 1e-30f)) exact = true;  // sigmoids that are 0 in float32
             factor *= 1.f / sum;
         }
         exact = (__ballot_sync(~0u, exact) & team) != 0u;
@@ -490,9 +638,9 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
                 int e = -1;
                 float gate = 0.f;
                 if (i < n) {
-                    const int code = first_at[warp][tw][i];
-                    e = base_of(code / EPL) + code % EPL;
-                    gate = share_of(score_of(code)) * factor;
+                    const int place = first_at[i];
+                    e = sh_base[place / EPL] + place % EPL;
+                    gate = first[i] * factor;
                     atomicAdd(&sh_n[e], 1u);
                 }
                 chosen[t * k + i] = e;
@@ -514,7 +662,7 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
     }
     copy_async_wait_all();
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += kRouteThreads) {
+    for (int e = threadIdx.x; e < E; e += kTeamThreads) {
         if (pl.counted)
             counts[e] = (int64_t)sh_n[e];
         else if (sh_n[e])
@@ -586,33 +734,34 @@ template <class T>
 cudaError_t route_rows(const RouteArgs& a, int64_t* counts, int32_t* chosen, float* gates, cudaStream_t st) {
     RoutePlan p{};
     const int L = route_team(a, sizeof(T), &p);
+    const int warps = L ? kTeamWarps : kRouteWarps;
     const int64_t tiles = L ? (a.tokens + 32 / L - 1) / (32 / L) : a.tokens;
-    const int64_t grid = std::min<int64_t>((tiles + kRouteWarps - 1) / kRouteWarps, 152 * 3);
+    const int64_t grid = std::min<int64_t>((tiles + warps - 1) / warps, 152 * (L ? team_ctas<T> : 4));
     p.counted = L && grid == 1;
     if (!p.counted) {
         const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)a.experts * sizeof(int64_t), st);
         if (e != cudaSuccess || a.tokens == 0) return e;
     }
-    auto go = [&](auto kernel, int shared, auto... more) {
+    auto go = [&](auto kernel, int threads, int shared, auto... more) {
         if (shared > 16 * 1024) {  // (what the kernels have besides is within 48 KB of it)
             const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, shared);
             if (e != cudaSuccess) return e;
         }
-        kernel<<<(unsigned)grid, kRouteThreads, shared, st>>>(a, more..., counts, chosen, gates);
+        kernel<<<(unsigned)grid, threads, shared, st>>>(a, more..., counts, chosen, gates);
         const cudaError_t e = cudaGetLastError();
         prof_mark(st, "route");
         return e;
     };
-    if (!L) return go(route_exact_kernel<T>, kRouteWarps * a.experts * (int)sizeof(double));
+    if (!L) return go(route_exact_kernel<T>, kRouteThreads, kRouteWarps * a.experts * (int)sizeof(double));
     return by_team(L, p.sub, [&](auto l, auto epl) {
         constexpr int LANES = decltype(l)::value, EPL = decltype(epl)::value, N = Word<T>::N;
         constexpr int tile = 32 * ((EPL / N) | 1) * 16;
         p.stage = std::max(tile, (a.experts + 1) / 2 * 16);
         p.vector = p.sub % N == 0 && p.size % N == 0 && chunks_fit(a.x, a.tokens, a.stride, a.experts, N, sizeof(T));
-        const int shared = kRouteWarps * 2 * p.stage;
+        const int shared = kTeamWarps * 2 * p.stage;
         if (p.mode == kByScore)
-            return a.top_k <= 8 ? go(route_kernel<T, LANES, EPL, false, 8>, shared, p) : go(route_kernel<T, LANES, EPL, false, 16>, shared, p);
-        return a.top_k <= 8 ? go(route_kernel<T, LANES, EPL, true, 8>, shared, p) : go(route_kernel<T, LANES, EPL, true, 16>, shared, p);
+            return a.top_k <= 8 ? go(route_kernel<T, LANES, EPL, false, 8>, kTeamThreads, shared, p) : go(route_kernel<T, LANES, EPL, false, 16>, kTeamThreads, shared, p);
+        return a.top_k <= 8 ? go(route_kernel<T, LANES, EPL, true, 8>, kTeamThreads, shared, p) : go(route_kernel<T, LANES, EPL, true, 16>, kTeamThreads, shared, p);
     });
 }
 

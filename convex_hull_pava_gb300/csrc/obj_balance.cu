@@ -72,7 +72,7 @@ balance_tokens_kernel(RouterArgs a, BalanceParts b, BalanceOuts o, int whole,
     __shared__ uint32_t sh_n[G * EPL];
     __shared__ uint32_t sh_live;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane & (G - 1), E = a.experts, k = a.top_k;
-    const unsigned group = group_lanes<G>(), before = group & ((1u << lane) - 1u);
+    const unsigned group = group_lanes<G>();
     for (int e = threadIdx.x; e < G * EPL; e += kTokThreads) sh_n[e] = 0u;
     if (threadIdx.x == 0) sh_live = 0u;
     __syncthreads();
