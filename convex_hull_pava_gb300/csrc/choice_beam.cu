@@ -15,41 +15,49 @@ namespace isodev {
 
 namespace {
 
-constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32, kRowCtas = 3;  // CTAs an SM
 constexpr int kUnroll = 4;                              // words of a thread at a time
 constexpr int kBatch = kRowThreads * kUnroll;           // words of a CTA at a time
-constexpr int kMostBatches = 16;                        // of a part
+constexpr int kMostBatches = 17;                        // of a part (2^17 16-bit scores wherever they start)
 constexpr int kMostWords = kBatch * kMostBatches;       // of a part
-constexpr int kList = 512;                              // what is ranked at once
-constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kList = 1024;                             // what is ranked at once
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinList = 512, kRemembered = 1024;
 // Exponents are kept against whole numbers c, so that sums are brought to another c without rounding;
-// beyond this the float32 product x a has lost its fraction, and the row's sum is formed in K2.
+// beyond this the float32 product x a has lost its fraction, and the row's sum is formed with the differences (exact_sum).
 constexpr float kFar = 8388608.f;
 
 struct PartState {
     float m, c, s, pad;  // largest score; sum s of 2^(x a - c)
 };
+// How the rows are shared out: each is `stretches` of `words` words, from the 128-byte line that it starts
+// in; those of all rows, end to end, are shared evenly among the CTAs, `share` words each.  What a
+// CTA has of one stretch is a part; a stretch has room for `most` of them.
 struct BeamParts {
-    PartState* state;  // [rows * parts]
-    float* value;      // [rows * parts][keep], -inf where there are fewer
+    PartState* state;  // [rows][stretches][most]
+    float* value;      // [rows][stretches][most][keep], -inf where there are fewer
     int32_t* token;
-    int parts, share;  // share: words of a part, from the 128-byte line that the row starts in
+    int64_t share;
+    int stretches, words, most;
 };
 
 // How far the log of a row's sum may be off: the hardware's exponential 2^-22; sums of a batch (a tree
 // of 6), a warp (5) and a CTA (3) at 2^-24 each, one more when they leave; exponents rounded at
 // 2^-24 |v| log 2 with |v| on average at most log2(n), and the scale's own rounding (half of that).
-__device__ __forceinline__ double lse_error(int n) {
-    return 2.4e-7 + 15 * 6e-8 + 6.3e-8 * (1.0 + (double)log2f((float)n)) + 1e-7;
+__device__ __forceinline__ float lse_error(int n) {
+    return 2.4e-7f + 15 * 6e-8f + 6.3e-8f * (1.f + log2f((float)n)) + 1.5e-7f;
 }
 
-__device__ __forceinline__ uint64_t order_key(double v) {
-    const uint64_t b = (uint64_t)__double_as_longlong(v + 0.);
-    return b >> 63 ? ~b : b | 1ull << 63;
+// Order-preserving key of a number that is not NaN, and the number; both zeros are equal.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    const uint32_t b = __float_as_uint(v + 0.f);
+    return b >> 31 ? ~b : b | 0x80000000u;
 }
-__device__ __forceinline__ double order_value(uint64_t key) {
-    return __longlong_as_double((long long)(key >> 63 ? key & ~(1ull << 63) : ~key));
+__device__ __forceinline__ float order_value(uint32_t key) {
+    return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key);
 }
+
+// 2^d of a whole number d <= 0; 0 below float32's exponents.
+__device__ __forceinline__ float power(float d) { return __uint_as_float((uint32_t)(127 + (int)fmaxf(d, -127.f)) << 23); }
 
 // The thread's running sum against the whole number c.
 struct PowerSum {
@@ -60,7 +68,7 @@ struct PowerSum {
             m = top;
             const float to = fminf(fmaxf(ceilf(top * a), -kFar), kFar);
             if (to > c) {
-                const float f = ex2(fmaxf(c - to, -200.f));
+                const float f = power(c - to);
                 s.hi *= f;
                 s.lo *= f;
                 c = to;
@@ -96,183 +104,35 @@ __device__ __forceinline__ bool beam_reads(const BeamArgs& a, int64_t row) {
     return isfinite(a.scores[row]) && !(a.done && a.done[row]);
 }
 
-// A part of a row: its sum of exponentials, and its `keep` largest scores.  Each thread notes the
-// largest of every 4 words that it takes; a bound that `keep` scores reach follows from the warps'
-// largest, and only words whose largest reaches it are looked at again (from L2).
+static_assert(kRowThreads == kJoinThreads, "below");
+// The k-th largest of the CTA's threads' numbers; 0 where fewer are above 0.  Where some warps have nothing to
+// make up a bound of.
+__device__ __noinline__ uint32_t largest_of_threads(uint32_t own, int k, uint32_t* all) {
+    __syncthreads();
+    all[threadIdx.x] = own;
+    if (threadIdx.x == 0) all[kRowThreads] = 0u;
+    __syncthreads();
+    int rank = 0;
+    for (int j = 0; j < kRowThreads; ++j) rank += all[j] > own || (all[j] == own && j < (int)threadIdx.x) ? 1 : 0;
+    if (rank == k - 1) all[kRowThreads] = own;
+    __syncthreads();
+    const uint32_t found = all[kRowThreads];
+    __syncthreads();
+    return found;
+}
+
+// The `keep` largest of a part by `keep` rounds of the largest that comes after the last one: where more
+// scores than the list holds reach the bound (many equal ones).
 template <class T>
-__global__ void __launch_bounds__(kRowThreads, 3)
-beam_rows_kernel(BeamArgs a, BeamParts parts, float scale) {
-    constexpr int N = Word<T>::N;
-    __shared__ float most[kMostBatches][kRowThreads];
-    __shared__ int hits[kList];
-    __shared__ float list[kList];
-    __shared__ int list_at[kList];
-    __shared__ float sh_v[kRowWarps], sh_c[kRowWarps], sh_s[kRowWarps];
-    __shared__ uint64_t sh_best[kRowWarps];
-    __shared__ int hit_n, list_n;
-    let_next_start();
+__device__ __noinline__ void rows_by_rounds(const RowSlots<T>& slots, int first, int begin, int end, int edge, float edge_x,
+                                            int k, float* value, int32_t* token, uint64_t* sh_best) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / parts.parts;
-    const int part = (int)(blockIdx.x % parts.parts);
-    if (!beam_reads(a, row)) return;
-    const T* const x = static_cast<const T*>(a.x) + row * a.stride;
-    const RowSlots<T> slots(x, a.n);
-    const int64_t from = (int64_t)part * parts.share;
-    const int begin = (int)max(from, (int64_t)slots.full);
-    const int end = (int)max((int64_t)begin, min(from + parts.share, (int64_t)slots.end));
-    const int first = (int)min(from, (int64_t)end);  // the slot of thread 0's first word
-    const int batches = (end - first + kBatch - 1) / kBatch;
-    if (tid == 0) hit_n = list_n = 0;
-
-    PowerSum st;
-    // the single scores
-    const int edge = part == 0 && warp == 0 ? slots.single(a.n, lane) : -1;
-    const float edge_x = edge >= 0 ? to_f32(x[edge]) : -INFINITY;
-    auto word = [&](int slot) {
-        return slot >= begin && slot < end ? load_streaming(slots.line + slot) : word_closed(T());
-    };
-    uint4 w[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) w[u] = word(first + tid + u * kRowThreads);
-    for (int b = 0; b < batches; ++b) {
-        uint4 next[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) next[u] = word(first + (b + 1) * kBatch + tid + u * kRowThreads);
-        float top = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) top = fmaxf(top, word_max(w[u], T()));
-        most[b][tid] = top;
-        st.raise(top, scale);
-        float2 sum[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            float2 v[N / 2];
-            unpack(w[u], v, T());
-#pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                v[i] = fma2(v[i], {scale, scale}, {-st.c, -st.c});
-                v[i] = {ex2(v[i].x), ex2(v[i].y)};
-            }
-#pragma unroll
-            for (int o = N / 4; o > 0; o >>= 1)
-#pragma unroll
-                for (int i = 0; i < o; ++i) v[i] = add2(v[i], v[i + o]);
-            sum[u] = v[0];
-        }
-        static_assert(kUnroll == 4, "the tree below");
-        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        st.s.add(sum[0].x + sum[0].y);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) w[u] = next[u];
-    }
-    const float mine = st.m;  // of the words
-    if (edge >= 0) {
-        st.raise(edge_x, scale);
-        st.s.add(ex2(fmaf(edge_x, scale, -st.c)));
-    }
-    // the part's sum
-    {
-        const float m = warp_max(st.m), c = warp_max(st.c);
-        const float s = warp_add(st.s.value() * ex2(fmaxf(st.c - c, -200.f)));
-        if (lane == 0) {
-            sh_v[warp] = m;
-            sh_c[warp] = c;
-            sh_s[warp] = s;
-        }
-    }
-    __syncthreads();
-    if (tid == 0) {
-        float m = sh_v[0], c = sh_c[0], s = 0.f;
-        for (int i = 1; i < kRowWarps; ++i) {
-            m = fmaxf(m, sh_v[i]);
-            c = fmaxf(c, sh_c[i]);
-        }
-        float part_of[kRowWarps];
-#pragma unroll
-        for (int i = 0; i < kRowWarps; ++i) part_of[i] = sh_s[i] * ex2(fmaxf(sh_c[i] - c, -200.f));
-#pragma unroll
-        for (int o = kRowWarps / 2; o > 0; o >>= 1)
-#pragma unroll
-            for (int i = 0; i < o; ++i) part_of[i] += part_of[i + o];
-        s = part_of[0];
-        parts.state[blockIdx.x] = {m, c, s, 0.f};
-    }
-    __syncthreads();  // (sh_v is used again)
-
-    // a bound that `keep` scores reach: the warps' largest of their threads', as many of each as it takes
-    const int k = a.keep;
-    const int active = min(kRowWarps, (end - first + 31) / 32);
-    float bound = -INFINITY;
-    if (active > 0) {
-        const int each = (k + active - 1) / active;
-        if (warp < active) {
-            float v = mine, least = -INFINITY;
-            for (int i = 0; i < each; ++i) {
-                least = warp_max(v);
-                if (v == least) v = -INFINITY;
-            }
-            if (lane == 0) sh_v[warp] = least;
-        }
-        __syncthreads();
-        bound = INFINITY;
-        for (int i = 0; i < active; ++i) bound = fminf(bound, sh_v[i]);
-        __syncthreads();
-    }
-    auto put = [&](float v, int at) {
-        const int i = atomicAdd(&list_n, 1);
-        if (i < kList) {
-            list[i] = v;
-            list_at[i] = at;
-        }
-    };
-    if (edge >= 0 && edge_x > -INFINITY && edge_x >= bound) put(edge_x, edge);
-    for (int b = 0; b < batches; ++b) {
-        const float v = most[b][tid];
-        if (v > -INFINITY && v >= bound) {
-            const int i = atomicAdd(&hit_n, 1);
-            if (i < kList) hits[i] = b << 16 | tid;
-        }
-    }
-    __syncthreads();
-    const int looked = min(hit_n, kList);
-    for (int i = tid; i < looked * kUnroll; i += kRowThreads) {
-        const int hit = hits[i / kUnroll], slot = first + (hit >> 16) * kBatch + (hit & 0xffff) + i % kUnroll * kRowThreads;
-        if (slot < begin || slot >= end) continue;
-        const uint4 q = slots.line[slot];
-        const T* v = reinterpret_cast<const T*>(&q);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const float f = to_f32(v[j]);
-            if (f > -INFINITY && f >= bound) put(f, slots.first_of(slot) + j);
-        }
-    }
-    __syncthreads();
-    float* const value = parts.value + (int64_t)blockIdx.x * k;
-    int32_t* const token = parts.token + (int64_t)blockIdx.x * k;
-    const int n = list_n;
-    if (hit_n <= kList && n <= kList) {
-        for (int i = tid; i < n; i += kRowThreads) {
-            const float v = list[i];
-            const int at = list_at[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += list[j] > v || (list[j] == v && list_at[j] < at) ? 1 : 0;
-            if (rank < k) {
-                value[rank] = v;
-                token[rank] = at;
-            }
-        }
-        for (int i = n + tid; i < k; i += kRowThreads) value[i] = -INFINITY;
-        return;
-    }
-    // More scores than the list holds reach the bound (many equal ones): `keep` rounds of the largest
-    // that comes after the last one.
     uint64_t last = ~0ull;  // key: the score's order, then the lower token
     for (int i = 0; i < k; ++i) {
         uint64_t best = 0;
         auto look = [&](float v, int at) {
             if (!(v > -INFINITY)) return;
-            const uint32_t u = __float_as_uint(v + 0.f);
-            const uint64_t key = (uint64_t)(u >> 31 ? ~u : u | 0x80000000u) << 32 | (uint32_t)~at;
+            const uint64_t key = (uint64_t)order_key(v) << 32 | (uint32_t)~at;
             if (key < last && key > best) best = key;
         };
         if (edge >= 0) look(edge_x, edge);
@@ -281,7 +141,7 @@ beam_rows_kernel(BeamArgs a, BeamParts parts, float scale) {
             const uint4 q = slots.line[slot];
             const T* v = reinterpret_cast<const T*>(&q);
 #pragma unroll
-            for (int j = 0; j < N; ++j) look(to_f32(v[j]), slots.first_of(slot) + j);
+            for (int j = 0; j < Word<T>::N; ++j) look(to_f32(v[j]), slots.first_of(slot) + j);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(~0u, best, o));
@@ -290,11 +150,235 @@ beam_rows_kernel(BeamArgs a, BeamParts parts, float scale) {
         for (int q = 0; q < kRowWarps; ++q) best = max(best, sh_best[q]);
         __syncthreads();
         if (tid == 0) {
-            const uint32_t u = (uint32_t)(best >> 32);
-            value[i] = best ? __uint_as_float(u >> 31 ? u & 0x7fffffffu : ~u) : -INFINITY;
+            value[i] = best ? order_value((uint32_t)(best >> 32)) : -INFINITY;
             token[i] = (int32_t)~(uint32_t)best;
         }
         last = best;  // (0: nothing is left, and nothing is found below it)
+    }
+}
+
+// A part of a row: its sum of exponentials, and its `keep` largest scores.  Each thread notes the
+// largest of every 4 words that it takes; a bound that `keep` scores reach follows from the warps'
+// largest, and only words whose largest reaches it are looked at again (from L2).  A CTA takes its parts
+// in turn, the next one's first words on their way while one is ranked.
+template <class T>
+__global__ void __launch_bounds__(kRowThreads, kRowCtas)
+beam_rows_kernel(BeamArgs a, BeamParts parts, float scale, int rows) {
+    constexpr int N = Word<T>::N;
+    __shared__ float most[kMostBatches][kRowThreads];
+    __shared__ int hits[kList];
+    __shared__ __align__(16) float list[kList + 4];
+    __shared__ int list_at[kList];
+    __shared__ float sh_m[kRowWarps], sh_c[kRowWarps], sh_s[kRowWarps], sh_least[kRowWarps];
+    __shared__ uint64_t sh_best[kRowWarps];
+    __shared__ uint32_t sh_all[kRowThreads + 1];
+    __shared__ int count[2][2];  // hits and list, of this part and the next
+    let_next_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.keep;
+    if (tid < 4) count[tid >> 1][tid & 1] = 0;
+
+    struct Part {
+        const T* x;
+        int64_t slot;            // its place among the parts
+        int begin, end, first;  // words; `first`: thread 0's first one
+        int spare;               // places of its stretch that no part takes, behind its last one
+        bool read, heads;        // heads: it begins its row
+    };
+    // the CTA's words: `left` of them from word `from` of a stretch, the `index`-th of its row, on
+    const int64_t begin_at = blockIdx.x * parts.share;
+    int64_t left = min(parts.share, (int64_t)rows * parts.stretches * parts.words - begin_at);
+    int64_t stretch = begin_at / parts.words;
+    int from = (int)(begin_at - stretch * parts.words), row = (int)(stretch / parts.stretches);
+    int index = (int)(stretch - (int64_t)row * parts.stretches);
+    int number = from == 0 ? 0 : (int)(blockIdx.x - stretch * parts.words / parts.share);
+    auto take = [&]() {
+        Part p{nullptr, 0, 0, 0, 0, 0, false, false};
+        if (left <= 0) return p;
+        const int size = (int)min((int64_t)(parts.words - from), left);
+        p.read = beam_reads(a, row);
+        if (p.read) {
+            p.slot = stretch * parts.most + number;
+            p.spare = from + size == parts.words ? parts.most - 1 - number : 0;
+            p.x = static_cast<const T*>(a.x) + row * a.stride;
+            const RowSlots<T> slots(p.x, a.n);
+            const int first = index * parts.words + from;  // (below 2^29 + 16)
+            p.heads = first == 0;
+            p.begin = max(first, slots.full);
+            p.end = max(p.begin, min(first + size, slots.end));
+            p.first = min(first, p.end);
+        }
+        left -= size;
+        from = number = 0;
+        ++stretch;
+        if (++index == parts.stretches) {
+            index = 0;
+            ++row;
+        }
+        return p;
+    };
+    uint4 w[kUnroll];
+    auto ask = [&](const Part& p, int b, uint4 (&to)[kUnroll]) {  // words of batch b
+        const uint4* const line = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p.x) & ~uintptr_t(127));
+        const int slot = p.first + b * kBatch + tid;
+        if (p.first + b * kBatch >= p.begin && p.first + (b + 1) * kBatch <= p.end) {
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) to[u] = load_streaming(line + slot + u * kRowThreads);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int q = slot + u * kRowThreads;
+            to[u] = q >= p.begin && q < p.end ? load_streaming(line + q) : word_closed(T());
+        }
+    };
+    bool more = true;
+    Part cur = take();
+    ask(cur, 0, w);
+    for (int turn = 0; more;) {
+        more = left > 0;
+        const Part next = take();
+        if (!cur.read) {
+            cur = next;
+            ask(cur, 0, w);
+            continue;
+        }
+        const RowSlots<T> slots(cur.x, a.n);
+        const int batches = (cur.end - cur.first + kBatch - 1) / kBatch;
+        PowerSum st;
+        // the single scores
+        const int edge = cur.heads && warp == 0 ? slots.single(a.n, lane) : -1;
+        const float edge_x = edge >= 0 ? to_f32(cur.x[edge]) : -INFINITY;
+#pragma unroll 2
+        for (int b = 0; b < batches; ++b) {
+            uint4 ahead[kUnroll];
+            if (b + 1 < batches) ask(cur, b + 1, ahead);
+            else ask(next, 0, ahead);
+            float top = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) top = fmaxf(top, word_max(w[u], T()));
+            most[b][tid] = top;
+            st.raise(top, scale);
+            float2 sum[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                float2 v[N / 2];
+                unpack(w[u], v, T());
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    v[i] = fma2(v[i], {scale, scale}, {-st.c, -st.c});
+                    v[i] = {ex2(v[i].x), ex2(v[i].y)};
+                }
+#pragma unroll
+                for (int o = N / 4; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < o; ++i) v[i] = add2(v[i], v[i + o]);
+                sum[u] = v[0];
+            }
+            static_assert(kUnroll == 4, "the tree below");
+            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            st.s.add(sum[0].x + sum[0].y);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) w[u] = ahead[u];
+        }
+        if (batches == 0) ask(next, 0, w);
+        // the warp's sum, and as many of its threads' largest as make up the bound
+        const int active = min(kRowWarps, (cur.end - cur.first + 31) / 32), each = active ? (k + active - 1) / active : 0;
+        const float own = st.m;  // of the words
+        {
+            float v = own, least = -INFINITY;
+            for (int i = 0; i < each; ++i) {
+                least = warp_max(v);
+                if (v == least) v = -INFINITY;
+            }
+            if (edge >= 0) {
+                st.raise(edge_x, scale);
+                st.s.add(ex2(fmaf(edge_x, scale, -st.c)));
+            }
+            const float m = warp_max(st.m), c = warp_max(st.c);
+            const float s = warp_add(st.s.value() * power(st.c - c));
+            if (lane == 0) {
+                sh_m[warp] = m;
+                sh_c[warp] = c;
+                sh_s[warp] = s;
+                sh_least[warp] = least;
+            }
+        }
+        __syncthreads();
+        int &hit_n = count[turn][0], &list_n = count[turn][1];
+        if (tid < 2) count[turn ^ 1][tid] = 0;
+        turn ^= 1;
+        if (warp == kRowWarps - 1) {  // the part's sum
+            const int i = lane & (kRowWarps - 1);
+            const float c = warp_max(sh_c[i]), m = warp_max(sh_m[i]);
+            float s = sh_s[i] * power(sh_c[i] - c);
+#pragma unroll
+            for (int o = kRowWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+            if (lane == 0) parts.state[cur.slot] = {m, c, s, 0.f};
+            if (lane < cur.spare) parts.state[cur.slot + 1 + lane] = {-INFINITY, -kFar, 0.f, 0.f};
+        }
+        float bound = active ? INFINITY : -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kRowWarps; ++i)
+            if (i < active) bound = fminf(bound, sh_least[i]);
+        if (bound == -INFINITY && active > 1) {  // (a part that is closed but for its first words)
+            const uint32_t found = largest_of_threads(own > -INFINITY ? order_key(own) : 0u, k, sh_all);
+            if (found) bound = order_value(found);
+        }
+        auto put = [&](float v, int at) {
+            const int i = atomicAdd(&list_n, 1);
+            if (i < kList) {
+                list[i] = v;
+                list_at[i] = at;
+            }
+        };
+        if (edge >= 0 && edge_x > -INFINITY && edge_x >= bound) put(edge_x, edge);
+        for (int b = 0; b < batches; ++b) {
+            const float v = most[b][tid];
+            if (v > -INFINITY && v >= bound) {
+                const int i = atomicAdd(&hit_n, 1);
+                if (i < kList) hits[i] = b << 16 | tid;
+            }
+        }
+        __syncthreads();
+        const int looked = min(hit_n, kList);
+        for (int i = tid; i < looked * kUnroll; i += kRowThreads) {
+            const int hit = hits[i / kUnroll], slot = cur.first + (hit >> 16) * kBatch + (hit & 0xffff) + i % kUnroll * kRowThreads;
+            if (slot < cur.begin || slot >= cur.end) continue;
+            const uint4 q = slots.line[slot];
+            const T* v = reinterpret_cast<const T*>(&q);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float f = to_f32(v[j]);
+                if (f > -INFINITY && f >= bound) put(f, slots.first_of(slot) + j);
+            }
+        }
+        __syncthreads();
+        float* const value = parts.value + cur.slot * k;
+        int32_t* const token = parts.token + cur.slot * k;
+        for (int i = tid; i < cur.spare * k; i += kRowThreads) value[k + i] = -INFINITY;
+        const int n = list_n;
+        if (hit_n <= kList && n <= kList) {
+            for (int i = tid; i < n; i += kRowThreads) {
+                const float v = list[i];
+                int above = 0, same = 0;
+                for (int j = 0; j < n; ++j) {
+                    above += list[j] > v;
+                    same += list[j] == v;
+                }
+                if (same > 1) {  // the lower tokens first
+                    const int at = list_at[i];
+                    for (int j = 0; j < n; ++j) above += list[j] == v && list_at[j] < at ? 1 : 0;
+                }
+                if (above < k) {
+                    value[above] = v;
+                    token[above] = list_at[i];
+                }
+            }
+            for (int i = n + tid; i < k; i += kRowThreads) value[i] = -INFINITY;
+        } else {
+            rows_by_rounds(slots, cur.first, cur.begin, cur.end, edge, edge_x, k, value, token, sh_best);
+        }
+        cur = next;
     }
 }
 
@@ -306,8 +390,7 @@ struct PowerTable {
     float2 of[32];  // 2^(i / 32)
 };
 template <class T>
-__device__ double exact_sum(const T* x, int n, float m, double scale, const PowerTable& table, Sum* sh) {
-    const float a_hi = (float)scale, a_lo = (float)(scale - (double)a_hi);
+__device__ __noinline__ double exact_sum(const T* x, int n, float m, float a_hi, float a_lo, const PowerTable& table, Sum* sh) {
     constexpr float kLn2Hi = (float)0.693147180559945309417, kLn2Lo = (float)(0.693147180559945309417 - (double)kLn2Hi);
     Sum s;
     for (int e = threadIdx.x; e < n; e += kJoinThreads) {
@@ -344,8 +427,25 @@ __device__ double exact_sum(const T* x, int n, float m, double scale, const Powe
     return total;
 }
 
+// A total as two floats, hi + lo, hi the larger, and its order: hi's key above lo's.
+struct Total {
+    float hi, lo;
+    __device__ __forceinline__ uint64_t key() const { return (uint64_t)order_key(hi) << 32 | order_key(lo); }
+    __device__ __forceinline__ float minus(Total q) const { return __fadd_rn(__fsub_rn(hi, q.hi), __fsub_rn(lo, q.lo)); }
+};
+__device__ __forceinline__ Total total_of(uint64_t key) { return {order_value((uint32_t)(key >> 32)), order_value((uint32_t)key)}; }
+__device__ __forceinline__ Total two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+    return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Total normal(float hi, float lo) {
+    const float s = __fadd_rn(hi, lo);
+    return {s, __fsub_rn(lo, __fsub_rn(s, hi))};
+}
+
+// A continuation; key 0: none.
 struct Continuation {
-    uint64_t key;  // order of its total
+    uint64_t key;
     float x;
     int beam, token;
 };
@@ -355,199 +455,107 @@ __device__ __forceinline__ bool before(const Continuation& p, const Continuation
     return p.x != q.x ? p.x > q.x : p.token < q.token;
 }
 
-// A batch item's beams: their parts' sums, and the continuations ranked.
-template <class T>
-__global__ void __launch_bounds__(kJoinThreads)
-beam_join_kernel(BeamArgs a, BeamParts parts, double scale) {
-    __shared__ double base[ISO_MAX_BEAMS];  // the total of a beam's largest score; -inf: the beam offers nothing
-    __shared__ double off[ISO_MAX_BEAMS];   // how far base may be off
-    __shared__ float largest[ISO_MAX_BEAMS];
-    __shared__ Continuation list[kList], sorted[kList];
-    __shared__ uint32_t sh_v[kJoinWarps];
-    __shared__ Sum sh_sum[kJoinWarps];
-    __shared__ PowerTable table;
-    __shared__ unsigned unsure;
-    __shared__ int list_n;
-    __shared__ Continuation sh_best[kJoinWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.keep, P = parts.parts;
-    const int64_t item = blockIdx.x, row0 = item * a.beams;
-    const double inv_t = 1. / a.temperature;
-    const float scale_f = (float)scale;
-    const T* const x0 = static_cast<const T*>(a.x) + row0 * a.stride;
-    if (tid == 0) {
-        unsure = 0u;
-        list_n = 0;
-    }
-    if (tid < 32) {
-        const double t = exp2((double)tid * 0.03125);
-        table.of[tid] = {(float)t, (float)(t - (double)(float)t)};
-    }
-    __syncthreads();
-    wait_for_previous();
-    for (int b = warp; b < a.beams; b += kJoinWarps) {
-        const float score = a.scores[row0 + b];
-        const bool done = a.done && a.done[row0 + b], read = isfinite(score) && !done;
-        double of = -INFINITY, err = 0.;
-        float m = -INFINITY;
-        uint32_t status = 0u;
-        if (isfinite(score) && done) of = score;
-        if (read) {
-            const PartState* s = parts.state + (row0 + b) * P;
-            float c = -kFar;
-            for (int p = lane; p < P; p += 32) {
-                m = fmaxf(m, s[p].m);
-                c = fmaxf(c, s[p].c);
-            }
-            m = warp_max(m);
-            c = warp_max(c);
-            double sum = 0.;
-            for (int p = lane; p < P; p += 32) sum += (double)s[p].s * (double)ex2(fmaxf(s[p].c - c, -200.f));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            if (!isfinite(m)) {
-                status = ISO_ROW_BAD_Y;
-            } else if (fabsf(m * scale_f) >= kFar) {
-                of = 0.;  // (set below)
-                if (lane == 0) atomicOr(&unsure, 1u << b);
-            } else if (!isfinite(sum)) {
-                status = ISO_ROW_BAD_Y;
-            } else {
-                // (against m by the float32 scale that the sums were formed with)
-                of = score - ((double)c - (double)m * (double)scale_f + log2(sum)) * 0.693147180559945309417;
-                err = lse_error(a.n);
-            }
-        }
-        if (lane == 0) {
-            base[b] = of;
-            off[b] = err;
-            largest[b] = m;
-            if (a.row_status) a.row_status[row0 + b] = status;
-        }
-    }
-    __syncthreads();
-    auto settle = [&]() {  // forms the sums of the beams in `unsure` again
-        const unsigned which = unsure;
-        __syncthreads();
-        for (int b = 0; b < a.beams; ++b) {
-            if (!(which >> b & 1u)) continue;
-            const double sum = exact_sum(x0 + b * a.stride, a.n, largest[b], scale, table, sh_sum);
-            if (tid == 0) {
-                const bool bad = !isfinite(sum);
-                base[b] = bad ? -INFINITY : (double)a.scores[row0 + b] - log(sum);
-                off[b] = 0.;
-                if (bad && a.row_status) a.row_status[row0 + b] = ISO_ROW_BAD_Y;
-            }
-        }
-        if (tid == 0) {
-            unsure = 0u;
-            list_n = 0;
-        }
-        __syncthreads();
-    };
-    if (unsure) settle();
+// 1 / T and log2(e) / T, each as two floats.
+struct BeamScale {
+    float inv_hi, inv_lo, a_hi, a_lo;
+};
 
-    // continuation q of all that the parts have left, then one of each beam that is done
-    const int64_t left = (int64_t)a.beams * P * k, count = left + (a.done ? a.beams : 0);
-    auto at = [&](int64_t q) {
+// What a batch item's kernel has of its beams.
+struct ItemBeams {
+    Total base[ISO_MAX_BEAMS];  // the total of a beam's largest score; -inf: the beam offers nothing
+    float off[ISO_MAX_BEAMS];   // how far base may be off
+    float largest[ISO_MAX_BEAMS];
+    bool ended[ISO_MAX_BEAMS];
+    unsigned unsure;            // beams whose sum is to be formed again
+};
+
+// Forms the sums of the beams in `unsure` again.
+template <class T>
+__device__ __noinline__ void settle(const BeamArgs& a, const BeamScale& sc, ItemBeams& beams, PowerTable& table, Sum* sh) {
+    const int64_t row0 = blockIdx.x * (int64_t)a.beams;
+    const unsigned which = beams.unsure;
+    if (threadIdx.x < 32) {
+        const double t = exp2((double)threadIdx.x * 0.03125);
+        table.of[threadIdx.x] = {(float)t, (float)(t - (double)(float)t)};
+    }
+    __syncthreads();
+    for (int b = 0; b < a.beams; ++b) {
+        if (!(which >> b & 1u)) continue;
+        const T* const x = static_cast<const T*>(a.x) + (row0 + b) * a.stride;
+        const double sum = exact_sum(x, a.n, beams.largest[b], sc.a_hi, sc.a_lo, table, sh);
+        if (threadIdx.x == 0) {
+            const bool bad = !isfinite(sum);
+            const double t = (double)a.scores[row0 + b] - log(sum);
+            beams.base[b] = bad ? Total{-INFINITY, 0.f} : Total{(float)t, (float)(t - (double)(float)t)};
+            beams.off[b] = 0.f;
+            if (bad && a.row_status) a.row_status[row0 + b] = ISO_ROW_BAD_Y;
+        }
+    }
+    if (threadIdx.x == 0) beams.unsure = 0u;
+    __syncthreads();
+}
+
+// Continuation q of all that an item's parts have left, then one of each beam that is done.
+struct ItemContinuations {
+    const float* value;
+    const int32_t* token;
+    uint32_t of_beam, left, count;
+    int end;
+    BeamScale sc;
+    __device__ __forceinline__ Continuation operator()(const ItemBeams& beams, uint32_t q) const {
         Continuation c{0, 0.f, 0, 0};
         if (q >= left) {
+            if (q >= count) return c;
             c.beam = (int)(q - left);
-            if (a.done[row0 + c.beam] && base[c.beam] > -INFINITY) {
-                c.key = order_key(base[c.beam]);
-                c.token = (int)a.end;
+            if (beams.ended[c.beam] && beams.base[c.beam].hi > -INFINITY) {
+                c.key = beams.base[c.beam].key();
+                c.token = end;
             }
             return c;
         }
-        c.beam = (int)(q / ((int64_t)P * k));
-        if (!(base[c.beam] > -INFINITY) || (a.done && a.done[row0 + c.beam])) return c;
-        c.x = parts.value[row0 * P * k + q];
+        c.beam = (int)(q / of_beam);
+        const Total of = beams.base[c.beam];
+        if (!(of.hi > -INFINITY) || beams.ended[c.beam]) return c;
+        c.x = value[q];
+        c.token = token[q];  // (of no meaning where the value is -inf)
         if (c.x > -INFINITY) {
-            c.key = order_key(base[c.beam] + ((double)c.x - (double)largest[c.beam]) * inv_t);
-            c.token = parts.token[row0 * P * k + q];
+            // base + (x - m) / T
+            const Total d = two_sum(c.x, -beams.largest[c.beam]);
+            const float y = __fmul_rn(d.hi, sc.inv_hi), y_low = __fmaf_rn(d.hi, sc.inv_hi, -y) + fmaf(d.hi, sc.inv_lo, d.lo * sc.inv_hi);
+            const Total t = two_sum(of.hi, y);
+            const Total r = normal(t.hi, t.lo + (of.lo + y_low));
+            c.key = isfinite(r.hi) ? r.key() : 0;  // (below float32's range: closed)
         }
         return c;
-    };
-    float* const out_scores = a.out_scores + item * k;
-    int32_t* const parents = a.parents + item * k;
-    int64_t* const tokens = a.tokens + item * k;
-    auto give = [&](int i, const Continuation& c) {
-        const bool some = c.key != 0;
-        out_scores[i] = some ? (float)order_value(c.key) : -INFINITY;
-        parents[i] = some ? c.beam : -1;
-        tokens[i] = some ? c.token : -1;
-    };
-    for (;;) {
-        // a bound that `keep` continuations reach, as for the parts, from the upper halves of their keys
-        uint32_t most = 0u;
-        for (int64_t q = tid; q < count; q += kJoinThreads) most = max(most, (uint32_t)(at(q).key >> 32));
-        const int active = (int)min((int64_t)kJoinWarps, (count + 31) / 32), each = (k + active - 1) / active;
-        uint32_t least = 0u;
-        for (int i = 0; i < each; ++i) {
-            least = __reduce_max_sync(~0u, most);
-            if (most == least) most = 0u;
-        }
-        if (lane == 0) sh_v[warp] = least;
-        __syncthreads();
-        uint32_t high = ~0u;
-        for (int i = 0; i < active; ++i) high = min(high, sh_v[i]);
-        // and as far below it as two beams may be off
-        const double slack = 2. * lse_error(a.n);
-        const uint64_t bound = high ? order_key(order_value((uint64_t)high << 32) - slack) : 1;
-        for (int64_t q = tid; q < count; q += kJoinThreads) {
-            const Continuation c = at(q);
-            if (c.key >= bound) {
-                const int i = atomicAdd(&list_n, 1);
-                if (i < kList) list[i] = c;
-            }
-        }
-        __syncthreads();
-        const int n = list_n;
-        if (n > kList) break;
-        for (int i = tid; i < n; i += kJoinThreads) {
-            const Continuation c = list[i];
-            int rank = 0;
-            for (int j = 0; j < n; ++j) rank += before(list[j], c);
-            sorted[rank] = c;
-        }
-        __syncthreads();
-        // neighbours of different beams that are nearer than they may be off
-        if (n > k) {
-            const double last = order_value(sorted[k - 1].key) - slack;
-            for (int i = tid; i + 1 < n; i += kJoinThreads) {
-                const Continuation p = sorted[i], q = sorted[i + 1];
-                const double gap = order_value(p.key) - order_value(q.key), may = off[p.beam] + off[q.beam];
-                if (p.beam != q.beam && may > 0. && !(gap > may) && order_value(q.key) >= last)
-                    atomicOr(&unsure, (off[p.beam] > 0. ? 1u << p.beam : 0u) | (off[q.beam] > 0. ? 1u << q.beam : 0u));
-            }
-        } else {
-            for (int i = tid; i + 1 < n; i += kJoinThreads) {
-                const Continuation p = sorted[i], q = sorted[i + 1];
-                const double gap = order_value(p.key) - order_value(q.key), may = off[p.beam] + off[q.beam];
-                if (p.beam != q.beam && may > 0. && !(gap > may))
-                    atomicOr(&unsure, (off[p.beam] > 0. ? 1u << p.beam : 0u) | (off[q.beam] > 0. ? 1u << q.beam : 0u));
-            }
-        }
-        __syncthreads();
-        if (!unsure) {
-            for (int i = tid; i < k; i += kJoinThreads) give(i, i < n ? sorted[i] : Continuation{0, 0.f, 0, 0});
-            return;
-        }
-        settle();
     }
-    // More continuations than the list holds reach the bound (many equal ones): all sums formed again,
-    // and `keep` rounds of the first that comes after the last one.
+};
+
+__device__ __forceinline__ void give(const BeamArgs& a, int i, const Continuation& c) {
+    const bool some = c.key != 0;
+    const int64_t at = blockIdx.x * (int64_t)a.keep + i;
+    a.out_scores[at] = some ? total_of(c.key).hi : -INFINITY;
+    a.parents[at] = some ? c.beam : -1;
+    a.tokens[at] = some ? c.token : -1;
+}
+
+// The continuations by `keep` rounds of the first that comes after the last one: where more reach the bound
+// than the list holds (many equal ones).  All sums are formed again first.
+template <class T>
+__device__ __noinline__ void join_by_rounds(const BeamArgs& a, const ItemContinuations& at, ItemBeams& beams, PowerTable& table,
+                                            Sum* sh, Continuation* sh_best) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __syncthreads();
     if (tid == 0) {
         for (int b = 0; b < a.beams; ++b)
-            if (off[b] > 0.) unsure |= 1u << b;
+            if (beams.off[b] > 0.f) beams.unsure |= 1u << b;
     }
     __syncthreads();
-    settle();
+    settle<T>(a, at.sc, beams, table, sh);
     Continuation last{~0ull, INFINITY, -1, -1};
-    for (int i = 0; i < k; ++i) {
+    for (int i = 0; i < a.keep; ++i) {
         Continuation best{0, 0.f, 0, 0};
-        for (int64_t q = tid; q < count; q += kJoinThreads) {
-            const Continuation c = at(q);
+        for (uint32_t q = tid; q < at.count; q += kJoinThreads) {
+            const Continuation c = at(beams, q);
             if (c.key && before(last, c) && (!best.key || before(c, best))) best = c;
         }
 #pragma unroll
@@ -566,25 +574,182 @@ beam_join_kernel(BeamArgs a, BeamParts parts, double scale) {
             if (c.key && (!best.key || before(c, best))) best = c;
         }
         __syncthreads();
-        if (tid == 0) give(i, best);
+        if (tid == 0) give(a, i, best);
         if (!best.key) {
-            for (int j = i + 1 + tid; j < k; j += kJoinThreads) give(j, best);
+            for (int j = i + 1 + tid; j < a.keep; j += kJoinThreads) give(a, j, best);
             return;
         }
         last = best;
     }
 }
 
-// Parts of a row: enough CTAs for the GPU, each with a batch of words at least, and no more words
-// than a part has room to note.
-int row_parts(int64_t rows, int64_t n, int size, int* share) {
-    const int64_t slots = (n * size + 112 + 15) / 16 + 1;
-    const int64_t want = (152 * 4 + rows - 1) / std::max<int64_t>(rows, 1);
-    int64_t parts = std::min<int64_t>(want, (slots + kBatch - 1) / kBatch);
-    parts = std::max<int64_t>(parts, (slots + kMostWords - 1) / kMostWords);
-    *share = (int)(((slots + parts - 1) / parts + 7) / 8 * 8);
-    if (*share > kMostWords) *share = kMostWords;
-    return (int)((slots + *share - 1) / *share);
+// A batch item's beams: their parts' sums, and the continuations ranked.  Totals are two floats: beside
+// lse's error (off) theirs is nothing (2^-46).
+template <class T>
+__global__ void __launch_bounds__(kJoinThreads)
+beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
+    __shared__ ItemBeams beams;
+    __shared__ uint64_t key_of[kRemembered];  // the first continuations' keys
+    __shared__ Continuation list[kJoinList], sorted[kJoinList];
+    __shared__ uint32_t sh_least[kJoinWarps], sh_all[kJoinThreads + 1];
+    __shared__ Sum sh_sum[kJoinWarps];
+    __shared__ PowerTable table;
+    __shared__ int list_n;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.keep, P = parts.stretches * parts.most;
+    const int64_t row0 = blockIdx.x * (int64_t)a.beams;
+    const float may_be = lse_error(a.n), slack = 2.f * may_be;
+    constexpr float kLn2Hi = (float)0.693147180559945309417, kLn2Lo = (float)(0.693147180559945309417 - (double)kLn2Hi);
+    if (tid == 0) beams.unsure = 0u;
+    __syncthreads();
+    wait_for_previous();
+#pragma unroll 1
+    for (int b = warp; b < a.beams; b += kJoinWarps) {
+        const float score = a.scores[row0 + b];
+        const bool done = a.done && a.done[row0 + b], finite = isfinite(score), read = finite && !done;
+        Total of{finite && done ? score : -INFINITY, 0.f};
+        float err = 0.f, m = -INFINITY;
+        uint32_t status = 0u;
+        if (read) {
+            const PartState* const s = parts.state + (row0 + b) * P;
+            float c = -kFar;
+            Sum sum;
+            PartState first{-INFINITY, -kFar, 0.f, 0.f};
+            if (lane < P) first = s[lane];
+            m = first.m;
+            c = first.c;
+            for (int p = lane + 32; p < P; p += 32) {
+                m = fmaxf(m, s[p].m);
+                c = fmaxf(c, s[p].c);
+            }
+            m = warp_max(m);
+            c = warp_max(c);
+            sum.add(first.s * power(first.c - c));
+            for (int p = lane + 32; p < P; p += 32) sum.add(s[p].s * power(s[p].c - c));
+            sum = warp_sum(sum);
+            const float total = __shfl_sync(~0u, sum.value(), 0);
+            const float p = __fmul_rn(m, sc.a_hi);
+            if (!isfinite(m)) {
+                status = ISO_ROW_BAD_Y;
+            } else if (!(fabsf(p) < kFar)) {
+                of = {0.f, 0.f};  // (formed below)
+                if (lane == 0) atomicOr(&beams.unsure, 1u << b);
+            } else if (!isfinite(total)) {
+                status = ISO_ROW_BAD_Y;
+            } else {
+                // score - log 2 (c + log2(total) - m a), a the float32 scale that the sum was formed with;
+                // total = f 2^e
+                const int e = (__float_as_int(total) - 0x3f3504f3) >> 23;  // 0x3f3504f3: 1 / sqrt(2)
+                const float f = __int_as_float(__float_as_int(total) - (e << 23));
+                const float p_low = __fmaf_rn(m, sc.a_hi, -p);
+                Total d = two_sum(__fadd_rn(c, (float)e), -p);  // c + e is a whole number below 2^24
+                d = normal(d.hi, d.lo - p_low);
+                const float q = __fmul_rn(d.hi, kLn2Hi), q_low = __fmaf_rn(d.hi, kLn2Hi, -q) + fmaf(d.hi, kLn2Lo, d.lo * kLn2Hi);
+                const Total t = two_sum(score, -q), r = two_sum(t.hi, -logf(f));
+                of = normal(r.hi, r.lo + (t.lo - q_low));
+                err = may_be;
+            }
+        }
+        if (lane == 0) {
+            beams.base[b] = of;
+            beams.off[b] = err;
+            beams.largest[b] = m;
+            beams.ended[b] = done;
+            if (a.row_status) a.row_status[row0 + b] = status;
+        }
+    }
+    __syncthreads();
+    if (beams.unsure) settle<T>(a, sc, beams, table, sh_sum);
+
+    const uint32_t of_beam = (uint32_t)P * k, left = a.beams * of_beam;
+    const ItemContinuations at{parts.value + row0 * P * k, parts.token + row0 * P * k, of_beam, left,
+                               left + (a.done ? a.beams : 0), (int)a.end, sc};
+    for (;;) {
+        // a bound that `keep` continuations reach, as for the parts, by their totals' larger floats.  A lane
+        // has `stretch` neighbouring ones, of which the warps take one in turn: each warp has some of all beams
+        if (tid == 0) list_n = 0;
+        const uint32_t stretch = (at.count + 31) / 32;
+        uint32_t most = 0u;
+#pragma unroll 1
+        for (uint32_t i = warp; i < stretch; i += kJoinWarps) {
+            const uint64_t key = at(beams, lane * stretch + i).key;
+            most = max(most, (uint32_t)(key >> 32));
+            if (i * 32 < kRemembered) key_of[i * 32 + lane] = key;
+        }
+        const int active = (int)min((uint32_t)kJoinWarps, stretch), each = (k + active - 1) / active;
+        uint32_t least = 0u;
+#pragma unroll 1
+        for (int i = 0; i < each; ++i) {
+            least = __reduce_max_sync(~0u, most);
+            if (most == least) most = 0u;
+        }
+        if (lane == 0) sh_least[warp] = warp < active ? least : ~0u;
+        __syncthreads();
+        uint32_t high = ~0u;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) high = min(high, sh_least[i]);
+        if (high == 0u && at.count > kJoinThreads) {  // (few of many beams in use)
+            most = 0u;
+#pragma unroll 1
+            for (uint32_t q = tid; q < at.count; q += kJoinThreads) most = max(most, (uint32_t)(at(beams, q).key >> 32));
+            high = largest_of_threads(most, k, sh_all);
+        }
+        // and as far below it as two beams may be off
+        const float lowest = high ? order_value(high) : 0.f;
+        const uint64_t bound = high ? (uint64_t)order_key(fmaf(fabsf(lowest), -2.4e-7f, lowest - slack)) << 32 : 1;
+#pragma unroll 1
+        for (uint32_t i = warp; i < stretch; i += kJoinWarps) {
+            if (i * 32 < kRemembered && key_of[i * 32 + lane] < bound) continue;
+            const Continuation c = at(beams, lane * stretch + i);
+            if (c.key < bound) continue;
+            const int to = atomicAdd(&list_n, 1);
+            if (to < kJoinList) list[to] = c;
+        }
+        __syncthreads();
+        const int n = list_n;
+        if (n > kJoinList) {
+            join_by_rounds<T>(a, at, beams, table, sh_sum, sorted);
+            return;
+        }
+        // 4 neighbouring threads rank one
+        for (int i = tid >> 2; i < ((n + 7) & ~7); i += kJoinThreads / 4) {
+            const Continuation c = i < n ? list[i] : Continuation{0, 0.f, 0, 0};
+            int rank = 0;
+            for (int j = tid & 3; j < n; j += 4) {
+                const uint64_t other = list[j].key;
+                rank += other > c.key || (other == c.key && before(list[j], c)) ? 1 : 0;
+            }
+            rank += __shfl_xor_sync(~0u, rank, 1);
+            rank += __shfl_xor_sync(~0u, rank, 2);
+            if (i < n && (tid & 3) == 0) sorted[rank] = c;
+        }
+        __syncthreads();
+        // neighbours of different beams that are nearer than they may be off, down to what may still be chosen
+        for (int i = tid; i + 1 < n; i += kJoinThreads) {
+            const Continuation p = sorted[i], q = sorted[i + 1];
+            const float may = beams.off[p.beam] + beams.off[q.beam];
+            if (p.beam == q.beam || !(may > 0.f) || total_of(p.key).minus(total_of(q.key)) > may) continue;
+            if (i < k || total_of(sorted[k - 1].key).minus(total_of(q.key)) <= slack)
+                atomicOr(&beams.unsure, (beams.off[p.beam] > 0.f ? 1u << p.beam : 0u) | (beams.off[q.beam] > 0.f ? 1u << q.beam : 0u));
+        }
+        __syncthreads();
+        if (!beams.unsure) {
+            for (int i = tid; i < k; i += kJoinThreads) give(a, i, i < n ? sorted[i] : Continuation{0, 0.f, 0, 0});
+            return;
+        }
+        settle<T>(a, sc, beams, table, sh_sum);
+    }
+}
+
+// CTAs for the rows; a CTA's share is a batch of words at least, or a row where that is less (so that short
+// rows get a CTA each).
+int64_t share_rows(int64_t rows, int64_t n, int size, BeamParts* p) {
+    const int64_t words = ((n * size + 112 + 15) / 16 + 1 + 7) / 8 * 8;  // wherever in 128 bytes a row starts
+    p->stretches = (int)((words + kMostWords - 1) / kMostWords);
+    p->words = (int)(((words + p->stretches - 1) / p->stretches + 7) / 8 * 8);
+    const int64_t all = rows * p->stretches * p->words, held = 152 * kRowCtas;
+    p->share = std::max<int64_t>(((all + held - 1) / held + 7) / 8 * 8, std::min(p->words, kBatch));
+    p->most = (int)(p->words % p->share == 0 ? p->words / p->share : p->share % p->words == 0 ? 1 : (p->words - 1) / p->share + 2);
+    return (all + p->share - 1) / p->share;
 }
 
 inline size_t align256c(size_t x) { return (x + 255) & ~size_t(255); }
@@ -594,30 +759,33 @@ inline int score_size(int dtype) { return dtype == ISO_F32 ? 4 : 2; }
 }  // namespace
 
 size_t beam_workspace(int64_t batch, int beams, int64_t n, int dtype, int keep) {
-    int share;
-    const size_t all = (size_t)(batch * beams) * row_parts(batch * beams, n, score_size(dtype), &share);
-    return align256c(all * sizeof(PartState)) + align256c(all * keep * 4) + align256c(all * keep * 4);
+    BeamParts p;
+    share_rows(batch * beams, n, score_size(dtype), &p);
+    const size_t all = (size_t)(batch * beams) * p.stretches * p.most;
+    return align256c(all * sizeof(PartState)) + 2 * align256c(all * keep * 4);
 }
 
 cudaError_t beam_choose(int dtype, const BeamArgs& a, void* ws, cudaStream_t st) {
     const int64_t rows = a.batch * a.beams;
     BeamParts p;
-    p.parts = row_parts(rows, a.n, score_size(dtype), &p.share);
-    const size_t all = (size_t)rows * p.parts;
-    if (all > 2147483647u) return cudaErrorInvalidConfiguration;
+    const int64_t grid = share_rows(rows, a.n, score_size(dtype), &p);
+    const size_t all = (size_t)rows * p.stretches * p.most;
     char* at = static_cast<char*>(ws);
     p.state = reinterpret_cast<PartState*>(at);
     p.value = reinterpret_cast<float*>(at += align256c(all * sizeof(PartState)));
     p.token = reinterpret_cast<int32_t*>(at += align256c(all * a.keep * 4));
-    const double scale = 1.4426950408889634074 / a.temperature;
+    const double scale = 1.4426950408889634074 / a.temperature, inv = 1. / a.temperature;
+    BeamScale sc{(float)inv, 0.f, (float)scale, 0.f};
+    sc.inv_lo = (float)(inv - (double)sc.inv_hi);
+    sc.a_lo = (float)(scale - (double)sc.a_hi);
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
-        beam_rows_kernel<T><<<(unsigned)all, kRowThreads, 0, st>>>(a, p, (float)scale);
+        beam_rows_kernel<T><<<(unsigned)grid, kRowThreads, 0, st>>>(a, p, sc.a_hi, (int)rows);
         cudaError_t e = cudaGetLastError();
         prof_mark(st, "beam_rows");
         if (e != cudaSuccess) return e;
         ClusterLaunch l(a.batch, kJoinThreads, 0, 1, true, st);
-        e = l(beam_join_kernel<T>, a, p, scale);
+        e = l(beam_join_kernel<T>, a, p, sc);
         prof_mark(st, "beam_join");
         return e;
     });

@@ -569,6 +569,7 @@ iso_status iso_route_backward(const void *logits, int dtype, int64_t tokens, int
  *  temperature  T: finite, above 0, 1 / T and log2(e) / T in float32's range.
  *  keep       1 <= keep <= ISO_MAX_KEEP.
  *  out_scores [batch, keep] float32, written: the totals in decreasing order; -inf where nothing is left.
+ *             (A total below float32's range counts as closed.)
  *  parents    [batch, keep] int32, written: the beam of each.    tokens [batch, keep] int64, written.
  *  workspace  iso_beam_choose_workspace_bytes(...) bytes, 256-byte aligned.
  *  row_status [batch * beams] uint32, written, or NULL: ISO_ROW_BAD_Y for a row with a NaN or
