@@ -18,9 +18,10 @@ namespace {
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32, kRowCtas = 3;  // CTAs an SM
 constexpr int kUnroll = 4;                              // words of a thread at a time
 constexpr int kBatch = kRowThreads * kUnroll;           // words of a CTA at a time
-constexpr int kMostBatches = 17;                        // of a part (2^17 16-bit scores wherever they start)
-constexpr int kMostWords = kBatch * kMostBatches;       // of a part
-constexpr int kList = 1024;                             // what is ranked at once
+constexpr int kMostBatches = 24;                        // of a group of parts
+constexpr int kMostWords = kBatch * 17;                 // of a part (2^17 16-bit scores wherever they start)
+constexpr int kGroup = 4;                               // parts that are ranked together
+constexpr int kList = 520, kHits = 1024;                // a part's candidates, a group's words that may have some
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kJoinList = 512, kRemembered = 1024;
 // Exponents are kept against whole numbers c, so that sums are brought to another c without rounding;
 // beyond this the float32 product x a has lost its fraction, and the row's sum is formed with the differences (exact_sum).
@@ -157,62 +158,81 @@ __device__ __noinline__ void rows_by_rounds(const RowSlots<T>& slots, int first,
     }
 }
 
-// A part of a row: its sum of exponentials, and its `keep` largest scores.  Each thread notes the
-// largest of every 4 words that it takes; a bound that `keep` scores reach follows from the warps'
-// largest, and only words whose largest reaches it are looked at again (from L2).  A CTA takes its parts
-// in turn, the next one's first words on their way while one is ranked.
+// What a CTA has to know of a part when it ranks it.
+struct PartNote {
+    int64_t row, slot;
+    int begin, end, first;  // words; `first`: thread 0's first one
+    int batch, batches;     // of the group's
+    int active;             // warps that have words
+    int spare, heads;
+};
+
+// Parts of rows: their sums of exponentials, and their `keep` largest scores.  Each thread notes the
+// largest of every 4 words that it takes; a bound that `keep` scores of a part reach follows from the warps'
+// largest, and only words whose largest reaches it are looked at again (from L2).  A CTA reads the words of
+// a group of parts first, the next words always on their way, and ranks all of them after that.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas)
 beam_rows_kernel(BeamArgs a, BeamParts parts, float scale, int rows) {
     constexpr int N = Word<T>::N;
     __shared__ float most[kMostBatches][kRowThreads];
-    __shared__ int hits[kList];
-    __shared__ __align__(16) float list[kList + 4];
-    __shared__ int list_at[kList];
-    __shared__ float sh_m[kRowWarps], sh_c[kRowWarps], sh_s[kRowWarps], sh_least[kRowWarps];
+    __shared__ uint8_t part_of[kMostBatches];
+    __shared__ int hits[kHits];
+    __shared__ float list[kGroup][kList];
+    __shared__ int list_at[kGroup][kList];
+    __shared__ PartNote note[kGroup];
+    __shared__ float sh_m[kGroup][kRowWarps], sh_c[kGroup][kRowWarps], sh_s[kGroup][kRowWarps], sh_least[kGroup][kRowWarps];
+    __shared__ float sh_bound[kGroup];
     __shared__ uint64_t sh_best[kRowWarps];
     __shared__ uint32_t sh_all[kRowThreads + 1];
-    __shared__ int count[2][2];  // hits and list, of this part and the next
+    __shared__ int hit_n, list_n[kGroup];
     let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.keep;
-    if (tid < 4) count[tid >> 1][tid & 1] = 0;
 
     struct Part {
         const T* x;
         int64_t slot;            // its place among the parts
+        int row;
         int begin, end, first;  // words; `first`: thread 0's first one
         int spare;               // places of its stretch that no part takes, behind its last one
         bool read, heads;        // heads: it begins its row
     };
     // the CTA's words: `left` of them from word `from` of a stretch, the `index`-th of its row, on
-    const int64_t begin_at = blockIdx.x * parts.share;
-    int64_t left = min(parts.share, (int64_t)rows * parts.stretches * parts.words - begin_at);
-    int64_t stretch = begin_at / parts.words;
-    int from = (int)(begin_at - stretch * parts.words), row = (int)(stretch / parts.stretches);
-    int index = (int)(stretch - (int64_t)row * parts.stretches);
-    int number = from == 0 ? 0 : (int)(blockIdx.x - stretch * parts.words / parts.share);
-    auto take = [&]() {
-        Part p{nullptr, 0, 0, 0, 0, 0, false, false};
-        if (left <= 0) return p;
-        const int size = (int)min((int64_t)(parts.words - from), left);
-        p.read = beam_reads(a, row);
+    struct Walk {
+        int64_t left, stretch;
+        int from, row, index, number;
+    } walk;
+    {
+        const int64_t at = blockIdx.x * parts.share;
+        walk.left = min(parts.share, (int64_t)rows * parts.stretches * parts.words - at);
+        walk.stretch = at / parts.words;
+        walk.from = (int)(at - walk.stretch * parts.words);
+        walk.row = (int)(walk.stretch / parts.stretches);
+        walk.index = (int)(walk.stretch - (int64_t)walk.row * parts.stretches);
+        walk.number = walk.from == 0 ? 0 : (int)(blockIdx.x - walk.stretch * parts.words / parts.share);
+    }
+    auto take = [&](Walk& w) {
+        Part p{nullptr, 0, 0, 0, 0, 0, 0, false, false};
+        const int size = (int)min((int64_t)(parts.words - w.from), w.left);
+        p.read = beam_reads(a, w.row);
         if (p.read) {
-            p.slot = stretch * parts.most + number;
-            p.spare = from + size == parts.words ? parts.most - 1 - number : 0;
-            p.x = static_cast<const T*>(a.x) + row * a.stride;
+            p.row = w.row;
+            p.slot = w.stretch * parts.most + w.number;
+            p.spare = w.from + size == parts.words ? parts.most - 1 - w.number : 0;
+            p.x = static_cast<const T*>(a.x) + w.row * a.stride;
             const RowSlots<T> slots(p.x, a.n);
-            const int first = index * parts.words + from;  // (below 2^29 + 16)
+            const int first = w.index * parts.words + w.from;  // (below 2^29 + 16)
             p.heads = first == 0;
             p.begin = max(first, slots.full);
             p.end = max(p.begin, min(first + size, slots.end));
             p.first = min(first, p.end);
         }
-        left -= size;
-        from = number = 0;
-        ++stretch;
-        if (++index == parts.stretches) {
-            index = 0;
-            ++row;
+        w.left -= size;
+        w.from = w.number = 0;
+        ++w.stretch;
+        if (++w.index == parts.stretches) {
+            w.index = 0;
+            ++w.row;
         }
         return p;
     };
@@ -231,154 +251,198 @@ beam_rows_kernel(BeamArgs a, BeamParts parts, float scale, int rows) {
             to[u] = q >= p.begin && q < p.end ? load_streaming(line + q) : word_closed(T());
         }
     };
-    bool more = true;
-    Part cur = take();
+    auto batches_of = [&](const Part& p) { return p.read ? (p.end - p.first + kBatch - 1) / kBatch : 0; };
+    Part cur = take(walk);
     ask(cur, 0, w);
-    for (int turn = 0; more;) {
-        more = left > 0;
-        const Part next = take();
-        if (!cur.read) {
-            cur = next;
-            ask(cur, 0, w);
-            continue;
-        }
-        const RowSlots<T> slots(cur.x, a.n);
-        const int batches = (cur.end - cur.first + kBatch - 1) / kBatch;
-        PowerSum st;
-        // the single scores
-        const int edge = cur.heads && warp == 0 ? slots.single(a.n, lane) : -1;
-        const float edge_x = edge >= 0 ? to_f32(cur.x[edge]) : -INFINITY;
-#pragma unroll 2
-        for (int b = 0; b < batches; ++b) {
-            uint4 ahead[kUnroll];
-            if (b + 1 < batches) ask(cur, b + 1, ahead);
-            else ask(next, 0, ahead);
-            float top = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) top = fmaxf(top, word_max(w[u], T()));
-            most[b][tid] = top;
-            st.raise(top, scale);
-            float2 sum[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                float2 v[N / 2];
-                unpack(w[u], v, T());
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    v[i] = fma2(v[i], {scale, scale}, {-st.c, -st.c});
-                    v[i] = {ex2(v[i].x), ex2(v[i].y)};
-                }
-#pragma unroll
-                for (int o = N / 4; o > 0; o >>= 1)
-#pragma unroll
-                    for (int i = 0; i < o; ++i) v[i] = add2(v[i], v[i + o]);
-                sum[u] = v[0];
+    bool more = true;
+    while (more) {
+        // the words of a group
+        int group = 0, noted = 0;
+        while (more && group < kGroup) {
+            const int batches = batches_of(cur);
+            if (noted + batches > kMostBatches) break;
+            more = walk.left > 0;
+            const Part next = more ? take(walk) : Part{nullptr, 0, 0, 0, 0, 0, 0, false, false};
+            if (!cur.read) {
+                cur = next;
+                ask(cur, 0, w);
+                continue;
             }
-            static_assert(kUnroll == 4, "the tree below");
-            sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            st.s.add(sum[0].x + sum[0].y);
+            PowerSum st;
+#pragma unroll 1
+            for (int b = 0; b < batches; ++b) {
+                uint4 ahead[kUnroll];
+                if (b + 1 < batches) ask(cur, b + 1, ahead);
+                else ask(next, 0, ahead);
+                float top = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < kUnroll; ++u) w[u] = ahead[u];
-        }
-        if (batches == 0) ask(next, 0, w);
-        // the warp's sum, and as many of its threads' largest as make up the bound
-        const int active = min(kRowWarps, (cur.end - cur.first + 31) / 32), each = active ? (k + active - 1) / active : 0;
-        const float own = st.m;  // of the words
-        {
-            float v = own, least = -INFINITY;
+                for (int u = 0; u < kUnroll; ++u) top = fmaxf(top, word_max(w[u], T()));
+                most[noted + b][tid] = top;
+                st.raise(top, scale);
+                float2 sum[kUnroll];
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) {
+                    float2 v[N / 2];
+                    unpack(w[u], v, T());
+#pragma unroll
+                    for (int i = 0; i < N / 2; ++i) {
+                        v[i] = fma2(v[i], {scale, scale}, {-st.c, -st.c});
+                        v[i] = {ex2(v[i].x), ex2(v[i].y)};
+                    }
+#pragma unroll
+                    for (int o = N / 4; o > 0; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < o; ++i) v[i] = add2(v[i], v[i + o]);
+                    sum[u] = v[0];
+                }
+                static_assert(kUnroll == 4, "the tree below");
+                sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                st.s.add(sum[0].x + sum[0].y);
+#pragma unroll
+                for (int u = 0; u < kUnroll; ++u) w[u] = ahead[u];
+            }
+            if (batches == 0) ask(next, 0, w);
+            // the warp's sum, and as many of its threads' largest as make up the bound
+            const int active = min(kRowWarps, (cur.end - cur.first + 31) / 32), each = active ? (k + active - 1) / active : 0;
+            float v = st.m, least = -INFINITY;  // of the words
             for (int i = 0; i < each; ++i) {
                 least = warp_max(v);
-                if (v == least) v = -INFINITY;
+                if (lane == __ffs(__ballot_sync(~0u, v == least)) - 1) v = -INFINITY;
             }
-            if (edge >= 0) {
-                st.raise(edge_x, scale);
-                st.s.add(ex2(fmaf(edge_x, scale, -st.c)));
+            if (cur.heads && warp == 0) {  // the single scores
+                const int edge = RowSlots<T>(cur.x, a.n).single(a.n, lane);
+                if (edge >= 0) {
+                    const float x = to_f32(cur.x[edge]);
+                    st.raise(x, scale);
+                    st.s.add(ex2(fmaf(x, scale, -st.c)));
+                }
             }
             const float m = warp_max(st.m), c = warp_max(st.c);
             const float s = warp_add(st.s.value() * power(st.c - c));
             if (lane == 0) {
-                sh_m[warp] = m;
-                sh_c[warp] = c;
-                sh_s[warp] = s;
-                sh_least[warp] = least;
+                sh_m[group][warp] = m;
+                sh_c[group][warp] = c;
+                sh_s[group][warp] = s;
+                sh_least[group][warp] = warp < active ? least : INFINITY;
             }
+            if (tid == 0) {
+                note[group] = {cur.row, cur.slot, cur.begin, cur.end, cur.first, noted, batches, active, cur.spare, cur.heads};
+                list_n[group] = 0;
+                hit_n = 0;
+            }
+            if (tid < batches) part_of[noted + tid] = (uint8_t)group;
+            noted += batches;
+            ++group;
+            cur = next;
+        }
+        if (group == 0) break;
+        __syncthreads();
+        if (warp < group) {  // warp g: the sum of part g, and its bound
+            const int i = lane & (kRowWarps - 1);
+            const float c = warp_max(sh_c[warp][i]), m = warp_max(sh_m[warp][i]);
+            float s = sh_s[warp][i] * power(sh_c[warp][i] - c), least = sh_least[warp][i];
+#pragma unroll
+            for (int o = kRowWarps / 2; o > 0; o >>= 1) {
+                s += __shfl_xor_sync(~0u, s, o);
+                least = fminf(least, __shfl_xor_sync(~0u, least, o));
+            }
+            const PartNote& p = note[warp];
+            if (lane == 0) {
+                parts.state[p.slot] = {m, c, s, 0.f};
+                sh_bound[warp] = p.active ? least : -INFINITY;
+            }
+            if (lane < p.spare) parts.state[p.slot + 1 + lane] = {-INFINITY, -kFar, 0.f, 0.f};
         }
         __syncthreads();
-        int &hit_n = count[turn][0], &list_n = count[turn][1];
-        if (tid < 2) count[turn ^ 1][tid] = 0;
-        turn ^= 1;
-        if (warp == kRowWarps - 1) {  // the part's sum
-            const int i = lane & (kRowWarps - 1);
-            const float c = warp_max(sh_c[i]), m = warp_max(sh_m[i]);
-            float s = sh_s[i] * power(sh_c[i] - c);
-#pragma unroll
-            for (int o = kRowWarps / 2; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-            if (lane == 0) parts.state[cur.slot] = {m, c, s, 0.f};
-            if (lane < cur.spare) parts.state[cur.slot + 1 + lane] = {-INFINITY, -kFar, 0.f, 0.f};
+        for (int g = 0; g < group; ++g)
+            if (sh_bound[g] == -INFINITY && note[g].batches > 0) {  // (a part with few words, or closed but for few)
+                float own = -INFINITY;
+                for (int b = 0; b < note[g].batches; ++b) own = fmaxf(own, most[note[g].batch + b][tid]);
+                const uint32_t found = largest_of_threads(own > -INFINITY ? order_key(own) : 0u, k, sh_all);
+                if (tid == 0 && found) sh_bound[g] = order_value(found);
+                __syncthreads();
+            }
+        for (int b = 0; b < noted; ++b) {
+            const float v = most[b][tid];
+            if (v > -INFINITY && v >= sh_bound[part_of[b]]) {
+                const int i = atomicAdd(&hit_n, 1);
+                if (i < kHits) hits[i] = b << 16 | tid;
+            }
         }
-        float bound = active ? INFINITY : -INFINITY;
-#pragma unroll
-        for (int i = 0; i < kRowWarps; ++i)
-            if (i < active) bound = fminf(bound, sh_least[i]);
-        if (bound == -INFINITY && active > 1) {  // (a part that is closed but for its first words)
-            const uint32_t found = largest_of_threads(own > -INFINITY ? order_key(own) : 0u, k, sh_all);
-            if (found) bound = order_value(found);
-        }
-        auto put = [&](float v, int at) {
-            const int i = atomicAdd(&list_n, 1);
+        auto put = [&](int g, float v, int at) {
+            const int i = atomicAdd(&list_n[g], 1);
             if (i < kList) {
-                list[i] = v;
-                list_at[i] = at;
+                list[g][i] = v;
+                list_at[g][i] = at;
             }
         };
-        if (edge >= 0 && edge_x > -INFINITY && edge_x >= bound) put(edge_x, edge);
-        for (int b = 0; b < batches; ++b) {
-            const float v = most[b][tid];
-            if (v > -INFINITY && v >= bound) {
-                const int i = atomicAdd(&hit_n, 1);
-                if (i < kList) hits[i] = b << 16 | tid;
+        if (warp < group && note[warp].heads) {
+            const T* const x = static_cast<const T*>(a.x) + note[warp].row * a.stride;
+            const int edge = RowSlots<T>(x, a.n).single(a.n, lane);
+            if (edge >= 0) {
+                const float v = to_f32(x[edge]);
+                if (v > -INFINITY && v >= sh_bound[warp]) put(warp, v, edge);
             }
         }
         __syncthreads();
-        const int looked = min(hit_n, kList);
-        for (int i = tid; i < looked * kUnroll; i += kRowThreads) {
-            const int hit = hits[i / kUnroll], slot = cur.first + (hit >> 16) * kBatch + (hit & 0xffff) + i % kUnroll * kRowThreads;
-            if (slot < cur.begin || slot >= cur.end) continue;
+        const int looked = min(hit_n, kHits) * kUnroll;
+        for (int i = tid; i < looked; i += kRowThreads) {
+            const int hit = hits[i / kUnroll], g = part_of[hit >> 16];
+            const PartNote& p = note[g];
+            const int slot = p.first + ((hit >> 16) - p.batch) * kBatch + (hit & 0xffff) + i % kUnroll * kRowThreads;
+            if (slot < p.begin || slot >= p.end) continue;
+            const RowSlots<T> slots(static_cast<const T*>(a.x) + p.row * a.stride, a.n);
             const uint4 q = slots.line[slot];
             const T* v = reinterpret_cast<const T*>(&q);
+            const float bound = sh_bound[g];
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 const float f = to_f32(v[j]);
-                if (f > -INFINITY && f >= bound) put(f, slots.first_of(slot) + j);
+                if (f > -INFINITY && f >= bound) put(g, f, slots.first_of(slot) + j);
             }
         }
         __syncthreads();
-        float* const value = parts.value + cur.slot * k;
-        int32_t* const token = parts.token + cur.slot * k;
-        for (int i = tid; i < cur.spare * k; i += kRowThreads) value[k + i] = -INFINITY;
-        const int n = list_n;
-        if (hit_n <= kList && n <= kList) {
-            for (int i = tid; i < n; i += kRowThreads) {
-                const float v = list[i];
-                int above = 0, same = 0;
-                for (int j = 0; j < n; ++j) {
-                    above += list[j] > v;
-                    same += list[j] == v;
-                }
-                if (same > 1) {  // the lower tokens first
-                    const int at = list_at[i];
-                    for (int j = 0; j < n; ++j) above += list[j] == v && list_at[j] < at ? 1 : 0;
-                }
-                if (above < k) {
-                    value[above] = v;
-                    token[above] = list_at[i];
+        const int all_hits = hit_n;
+        // a quarter of the threads a part at a time
+        for (int g = warp / (kRowWarps / kGroup); g < group; g += kGroup) {
+            const int n = list_n[g];
+            if (all_hits > kHits || n > kList) continue;
+            float* const value = parts.value + note[g].slot * k;
+            int32_t* const token = parts.token + note[g].slot * k;
+            for (int i = tid % (kRowThreads / kGroup); i < max(n, k); i += kRowThreads / kGroup) {
+                if (i < n) {
+                    const float v = list[g][i];
+                    int above = 0, same = 0;
+                    for (int j = 0; j < n; ++j) {
+                        above += list[g][j] > v;
+                        same += list[g][j] == v;
+                    }
+                    if (same > 1) {  // the lower tokens first
+                        const int at = list_at[g][i];
+                        for (int j = 0; j < n; ++j) above += list[g][j] == v && list_at[g][j] < at ? 1 : 0;
+                    }
+                    if (above < k) {
+                        value[above] = v;
+                        token[above] = list_at[g][i];
+                    }
+                } else {
+                    value[i] = -INFINITY;
                 }
             }
-            for (int i = n + tid; i < k; i += kRowThreads) value[i] = -INFINITY;
-        } else {
-            rows_by_rounds(slots, cur.first, cur.begin, cur.end, edge, edge_x, k, value, token, sh_best);
         }
-        cur = next;
+        for (int g = 0; g < group; ++g) {
+            const PartNote& p = note[g];
+            float* const value = parts.value + p.slot * k;
+            for (int i = tid; i < p.spare * k; i += kRowThreads) value[k + i] = -INFINITY;
+            if (all_hits > kHits || list_n[g] > kList) {
+                const T* const x = static_cast<const T*>(a.x) + p.row * a.stride;
+                const RowSlots<T> slots(x, a.n);
+                const int edge = p.heads && warp == 0 ? slots.single(a.n, lane) : -1;
+                rows_by_rounds(slots, p.first, p.begin, p.end, edge, edge >= 0 ? to_f32(x[edge]) : -INFINITY, k, value,
+                               parts.token + p.slot * k, sh_best);
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -680,7 +744,7 @@ beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
 #pragma unroll 1
         for (int i = 0; i < each; ++i) {
             least = __reduce_max_sync(~0u, most);
-            if (most == least) most = 0u;
+            if (lane == __ffs(__ballot_sync(~0u, most == least)) - 1) most = 0u;
         }
         if (lane == 0) sh_least[warp] = warp < active ? least : ~0u;
         __syncthreads();
@@ -716,7 +780,8 @@ beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
             int rank = 0;
             for (int j = tid & 3; j < n; j += 4) {
                 const uint64_t other = list[j].key;
-                rank += other > c.key || (other == c.key && before(list[j], c)) ? 1 : 0;
+                if (other == c.key) rank += before(list[j], c) || (!before(c, list[j]) && j < i) ? 1 : 0;
+                else rank += other > c.key ? 1 : 0;
             }
             rank += __shfl_xor_sync(~0u, rank, 1);
             rank += __shfl_xor_sync(~0u, rank, 2);
