@@ -53,10 +53,14 @@ class Route:
 class BeamChoice:
     """What :func:`iso_beam_choose` returns."""
     _fields = ("scores", "beams", "tokens", "row_status")
-    __slots__ = _fields
+    __slots__ = ("scores", "beams", "tokens", "_buf", "_rows")
 
-    def __init__(self, scores, beams, tokens, row_status):
-        self.scores, self.beams, self.tokens, self.row_status = scores, beams, tokens, row_status
+    def __init__(self, scores, beams, tokens, buf, rows):
+        self.scores, self.beams, self.tokens, self._buf, self._rows = scores, beams, tokens, buf, rows
+
+    @property
+    def row_status(self):
+        return self._buf[self._buf.numel() - self._rows:]   # the call's workspace is in front of it
 
     def __iter__(self):
         return (getattr(self, name) for name in self._fields)
@@ -179,23 +183,14 @@ def iso_beam_choose(logits, scores, keep: int, done=None, *, end: int = 0, tempe
     best = torch.empty((batch, keep), dtype=torch.float32, device=dev)
     parents = torch.empty((batch, keep), dtype=torch.int32, device=dev)
     tokens = torch.empty((batch, keep), dtype=torch.int64, device=dev)
-    status = torch.empty(rows, dtype=torch.int32, device=dev)
-    if workspace is not None:
-        ws, need = _own_workspace(workspace, dev)
-    else:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws = workspace.data_ptr()
+    ahead = need if workspace is None else 0
+    buf = torch.empty((ahead >> 2) + rows, dtype=torch.int32, device=dev)
+    ws, ws_bytes = (buf.data_ptr(), need) if workspace is None else _own_workspace(workspace, dev)
     _done(_obj._abi.iso_beam_choose(
         logits.data_ptr(), code, batch, beams, n, stride, scores.data_ptr(), _ptr(done), end,
-        temperature, keep, best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), ws, need,
-        status.data_ptr(), _obj._raw_stream(dev.index)), "iso_beam_choose")
-    return BeamChoice(best, parents, tokens, status)
-
-
-class _State(ctypes.Structure):
-    """iso_state"""
-    _fields_ = [("base", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("runs", ctypes.c_int64),
-                ("run_stride", ctypes.c_int64), ("run_bytes", ctypes.c_int64)]
+        temperature, keep, best.data_ptr(), parents.data_ptr(), tokens.data_ptr(), ws, ws_bytes,
+        buf.data_ptr() + ahead, _obj._raw_stream(dev.index)), "iso_beam_choose")
+    return BeamChoice(best, parents, tokens, buf, rows)
 
 
 def _layout(shape, stride, rows, batch):
@@ -242,36 +237,56 @@ def iso_beam_reorder(states, beams, *, stream=None):
     if not 1 <= width <= MAX_BEAMS:
         raise ValueError(f"1 to {MAX_BEAMS} beams")
     rows = batch * width
-    table = (_State * len(states))()
-    seen = set()
-    for at, x in zip(table, states):
-        if not isinstance(x, torch.Tensor) or x.device != dev:
-            raise ValueError(f"states must be tensors on {dev}")
-        if x.requires_grad and torch.is_grad_enabled():
-            raise ValueError("states are moved in place: they may not require a gradient")
-        shape = x.shape
-        if x.dim() < 1 or (shape[0] != rows and shape[0] != batch):
-            raise ValueError("states must be [batch * beams, ...] or [batch, beams, ...]")
-        if 0 in shape:
-            continue
-        got = _layout(shape, x.stride(), rows, batch)
-        if got is None:
-            raise ValueError("a state may be contiguous but for one dimension beyond its rows")
-        base, size = x.data_ptr(), x.element_size()
-        if base in seen:
-            raise ValueError("states may not share memory")
-        seen.add(base)
-        at.base, at.row_stride, at.runs = base, got[0] * size, got[1]
-        at.run_stride, at.run_bytes = got[2] * size, got[3] * size
+    if not all(issubclass(kind, torch.Tensor) for kind in set(map(type, states))):
+        raise ValueError("states must be tensors")
+    # (states of one call mostly have one layout: it is looked at once)
+    kinds = [(x.shape, x.stride(), x.dtype, x.device, x.requires_grad) for x in states]
+    layouts = {}
+    for x, kind in zip(states, kinds):
+        if kind not in layouts:
+            if kind[3] != dev:
+                raise ValueError(f"states must be tensors on {dev}")
+            if kind[4] and torch.is_grad_enabled():
+                raise ValueError("states are moved in place: they may not require a gradient")
+            layouts[kind] = _described(x, rows, batch)
+    words, bases = [], set()
+    for x, kind in zip(states, kinds):
+        got = layouts[kind]
+        if got:
+            base = x.data_ptr()
+            bases.add(base)
+            words += (base,) + got
+    if 5 * len(bases) != len(words):
+        raise ValueError("states may not share memory")
     there = _elsewhere(torch, dev, stream)
-    if there is not None:
+    if there is None:
+        _reorder(words, batch, width, beams)
+    else:
         with there:
-            return _reorder(table, len(states), batch, width, beams)
-    return _reorder(table, len(states), batch, width, beams)
+            _reorder(words, batch, width, beams)
+    # a graph that has saved a state for its backward finds that it was changed
+    torch.autograd.graph.increment_version(states)
 
 
-def _reorder(table, count, batch, width, beams):
-    _done(_obj._abi.iso_beam_reorder(table, count, batch, width, beams.data_ptr(),
+def _described(x, rows, batch):
+    """iso_state's numbers behind the base, in bytes; () for a state without elements."""
+    shape = x.shape
+    if x.dim() < 1 or (shape[0] != rows and shape[0] != batch):
+        raise ValueError("states must be [batch * beams, ...] or [batch, beams, ...]")
+    if 0 in shape:
+        return ()
+    got = _layout(shape, x.stride(), rows, batch)
+    if got is None:
+        raise ValueError("a state may be contiguous but for one dimension beyond its rows")
+    size = x.element_size()
+    row, runs, apart, inner = got
+    return row * size, runs, apart * size, inner * size
+
+
+def _reorder(words, batch, width, beams):
+    # iso_state: five 64-bit numbers
+    table = (ctypes.c_int64 * len(words))(*words)
+    _done(_obj._abi.iso_beam_reorder(table, len(words) // 5, batch, width, beams.data_ptr(),
                                      _obj._raw_stream(beams.device.index)), "iso_beam_reorder")
 
 

@@ -295,8 +295,10 @@ beam_rows_kernel(BeamArgs a, BeamParts parts, float scale, int rows) {
                         for (int i = 0; i < o; ++i) v[i] = add2(v[i], v[i + o]);
                     sum[u] = v[0];
                 }
-                static_assert(kUnroll == 4, "the tree below");
-                sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+#pragma unroll
+                for (int o = kUnroll / 2; o > 0; o >>= 1)
+#pragma unroll
+                    for (int u = 0; u < o; ++u) sum[u] = add2(sum[u], sum[u + o]);
                 st.s.add(sum[0].x + sum[0].y);
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) w[u] = ahead[u];

@@ -13,20 +13,22 @@ namespace isodev {
 namespace {
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveStates = 32;  // states of a launch
+constexpr int kMoveStates = 64;  // states of a launch, a power of two
 
 // A state of one launch: words of `width` bytes, `tail` single bytes behind each run's words.
 struct MoveState {
     char* base;
     int64_t row_stride, run_stride;
-    int64_t words, units_of_run;  // of a run, the tail's bytes counted as words
-    int64_t first_unit;           // the launch's units before this state's
-    int32_t runs, tail, width;
+    int64_t words;          // of a run
+    uint32_t units_of_run;  // one at least
+    uint32_t first_unit;    // the launch's units before this state's
+    uint32_t runs;
+    int32_t tail, width;
 };
 struct MoveArgs {
     MoveState state[kMoveStates];
     const int32_t* parents;
-    int64_t units;
+    uint32_t units;
     int32_t count, beams;
 };
 
@@ -37,76 +39,85 @@ template <> struct MoveWord<4> { using type = uint32_t; };
 template <> struct MoveWord<2> { using type = uint16_t; };
 template <> struct MoveWord<1> { using type = uint8_t; };
 
-template <int B, int W>
-__device__ __forceinline__ void move_words(char* at, int64_t row_stride, int moved, const int (&to)[B], const int (&from)[B]) {
-    using V = typename MoveWord<W>::type;
-    V v[B];
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-        if (i < moved) v[i] = *reinterpret_cast<const V*>(at + from[i] * row_stride);
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-        if (i < moved) *reinterpret_cast<V*>(at + to[i] * row_stride) = v[i];
-}
+// What a warp has to know of its item's beams that move: byte offsets of their rows.
+struct Move {
+    int64_t to, from;
+};
 
-// A unit is kMoveThreads words of a run, of all beams of an item.
-template <int B>
-__global__ void __launch_bounds__(kMoveThreads)
-beam_reorder_kernel(const __grid_constant__ MoveArgs a) {
-    __shared__ int sh_to[32], sh_from[32], sh_moved;
-    for (int64_t unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-        int s = 0;
-        for (int i = 1; i < a.count; ++i)
-            if (unit >= a.state[i].first_unit) s = i;
-        const MoveState& st = a.state[s];
-        int64_t u = unit - st.first_unit;
-        const int64_t block = u % st.units_of_run;
-        u /= st.units_of_run;
-        const int run = (int)(u % st.runs);
-        const int64_t item = u / st.runs;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-            const int b = threadIdx.x;
-            const int p = b < a.beams ? a.parents[item * a.beams + b] : b;
-            const bool moves = p != b && p >= 0 && p < a.beams;
-            const unsigned all = __ballot_sync(~0u, moves);
-            if (moves) {
-                const int i = __popc(all & ((1u << b) - 1u));
-                sh_to[i] = b;
-                sh_from[i] = p;
-            }
-            if (b == 0) sh_moved = __popc(all);
-        }
-        __syncthreads();
-        const int moved = sh_moved;
-        const int64_t word = block * kMoveThreads + threadIdx.x;
-        if (moved == 0 || word >= st.words) continue;
-        int to[B], from[B];
+// M words of each of up to B beams that move, `apart` bytes apart; the first `mine` of them are there.
+template <int B, int M, int W>
+__device__ __forceinline__ void move_words(char* at, int apart, int mine, int moved, const Move* moves) {
+    using V = typename MoveWord<W>::type;
+    V v[B][M];
 #pragma unroll
-        for (int i = 0; i < B; ++i) {
-            to[i] = i < moved ? sh_to[i] : 0;
-            from[i] = i < moved ? sh_from[i] : 0;
+    for (int i = 0; i < B; ++i) {
+        if (i < moved) {
+            const char* const p = at + moves[i].from;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                if (m < mine) v[i][m] = *reinterpret_cast<const V*>(p + m * apart);
         }
-        const int64_t whole = st.words - st.tail;
-        char* at = st.base + item * a.beams * st.row_stride + run * st.run_stride;
-        if (word < whole) {
-            at += word * st.width;
-            switch (st.width) {
-                case 16: move_words<B, 16>(at, st.row_stride, moved, to, from); break;
-                case 8: move_words<B, 8>(at, st.row_stride, moved, to, from); break;
-                case 4: move_words<B, 4>(at, st.row_stride, moved, to, from); break;
-                case 2: move_words<B, 2>(at, st.row_stride, moved, to, from); break;
-                default: move_words<B, 1>(at, st.row_stride, moved, to, from);
-            }
-        } else {
-            move_words<B, 1>(at + whole * st.width + (word - whole), st.row_stride, moved, to, from);
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        if (i < moved) {
+            char* const p = at + moves[i].to;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+                if (m < mine) *reinterpret_cast<V*>(p + m * apart) = v[i][m];
         }
     }
 }
 
-// The largest power of two up to 16 that divides the address and the strides.
-int common_width(const iso_state& s, int64_t rows) {
-    uint64_t v = reinterpret_cast<uintptr_t>(s.base) | 16u;
+// A unit is 32 M words of a run, of all beams of an item; warps take them in turn.  WIDE: all states' words
+// are of 16 bytes (with the other widths beside it the kernel needs twice the registers).
+template <int B, int M, bool WIDE>
+__global__ void __launch_bounds__(kMoveThreads)
+beam_reorder_kernel(const __grid_constant__ MoveArgs a) {
+    __shared__ Move sh_moves[kMoveThreads / 32][B];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Move* const moves = sh_moves[warp];
+    for (uint32_t unit = blockIdx.x * (kMoveThreads / 32) + warp; unit < a.units; unit += gridDim.x * (kMoveThreads / 32)) {
+        int s = 0;
+        for (int step = kMoveStates / 2; step > 0; step >>= 1)
+            if (s + step < a.count && unit >= a.state[s + step].first_unit) s += step;
+        const MoveState& st = a.state[s];
+        const uint32_t u = unit - st.first_unit, line = u / st.units_of_run, block = u - line * st.units_of_run;
+        const uint32_t item = line / st.runs, run = line - item * st.runs;
+        const int p = lane < a.beams ? a.parents[(int64_t)item * a.beams + lane] : lane;
+        const bool moving = p != lane && p >= 0 && p < a.beams;
+        const unsigned all = __ballot_sync(~0u, moving);
+        const int moved = __popc(all);
+        if (moving) moves[__popc(all & ((1u << lane) - 1u))] = {lane * st.row_stride, p * st.row_stride};
+        __syncwarp();
+        char* const base = st.base + (int64_t)item * a.beams * st.row_stride + run * st.run_stride;
+        const int64_t first = (int64_t)block * (32 * M), whole = st.words;
+        const int64_t word = first + lane;
+        if (moved > 0 && word < whole) {
+            const int mine = (int)min((int64_t)M, (whole - word + 31) / 32), apart = 32 * st.width;
+            char* const at = base + word * st.width;
+            if constexpr (WIDE) {
+                move_words<B, M, 16>(at, apart, mine, moved, moves);
+            } else switch (st.width) {
+                case 16:
+                    if constexpr (B <= 16) move_words<B, M, 16>(at, apart, mine, moved, moves);
+                    break;
+                case 8: move_words<B, M, 8>(at, apart, mine, moved, moves); break;
+                case 4: move_words<B, M, 4>(at, apart, mine, moved, moves); break;
+                case 2: move_words<B, M, 2>(at, apart, mine, moved, moves); break;
+                default: move_words<B, M, 1>(at, apart, mine, moved, moves);
+            }
+        }
+        // the bytes behind the last word, with the last unit
+        if (moved > 0 && block == st.units_of_run - 1 && lane < st.tail)
+            move_words<B, 1, 1>(base + whole * st.width + lane, 0, 1, moved, moves);
+        __syncwarp();
+    }
+}
+
+// The largest power of two up to `most` that divides the address and the strides.
+int common_width(const iso_state& s, int64_t rows, unsigned most) {
+    uint64_t v = reinterpret_cast<uintptr_t>(s.base) | most;
     if (rows > 1) v |= (uint64_t)s.row_stride;
     if (s.runs > 1) v |= (uint64_t)s.run_stride;
     return (int)(v & (~v + 1));
@@ -120,40 +131,59 @@ cudaError_t beam_reorder(const iso_state* states, int64_t count, int64_t batch, 
     MoveArgs a;
     a.parents = parents;
     a.beams = beams;
-    a.count = 0;
-    a.units = 0;
-    auto go = [&]() {
-        if (a.count == 0) return cudaSuccess;
-        const unsigned grid = (unsigned)std::min<int64_t>(a.units, 152 * 32);
-        auto kernel = beams <= 4 ? beam_reorder_kernel<4> : beams <= 8 ? beam_reorder_kernel<8>
-                    : beams <= 16 ? beam_reorder_kernel<16> : beam_reorder_kernel<32>;
-        kernel<<<grid, kMoveThreads, 0, st>>>(a);
-        const cudaError_t e = cudaGetLastError();
-        prof_mark(st, "beam_reorder");
+    // The states of 16-byte words first, those of others in launches of their own.
+    for (int wide = 1; wide >= 0; --wide) {
+        // words of a thread at a time, 16 of all beams (8 beams: one each took 485 us of the largest case and not 387)
+        const int words = wide && beams <= 8 ? 2 : 1;
         a.count = 0;
         a.units = 0;
-        return e;
-    };
-    for (int64_t i = 0; i < count; ++i) {
-        const iso_state& s = states[i];
-        if (s.runs == 0 || s.run_bytes == 0) continue;
-        MoveState& m = a.state[a.count++];
-        m.base = static_cast<char*>(s.base);
-        m.row_stride = s.row_stride;
-        m.run_stride = s.run_stride;
-        m.runs = (int32_t)s.runs;
-        m.width = common_width(s, batch * beams);
-        m.tail = (int32_t)(s.run_bytes % m.width);
-        m.words = s.run_bytes / m.width + m.tail;
-        m.units_of_run = (m.words + kMoveThreads - 1) / kMoveThreads;
-        m.first_unit = a.units;
-        a.units += (int64_t)m.units_of_run * m.runs * batch;
-        if (a.count == kMoveStates) {
-            const cudaError_t e = go();
-            if (e != cudaSuccess) return e;
+        auto go = [&]() {
+            if (a.count == 0) return cudaSuccess;
+            constexpr int kWarps = kMoveThreads / 32;
+            const unsigned grid = std::min<uint32_t>((a.units + kWarps - 1) / kWarps, 152 * 32);
+            auto kernel = beam_reorder_kernel<32, 1, false>;
+            if (beams <= 4)
+                kernel = wide ? beam_reorder_kernel<4, 2, true> : beam_reorder_kernel<4, 1, false>;
+            else if (beams <= 8)
+                kernel = wide ? beam_reorder_kernel<8, 2, true> : beam_reorder_kernel<8, 1, false>;
+            else if (beams <= 16)
+                kernel = wide ? beam_reorder_kernel<16, 1, true> : beam_reorder_kernel<16, 1, false>;
+            kernel<<<grid, kMoveThreads, 0, st>>>(a);
+            const cudaError_t e = cudaGetLastError();
+            prof_mark(st, "beam_reorder");
+            a.count = 0;
+            a.units = 0;
+            return e;
+        };
+        for (int64_t i = 0; i < count; ++i) {
+            const iso_state& s = states[i];
+            if (s.runs == 0 || s.run_bytes == 0) continue;
+            const int width = common_width(s, batch * beams, beams <= 16 ? 16 : 8);  // (a thread holds 32 of 8 bytes)
+            if ((width == 16) != (wide == 1)) continue;
+            const int64_t whole = s.run_bytes / width, of_run = std::max<int64_t>(1, (whole + 32 * words - 1) / (32 * words));
+            // (states that are really there are far below this)
+            if (of_run > 0x7fffffff / s.runs || of_run * s.runs > 0x7fffffff / batch) return cudaErrorInvalidValue;
+            const uint32_t units = (uint32_t)(of_run * s.runs * batch);
+            if (a.count == kMoveStates || a.units + units > 0x7fffffffu) {
+                const cudaError_t e = go();
+                if (e != cudaSuccess) return e;
+            }
+            MoveState& m = a.state[a.count++];
+            m.base = static_cast<char*>(s.base);
+            m.row_stride = s.row_stride;
+            m.run_stride = s.run_stride;
+            m.runs = (uint32_t)s.runs;
+            m.width = width;
+            m.tail = (int32_t)(s.run_bytes % width);
+            m.words = whole;
+            m.units_of_run = (uint32_t)of_run;
+            m.first_unit = a.units;
+            a.units += units;
         }
+        const cudaError_t e = go();
+        if (e != cudaSuccess) return e;
     }
-    return go();
+    return cudaSuccess;
 }
 
 }  // namespace isodev

@@ -72,7 +72,7 @@ def test_beam_workspace():
 
 
 def reorder(states, batch=2, beams=3, parents=P, count=None):
-    table = (choices._State * len(states))(*states)
+    table = (ctypes.c_int64 * (5 * len(states)))(*[v or 0 for s in states for v in s])   # iso_state: five 64-bit numbers
     return chp.load_library().iso_beam_reorder(table, len(states) if count is None else count, batch, beams, parents, None)
 
 
