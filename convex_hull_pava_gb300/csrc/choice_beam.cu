@@ -8,7 +8,7 @@
 // sums round, by at most lse_error(n): where two continuations of different beams are nearer to each
 // other than that, the rows' sums are formed again to about 2^-36 before they are ranked.
 #include "choice_internal.h"
-#include "obj_device.cuh"
+#include "choice_device.cuh"
 #include "obj_launch.h"
 
 namespace isodev {
@@ -448,42 +448,12 @@ beam_rows_kernel(BeamArgs a, BeamParts parts, float scale, int rows) {
     }
 }
 
-// exp of a row's scores against its largest m, summed to about 2^-36 of the sum: the exponent
-// (x - m) log2(e) / T as two floats is split into i / 32 and a rest of at most 1 / 64; 2^(i / 32)
-// is a table of two floats, the rest's exponential a polynomial (its z^5 / 120 is under 1.3e-12).
-// NaN where a score is NaN or m is not finite.  In the order of the scores, whatever their place in memory.
-struct PowerTable {
-    float2 of[32];  // 2^(i / 32)
-};
+// The exponentials of a row's scores against its largest m, summed to about 2^-36 of the sum, in the order
+// of the scores, whatever their place in memory.  NaN where a score is NaN or m is not finite.
 template <class T>
-__device__ __noinline__ double exact_sum(const T* x, int n, float m, float a_hi, float a_lo, const PowerTable& table, Sum* sh) {
-    constexpr float kLn2Hi = (float)0.693147180559945309417, kLn2Lo = (float)(0.693147180559945309417 - (double)kLn2Hi);
+__device__ __noinline__ double exact_sum(const T* x, int n, float m, float a_hi, float a_lo, Sum* sh) {
     Sum s;
-    for (int e = threadIdx.x; e < n; e += kJoinThreads) {
-        const float v = to_f32(x[e]);
-        // v - m = d + d_low
-        const float d = __fsub_rn(v, m), back = __fsub_rn(d, v);
-        const float d_low = __fsub_rn(__fsub_rn(v, __fsub_rn(d, back)), __fadd_rn(m, back));
-        float y = __fmul_rn(d, a_hi);
-        if (!(y > -126.f)) {  // nothing, beside a term of 1 (or NaN)
-            s.hi += d == d || v == -INFINITY ? 0.f : NAN;
-            continue;
-        }
-        const float y_low = __fmaf_rn(d, a_hi, -y) + (d * a_lo + d_low * a_hi);
-        const float i = rintf(y * 32.f);
-        const float r = __fmaf_rn(i, -0.03125f, y);  // exact
-        // z = (r + y_low) log 2, two floats
-        const float z = __fmul_rn(r, kLn2Hi);
-        const float z_low = __fmaf_rn(r, kLn2Hi, -z) + __fmaf_rn(r, kLn2Lo, y_low * kLn2Hi);
-        const float rest = __fmaf_rn(z * z, __fmaf_rn(z, __fmaf_rn(z, 1.f / 24, 1.f / 6), 0.5f), z_low * (1.f + z));
-        const int k = (int)i;
-        const float2 t = table.of[k & 31];
-        const float p = __fmul_rn(t.x, z), p_low = __fmaf_rn(t.x, z, -p) + __fmaf_rn(t.x, rest, t.y * (1.f + z));
-        const float f = __uint_as_float((uint32_t)(127 + (k >> 5)) << 23);  // 2^(k >> 5); k >= -126 * 32
-        s.add(t.x * f);
-        s.add(p * f);
-        s.lo += p_low * f;
-    }
+    for (int e = threadIdx.x; e < n; e += kJoinThreads) exp_add(s, to_f32(x[e]), m, a_hi, a_lo);
     s = warp_sum(s);
     if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
     __syncthreads();
@@ -537,18 +507,14 @@ struct ItemBeams {
 
 // Forms the sums of the beams in `unsure` again.
 template <class T>
-__device__ __noinline__ void settle(const BeamArgs& a, const BeamScale& sc, ItemBeams& beams, PowerTable& table, Sum* sh) {
+__device__ __noinline__ void settle(const BeamArgs& a, const BeamScale& sc, ItemBeams& beams, Sum* sh) {
     const int64_t row0 = blockIdx.x * (int64_t)a.beams;
     const unsigned which = beams.unsure;
-    if (threadIdx.x < 32) {
-        const double t = exp2((double)threadIdx.x * 0.03125);
-        table.of[threadIdx.x] = {(float)t, (float)(t - (double)(float)t)};
-    }
     __syncthreads();
     for (int b = 0; b < a.beams; ++b) {
         if (!(which >> b & 1u)) continue;
         const T* const x = static_cast<const T*>(a.x) + (row0 + b) * a.stride;
-        const double sum = exact_sum(x, a.n, beams.largest[b], sc.a_hi, sc.a_lo, table, sh);
+        const double sum = exact_sum(x, a.n, beams.largest[b], sc.a_hi, sc.a_lo, sh);
         if (threadIdx.x == 0) {
             const bool bad = !isfinite(sum);
             const double t = (double)a.scores[row0 + b] - log(sum);
@@ -607,8 +573,8 @@ __device__ __forceinline__ void give(const BeamArgs& a, int i, const Continuatio
 // The continuations by `keep` rounds of the first that comes after the last one: where more reach the bound
 // than the list holds (many equal ones).  All sums are formed again first.
 template <class T>
-__device__ __noinline__ void join_by_rounds(const BeamArgs& a, const ItemContinuations& at, ItemBeams& beams, PowerTable& table,
-                                            Sum* sh, Continuation* sh_best) {
+__device__ __noinline__ void join_by_rounds(const BeamArgs& a, const ItemContinuations& at, ItemBeams& beams, Sum* sh,
+                                            Continuation* sh_best) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     __syncthreads();
     if (tid == 0) {
@@ -616,7 +582,7 @@ __device__ __noinline__ void join_by_rounds(const BeamArgs& a, const ItemContinu
             if (beams.off[b] > 0.f) beams.unsure |= 1u << b;
     }
     __syncthreads();
-    settle<T>(a, at.sc, beams, table, sh);
+    settle<T>(a, at.sc, beams, sh);
     Continuation last{~0ull, INFINITY, -1, -1};
     for (int i = 0; i < a.keep; ++i) {
         Continuation best{0, 0.f, 0, 0};
@@ -659,7 +625,6 @@ beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
     __shared__ Continuation list[kJoinList], sorted[kJoinList];
     __shared__ uint32_t sh_least[kJoinWarps], sh_all[kJoinThreads + 1];
     __shared__ Sum sh_sum[kJoinWarps];
-    __shared__ PowerTable table;
     __shared__ int list_n;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = a.keep, P = parts.stretches * parts.most;
     const int64_t row0 = blockIdx.x * (int64_t)a.beams;
@@ -724,7 +689,7 @@ beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
         }
     }
     __syncthreads();
-    if (beams.unsure) settle<T>(a, sc, beams, table, sh_sum);
+    if (beams.unsure) settle<T>(a, sc, beams, sh_sum);
 
     const uint32_t of_beam = (uint32_t)P * k, left = a.beams * of_beam;
     const ItemContinuations at{parts.value + row0 * P * k, parts.token + row0 * P * k, of_beam, left,
@@ -773,7 +738,7 @@ beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
         __syncthreads();
         const int n = list_n;
         if (n > kJoinList) {
-            join_by_rounds<T>(a, at, beams, table, sh_sum, sorted);
+            join_by_rounds<T>(a, at, beams, sh_sum, sorted);
             return;
         }
         // 4 neighbouring threads rank one
@@ -803,7 +768,7 @@ beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
             for (int i = tid; i < k; i += kJoinThreads) give(a, i, i < n ? sorted[i] : Continuation{0, 0.f, 0, 0});
             return;
         }
-        settle<T>(a, sc, beams, table, sh_sum);
+        settle<T>(a, sc, beams, sh_sum);
     }
 }
 

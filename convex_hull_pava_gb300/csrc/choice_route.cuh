@@ -10,6 +10,7 @@
 //   sigmoid:               gate_i (1 - s_i) g_i,  renormalised: gate_i (1 - s_i) (g_i - sum_j w_j g_j)
 #pragma once
 
+#include "choice_device.cuh"
 #include "choice_internal.h"
 #include "router_rows.cuh"
 
@@ -128,6 +129,8 @@ __device__ __noinline__ void choose_exact(const RouteArgs& a, const T* x, double
 // experts of one group: `per_group` lanes a group of `size` experts, `sub` experts a lane.
 struct RoutePlan {
     int size, per_group, sub;
+    int shift;              // per_group is 1 << shift
+    float of_size, of_sub;  // a little over 1 / size and 1 / sub
     int halves;   // sub-teams of the L lanes that give a bound each (1 or 2)
     int mode;
     int vector;   // rows are copied 16 bytes at a time
@@ -207,9 +210,21 @@ __device__ __forceinline__ float unsure(bool sigmoid, float c, float share) {
     return (sigmoid ? 7e-7f : fmaf(fabsf(share), 3.2e-6f, 1e-7f)) + 1.3e-7f * fabsf(c);
 }
 
-// What is ranked, in 64 bits; of softmax with float32's sum (inv its reciprocal, m the largest score).
-__device__ __noinline__ double ranked_value(bool sigmoid, float x, float b, float m, float inv) {
-    return (sigmoid ? 1. / (1. + exp(-(double)x)) : exp((double)x - (double)m) * (double)inv) + (double)b;
+// What is ranked, in 64 bits; of softmax with the largest score m and one over the sum.
+__device__ __noinline__ double ranked_value(bool sigmoid, float x, float b, float m, double inv) {
+    return (sigmoid ? 1. / (1. + exp(-(double)x)) : exp((double)x - (double)m) * inv) + (double)b;
+}
+
+// One over the softmax's sum of a token's scores to about 2^-36, of which the team's lanes have `count` each.
+template <class T, int L>
+__device__ __noinline__ double inverse_sum(const T* x, int count, float m) {
+    Sum part;
+    for (int i = 0; i < count; ++i) exp_add(part, to_f32(x[i]), m, kLog2e, (float)(1.44269504088896340736 - (double)kLog2e));
+    double sum = (double)part.hi + (double)part.lo;
+    __syncwarp();
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    return 1. / sum;
 }
 
 constexpr int kFound = 32;  // candidates of a token
@@ -221,8 +236,7 @@ constexpr int team_ctas = sizeof(T) == 4 ? 3 : 4;  // an SM, by shared memory an
 // the lanes' partial maxima (8 a lane), which the lanes sort and merge (LIST of them).  VALUES: what is
 // ranked is formed from the scores; otherwise it is the scores themselves, which nothing rounds.  Where
 // candidates' values or groups' sums are nearer to each other than float32 tells they are formed again in
-// 64 bits; tokens with NaN, without probabilities, with too many candidates, or whose order hangs on
-// the softmax's sum are chosen by choose_exact.
+// 64 bits; tokens with NaN, without probabilities, or with too many candidates are chosen by choose_exact.
 template <class T, int L, int EPL, bool VALUES, int LIST>
 __global__ void __launch_bounds__(kTeamThreads, team_ctas<T>)
 route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float* gates) {
@@ -244,11 +258,16 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
     float* const first = sh_first[warp][tw];
     uint16_t* const found_at = sh_found_at[warp][tw];
     uint16_t* const first_at = sh_first_at[warp][tw];
-    auto base_of = [&](int l) { return l / pl.per_group * pl.size + l % pl.per_group * pl.sub; };
+    // lane l's first expert and how many it has; the lane of expert e (quotients by products: exact up to 1,024)
+    auto base_of = [&](int l) { return (l >> pl.shift) * pl.size + (l & (pl.per_group - 1)) * pl.sub; };
     auto held_by = [&](int l) {
-        return l < a.groups * pl.per_group ? max(0, min(pl.sub, pl.size - l % pl.per_group * pl.sub)) : 0;
+        return l < a.groups << pl.shift ? max(0, min(pl.sub, pl.size - (l & (pl.per_group - 1)) * pl.sub)) : 0;
     };
-    const bool has_group = gl < a.groups * pl.per_group;
+    auto lane_of = [&](int e) {
+        const int g = (int)((float)e * pl.of_size), r = e - g * pl.size;
+        return (g << pl.shift) + (int)((float)r * pl.of_sub);
+    };
+    const bool has_group = gl < a.groups << pl.shift;
     const int own_count = held_by(gl);
     const bool sigmoid = VALUES && pl.mode == kSigmoid;
     const T closed = from_f32<T>(sigmoid ? 0.f : -INFINITY);  // places without an expert (their bias is -inf)
@@ -273,7 +292,7 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
     if (pl.vector) {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-            const int e = (gl + i * L) * N, l = e / pl.size * pl.per_group + e % pl.size / pl.sub;
+            const int e = (gl + i * L) * N, l = lane_of(e);
             to[i] = e < E ? (tw * L + l) * LANE + (e - base_of(l)) * (int)sizeof(T) : -1;
         }
     }
@@ -288,11 +307,17 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
                     if (to[i] >= 0) copy_async(stage + to[i], x + (gl + i * L) * N);
             } else {
                 // element by element, the lanes of a token side by side
-                int g = gl / pl.size, r = gl % pl.size;
-                for (int e = gl; e < E; e += L) {
-                    const int q = r / pl.sub;
-                    *reinterpret_cast<T*>(stage + (tw * L + g * pl.per_group + q) * LANE + (r - q * pl.sub) * (int)sizeof(T)) = x[e];
-                    for (r += L; r >= pl.size; r -= pl.size) ++g;
+                T f[EPL];
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if (gl + i * L < E) f[i] = x[gl + i * L];
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    const int e = gl + i * L;
+                    if (e < E) {
+                        const int l = lane_of(e);
+                        *reinterpret_cast<T*>(stage + (tw * L + l) * LANE + (e - base_of(l)) * (int)sizeof(T)) = f[i];
+                    }
                 }
             }
         }
@@ -413,7 +438,7 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
                 one = fmaxf(one, p);
             }
             const float value = pairs && two > -INFINITY ? one + two : one;
-            const int own = gl / pl.per_group;
+            const int own = gl >> pl.shift;
             int rank = 0;
             for (int g = 0; g < a.groups; ++g) {
                 const float other = __shfl_sync(~0u, value, g * pl.per_group, L);
@@ -430,18 +455,17 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
                 const float least = 2.f * unsure(sigmoid, below, 1.f);
                 bool near = on && !exact && above > -INFINITY && !(below - above > least);
                 near = (__ballot_sync(~0u, near) & team) != 0u;
-                if (!sigmoid) {
-                    exact |= near;
-                } else if (__any_sync(~0u, near)) {
+                if (__any_sync(~0u, near)) {
                     // the groups' sums in 64 bits, of what may be among their largest
+                    const double of_sum = sigmoid ? 0. : inverse_sum<T, L>(reinterpret_cast<const T*>(token + gl * LANE), own_count, top);
                     double p = -INFINITY, q = -INFINITY;
                     unsigned may = 0u;
                     const float from = pairs && two > -INFINITY ? two : one;
 #pragma unroll
-                    for (int i = 0; i < EPL; ++i) may |= (v[i] >= from - unsure(true, from, 1.f) && v[i] > -INFINITY ? 1u : 0u) << i;
+                    for (int i = 0; i < EPL; ++i) may |= (v[i] >= from - unsure(sigmoid, from, 1.f) && v[i] > -INFINITY ? 1u : 0u) << i;
                     for (; may; may &= may - 1u) {
                         const int place = gl * EPL + __ffs(may) - 1;
-                        const double c = ranked_value(true, score_of(place), bias_of(place), 0.f, 0.f);
+                        const double c = ranked_value(sigmoid, score_of(place), bias_of(place), top, of_sum);
                         q = fmax(q, fmin(p, c));
                         p = fmax(p, c);
                     }
@@ -579,10 +603,11 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
             near = (__ballot_sync(~0u, near) & team) != 0u;
             if (__any_sync(~0u, near)) {
                 // the candidates in 64 bits, as two floats
+                const double of_sum = sigmoid ? 0. : inverse_sum<T, L>(reinterpret_cast<const T*>(token + gl * LANE), own_count, top);
                 if (near) {
                     for (int j = gl; j < n; j += L) {
                         const int place = found_at[j];
-                        const double c = ranked_value(sigmoid, score_of(place), bias_of(place), top, inv);
+                        const double c = ranked_value(sigmoid, score_of(place), bias_of(place), top, of_sum);
                         found[j] = (float)c;
                         first[j] = isfinite(c) ? (float)(c - (double)(float)c) : 0.f;
                     }
@@ -592,19 +617,11 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
                     for (int j = gl; j < n; j += L) {
                         const float c = found[j], d = first[j];
                         int rank = 0;
-                        bool open = false;
                         for (int q = 0; q < n; ++q) {
                             const float e = found[q], f = first[q];
                             rank += e > c || (e == c && (f > d || (f == d && q < j))) ? 1 : 0;
-                            if (!sigmoid && q != j) {  // what the sum's own error may turn round
-                                const int p = found_at[j], r = found_at[q];
-                                const float apart = fabsf(bias_of(p) - bias_of(r));
-                                open |= !(fabsf((c - e) + (d - f)) > fmaf(apart, 3e-6f, 1e-12f)) &&
-                                        (score_of(p) != score_of(r) || apart != 0.f);
-                            }
                         }
                         first_at[rank] = found_at[j];
-                        exact |= open && rank <= k;
                     }
                 }
                 __syncwarp();
@@ -723,6 +740,10 @@ int route_team(const RouteArgs& a, int size_of, RoutePlan* p) {
         if (sub > 32) continue;
         p->per_group = per;
         p->sub = sub;
+        p->shift = 0;
+        while (1 << p->shift < per) ++p->shift;
+        p->of_size = 1.00001f / (float)p->size;  // (e / size is at least 1 / 1,024 below the next whole number)
+        p->of_sub = 1.00001f / (float)sub;
         return L;
     }
     return 0;
