@@ -136,8 +136,8 @@ def load_library(path: str | None = None):
             getattr(lib, f"iso_{name}_loss").restype = ci
         for name in ("iso_token_logp", "iso_token_logp_backward", "iso_balance_loss_backward"):
             getattr(lib, name).restype = ci
-        lib.iso_route.argtypes = scores + [ci, vp, vp] + [ci] * 5 + [cf] + [vp] * 4
-        lib.iso_route_backward.argtypes = scores + [ci, ci, ci, cf] + [vp] * 4 + [i64, vp]
+        lib.iso_route.argtypes = scores + [ci, vp, vp] + [ci] * 5 + [cf] + [vp] * 5
+        lib.iso_route_backward.argtypes = scores + [ci, ci, ci, cf] + [vp] * 5 + [i64, vp]
         lib.iso_beam_choose_workspace_bytes.argtypes = [i64, i64, i64, ci, ci]
         lib.iso_beam_choose_workspace_bytes.restype = sz
         lib.iso_beam_choose.argtypes = [vp, ci] + [i64] * 4 + [vp, vp, i64, ctypes.c_double, ci,

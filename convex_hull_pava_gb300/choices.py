@@ -36,11 +36,11 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 
 class Route:
     """What :func:`iso_route` returns."""
-    _fields = ("gates", "experts", "counts", "score", "renormalize", "scale")
+    _fields = ("gates", "experts", "counts", "score", "renormalize", "scale", "picked")
     __slots__ = _fields
 
-    def __init__(self, gates, experts, counts, score, renormalize, scale):
-        self.gates, self.experts, self.counts = gates, experts, counts
+    def __init__(self, gates, experts, counts, score, renormalize, scale, picked=None):
+        self.gates, self.experts, self.counts, self.picked = gates, experts, counts, picked
         self.score, self.renormalize, self.scale = score, renormalize, scale
 
     def __iter__(self):
@@ -90,14 +90,16 @@ def _router(logits, top_k, score):
 
 def iso_route(logits, top_k: int, mask=None, *, score: str = "softmax", bias=None, groups: int = 1,
               top_groups: int = 1, group_best: int = 2, renormalize: bool = False,
-              scale: float = 1.0, stream=None):
+              scale: float = 1.0, want_grad: bool = True, stream=None):
     """A router's choice of ``top_k`` experts for each row of ``logits`` ``[tokens, experts]``, by
     "softmax" or "sigmoid" scores and a ``bias`` (float32 ``[experts]``) that moves the choice and
     not the gates; with ``groups`` above 1, among the experts of the ``top_groups`` groups whose
     ``group_best`` (1 or 2) largest scores have the largest sum.  ``mask``: bool or uint8
     ``[tokens]``, false where a token takes no part.  Returns a :class:`Route`: ``gates`` (float32
     ``[tokens, top_k]``: ``scale`` times the scores, with ``renormalize`` divided by their sum),
-    ``experts`` (int32, -1 where none), ``counts`` (int64 ``[experts]``)."""
+    ``experts`` (int32, -1 where none), ``counts`` (int64 ``[experts]``), ``picked`` (with "sigmoid": the
+    scores of the chosen, float32, which the backward takes instead of gathering them; None
+    without ``want_grad``)."""
     torch, code, tokens, experts, stride, dev, how = _router(logits, top_k, score)
     if mask is not None:
         _mask(mask, "mask", logits.shape[:1], dev)
@@ -114,16 +116,17 @@ def iso_route(logits, top_k: int, mask=None, *, score: str = "softmax", bias=Non
         with there:
             return iso_route(logits, top_k, mask, score=score, bias=bias, groups=groups,
                              top_groups=top_groups, group_best=group_best, renormalize=renormalize,
-                             scale=scale)
+                             scale=scale, want_grad=want_grad)
     counts = torch.empty(experts, dtype=torch.int64, device=dev)
     chosen = torch.empty((tokens, top_k), dtype=torch.int32, device=dev)
     gates = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
     renormalize = bool(renormalize)
+    picked = torch.empty((tokens, top_k), dtype=torch.float32, device=dev) if how and want_grad else None
     _done(_obj._abi.iso_route(
         logits.data_ptr(), code, tokens, experts, stride, top_k, _ptr(mask), _ptr(bias), how, groups,
         top_groups, group_best, renormalize, scale, counts.data_ptr(), chosen.data_ptr(),
-        gates.data_ptr(), _obj._raw_stream(dev.index)), "iso_route")
-    return Route(gates, chosen, counts, score, renormalize, scale)
+        gates.data_ptr(), _ptr(picked), _obj._raw_stream(dev.index)), "iso_route")
+    return Route(gates, chosen, counts, score, renormalize, scale, picked)
 
 
 def iso_route_backward(grad_gates, logits, result, *, out=None, stream=None):
@@ -146,8 +149,8 @@ def iso_route_backward(grad_gates, logits, result, *, out=None, stream=None):
         out_stride = _check_out(out, logits)
     _done(_obj._abi.iso_route_backward(
         logits.data_ptr(), code, tokens, experts, stride, shape[1], how, result.renormalize,
-        result.scale, result.experts.data_ptr(), result.gates.data_ptr(), grad_gates.data_ptr(),
-        out.data_ptr(), out_stride, _obj._raw_stream(dev.index)), "iso_route_backward")
+        result.scale, result.experts.data_ptr(), result.gates.data_ptr(), _ptr(result.picked),
+        grad_gates.data_ptr(), out.data_ptr(), out_stride, _obj._raw_stream(dev.index)), "iso_route_backward")
     return out
 
 
@@ -305,16 +308,16 @@ def _make():
     class _Route(torch.autograd.Function):
         @staticmethod
         def forward(ctx, logits, top_k, mask, options):
-            r = iso_route(logits, top_k, mask, **options)
-            ctx.save_for_backward(logits, r.gates, r.experts, r.counts)
+            r = iso_route(logits, top_k, mask, want_grad=ctx.needs_input_grad[0], **options)
+            ctx.save_for_backward(logits, r.gates, r.experts, r.counts, r.picked)
             ctx.how = (r.score, r.renormalize, r.scale)
             ctx.mark_non_differentiable(r.experts, r.counts)
             return r.gates, r.experts, r.counts
 
         @staticmethod
         def backward(ctx, g, *_):
-            logits, gates, experts, counts = ctx.saved_tensors
-            d = iso_route_backward(g.contiguous(), logits, Route(gates, experts, counts, *ctx.how))
+            logits, gates, experts, counts, picked = ctx.saved_tensors
+            d = iso_route_backward(g.contiguous(), logits, Route(gates, experts, counts, *ctx.how, picked))
             # (a kernel's output, without a graph of its own: its derivative is refused)
             if torch.is_grad_enabled() and logits.requires_grad:
                 d = _FirstOnly.apply(d, logits)

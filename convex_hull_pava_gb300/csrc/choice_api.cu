@@ -53,7 +53,8 @@ extern "C" {
 
 iso_status iso_route(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t stride, int top_k,
                      const uint8_t* mask, const float* bias, int score, int groups, int top_groups, int group_best,
-                     int renormalize, float scale, int64_t* counts, int32_t* chosen, float* gates, void* stream) {
+                     int renormalize, float scale, int64_t* counts, int32_t* chosen, float* gates, float* picked,
+                     void* stream) {
     if (!route_ok(dtype, tokens, experts, stride, 0, top_k, score, renormalize, scale) || !counts ||
         (tokens > 0 && (!logits || !chosen || !gates)))
         return ISO_ERR_INVALID_ARG;
@@ -61,14 +62,14 @@ iso_status iso_route(const void* logits, int dtype, int64_t tokens, int64_t expe
         top_k > top_groups * (experts / groups) || (groups > 1 && group_best != 1 && group_best != 2))
         return ISO_ERR_INVALID_ARG;
     const isodev::RouteArgs a{logits, tokens, (int)experts, stride,     top_k,       mask,  bias,
-                              score,  groups, top_groups,   group_best, renormalize, scale};
+                              score,  groups, top_groups,   group_best, renormalize, scale, picked};
     isodev::prof_start(static_cast<cudaStream_t>(stream));
     return from_cuda(isodev::route(dtype, a, counts, chosen, gates, static_cast<cudaStream_t>(stream)));
 }
 
 iso_status iso_route_backward(const void* logits, int dtype, int64_t tokens, int64_t experts, int64_t stride,
                               int top_k, int score, int renormalize, float scale, const int32_t* chosen,
-                              const float* gates, const float* grad_gates, void* dlogits, int64_t out_stride,
+                              const float* gates, const float* picked, const float* grad_gates, void* dlogits, int64_t out_stride,
                               void* stream) {
     if (!route_ok(dtype, tokens, experts, stride, 0, top_k, score, renormalize, scale) ||
         !rows_ok(dtype, tokens, experts, out_stride, experts))
@@ -85,7 +86,7 @@ iso_status iso_route_backward(const void* logits, int dtype, int64_t tokens, int
     a.renormalize = renormalize;
     a.scale = scale;
     isodev::prof_start(static_cast<cudaStream_t>(stream));
-    return from_cuda(isodev::route_backward(dtype, a, chosen, gates, grad_gates, dlogits, out_stride,
+    return from_cuda(isodev::route_backward(dtype, a, chosen, gates, picked, grad_gates, dlogits, out_stride,
                                             static_cast<cudaStream_t>(stream)));
 }
 

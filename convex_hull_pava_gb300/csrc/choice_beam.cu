@@ -173,7 +173,7 @@ struct PartNote {
 // a group of parts first, the next words always on their way, and ranks all of them after that.
 template <class T>
 __global__ void __launch_bounds__(kRowThreads, kRowCtas)
-beam_rows_kernel(BeamArgs a, BeamParts parts, float scale, int rows) {
+beam_rows_kernel(const __grid_constant__ BeamArgs a, const __grid_constant__ BeamParts parts, float scale, int rows) {
     constexpr int N = Word<T>::N;
     __shared__ float most[kMostBatches][kRowThreads];
     __shared__ uint8_t part_of[kMostBatches];
@@ -619,7 +619,7 @@ __device__ __noinline__ void join_by_rounds(const BeamArgs& a, const ItemContinu
 // lse's error (off) theirs is nothing (2^-46).
 template <class T>
 __global__ void __launch_bounds__(kJoinThreads)
-beam_join_kernel(BeamArgs a, BeamParts parts, BeamScale sc) {
+beam_join_kernel(const __grid_constant__ BeamArgs a, const __grid_constant__ BeamParts parts, const __grid_constant__ BeamScale sc) {
     __shared__ ItemBeams beams;
     __shared__ uint64_t key_of[kRemembered];  // the first continuations' keys
     __shared__ Continuation list[kJoinList], sorted[kJoinList];

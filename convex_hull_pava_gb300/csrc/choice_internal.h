@@ -20,11 +20,13 @@ struct RouteArgs {
     const float* bias;
     int score, groups, top_groups, group_best, renormalize;
     float scale;
+    float* picked;  // [tokens, top_k] the chosen's scores, written; or NULL
 };
 cudaError_t route(int dtype, const RouteArgs& a, int64_t* counts, int32_t* chosen, float* gates,
                   cudaStream_t st);
+// `picked`: as the forward left them, or NULL: the chosen's scores are read from the rows.
 cudaError_t route_backward(int dtype, const RouteArgs& a, const int32_t* chosen, const float* gates,
-                           const float* grad_gates, void* out, int64_t out_stride, cudaStream_t st);
+                           const float* picked, const float* grad_gates, void* out, int64_t out_stride, cudaStream_t st);
 
 // A step of beam search: rows of scores, `beams` of them a batch item.
 struct BeamArgs {

@@ -12,7 +12,7 @@ namespace {
 // shared memory, a warp's tokens beside one another; the next tokens' scores are on their way meanwhile.
 template <class T, int G, int EPL>
 __global__ void __launch_bounds__(256)
-route_dense_backward_kernel(RouteArgs a, int whole, const int32_t* chosen, const float* gates, const float* grad_gates,
+route_dense_backward_kernel(const __grid_constant__ RouteArgs a, int whole, const int32_t* chosen, const float* gates, const float* grad_gates,
                             T* out, int64_t out_stride) {
     constexpr int W = 256 / 32, TPW = 32 / G;
     __shared__ __align__(16) float extra[W * TPW][G * EPL];
@@ -65,11 +65,11 @@ route_dense_backward_kernel(RouteArgs a, int whole, const int32_t* chosen, const
 // The others: the chosen alone have a gradient.  A warp has as many tokens at a time as its lanes have
 // places (`places` lanes a token, a power of two); their rows, zero but for the chosen, lie in shared memory
 // in the output's type and are stored from there, 16 bytes a lane.  The next tokens' choice is asked
-// for one turn ahead, and its scores as soon as that is there.  `chunk`: bytes of a store.
+// for one turn ahead, and (where the forward has not kept them) its scores as soon as that is there.  `chunk`: bytes of a store.
 template <class T>
 __global__ void __launch_bounds__(256)
-route_sparse_backward_kernel(RouteArgs a, int places, int tokens, int chunk, const int32_t* chosen, const float* gates,
-                             const float* grad_gates, T* out, int64_t out_stride) {
+route_sparse_backward_kernel(const __grid_constant__ RouteArgs a, int places, int tokens, int chunk, const int32_t* chosen, const float* gates,
+                             const float* picked, const float* grad_gates, T* out, int64_t out_stride) {
     extern __shared__ __align__(16) char rows[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts, k = a.top_k;
     const int place = lane & (places - 1), tw = lane / places;
@@ -88,11 +88,12 @@ route_sparse_backward_kernel(RouteArgs a, int places, int tokens, int chunk, con
             slot = chosen[t * k + place];
             gate = gates[t * k + place];
             g = grad_gates[t * k + place];
+            if (picked) x = picked[t * k + place];
             if (slot < 0 || slot >= E) slot = -1;
         }
     };
     auto score = [&](int64_t first) {
-        if (sigmoid && slot >= 0) x = to_f32(base[(first + tw) * a.stride + slot]);
+        if (sigmoid && !picked && slot >= 0) x = to_f32(base[(first + tw) * a.stride + slot]);
     };
     int64_t first = ((int64_t)blockIdx.x * 8 + warp) * tokens;
     fetch(first);
@@ -144,7 +145,7 @@ cudaError_t route(int dtype, const RouteArgs& a, int64_t* counts, int32_t* chose
 }
 
 cudaError_t route_backward(int dtype, const RouteArgs& a, const int32_t* chosen, const float* gates,
-                           const float* grad_gates, void* out, int64_t out_stride, cudaStream_t st) {
+                           const float* picked, const float* grad_gates, void* out, int64_t out_stride, cudaStream_t st) {
     return by_type(dtype, [&](auto t) {
         using T = decltype(t);
         constexpr int N = Word<T>::N;
@@ -165,8 +166,8 @@ cudaError_t route_backward(int dtype, const RouteArgs& a, const int32_t* chosen,
         const int pitch = (a.experts * (int)sizeof(T) + 15) / 16 * 16;
         const int tokens = std::max(1, std::min(32 / places, 4096 / pitch));  // of a warp at a time: up to 4 KB
         const int chunk = chunks_fit(out, a.tokens, out_stride, a.experts, N, sizeof(T)) ? 16 : (int)sizeof(T);
-        const int64_t grid = std::min<int64_t>((a.tokens + 8 * tokens - 1) / (8 * tokens), 152 * 6);
-        route_sparse_backward_kernel<T><<<(unsigned)grid, 256, 8 * tokens * pitch, st>>>(a, places, tokens, chunk, chosen, gates, grad_gates, to, out_stride);
+        const int64_t grid = std::min<int64_t>((a.tokens + 8 * tokens - 1) / (8 * tokens), 152 * 24);  // (152 * 6: 22.3 us and not 20.6)
+        route_sparse_backward_kernel<T><<<(unsigned)grid, 256, 8 * tokens * pitch, st>>>(a, places, tokens, chunk, chosen, gates, picked, grad_gates, to, out_stride);
         const cudaError_t e = cudaGetLastError();
         prof_mark(st, "route_backward");
         return e;

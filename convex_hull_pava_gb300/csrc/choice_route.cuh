@@ -35,8 +35,9 @@ __device__ __forceinline__ uint64_t order_key(double v) {
 // The choice of one token by a warp in 64 bits: `c` has room for its experts.  Where there is no
 // bias the order of c is that of x, which needs no rounding: c holds x then.
 template <class T>
-__device__ __noinline__ void choose_exact(const RouteArgs& a, const T* x, double* c, int32_t* to, float* gate_to,
+__device__ __noinline__ void choose_exact(const RouteArgs& a, int64_t t, double* c, int32_t* chosen, float* gates,
                                           uint32_t* counts) {
+    const T* const x = static_cast<const T*>(a.x) + t * a.stride;
     const int lane = threadIdx.x & 31, E = a.experts;
     float top = -INFINITY;
     bool bad = false;  // a NaN or +inf: no probabilities
@@ -118,8 +119,10 @@ __device__ __noinline__ void choose_exact(const RouteArgs& a, const T* x, double
         s /= warp_add(s);
     }
     if (lane < a.top_k) {
-        to[lane] = mine;
-        gate_to[lane] = mine < 0 ? 0.f : bad ? NAN : (float)((double)a.scale * s);
+        const int64_t to = t * a.top_k + lane;
+        chosen[to] = mine;
+        if (a.picked) a.picked[to] = (float)v;
+        gates[to] = mine < 0 ? 0.f : bad ? NAN : (float)((double)a.scale * s);
         if (mine >= 0) atomicAdd(&counts[mine], 1u);
     }
     __syncwarp();
@@ -228,9 +231,8 @@ __device__ __noinline__ double inverse_sum(const T* x, int count, float m) {
 }
 
 constexpr int kFound = 32;  // candidates of a token
-constexpr int kTeamWarps = 6, kTeamThreads = 32 * kTeamWarps;
-template <class T>
-constexpr int team_ctas = sizeof(T) == 4 ? 3 : 4;  // an SM, by shared memory and registers
+constexpr int kTeamWarps = 4, kTeamThreads = 32 * kTeamWarps;
+constexpr int kTeamCtas = 4;  // an SM, by shared memory; 6 warps and 3 CTAs took 81 us of the largest case and not 75, 3 and 6 83'
 
 // Candidates: experts whose ranked value reaches a bound that top_k of them reach, the top_k-th largest of
 // the lanes' partial maxima (8 a lane), which the lanes sort and merge (LIST of them).  VALUES: what is
@@ -238,8 +240,8 @@ constexpr int team_ctas = sizeof(T) == 4 ? 3 : 4;  // an SM, by shared memory an
 // candidates' values or groups' sums are nearer to each other than float32 tells they are formed again in
 // 64 bits; tokens with NaN, without probabilities, or with too many candidates are chosen by choose_exact.
 template <class T, int L, int EPL, bool VALUES, int LIST>
-__global__ void __launch_bounds__(kTeamThreads, team_ctas<T>)
-route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float* gates) {
+__global__ void __launch_bounds__(kTeamThreads, kTeamCtas)
+route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RoutePlan pl, int64_t* counts, int32_t* chosen, float* gates) {
     constexpr int N = 16 / (int)sizeof(T), TPW = 32 / L, WORDS = EPL / N, LANE = (WORDS | 1) * 16, BIAS = (EPL / 4 | 1) * 4;
     constexpr int PER = EPL / 8;  // experts of a partial maximum
     extern __shared__ __align__(16) char memory[];
@@ -531,9 +533,10 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
         }
         if (VALUES) bound -= unsure(sigmoid, bound, 1.f);
         bound = fmaxf(bound, __uint_as_float(0xff7fffffu));  // (the lowest)
-        unsigned mask = 0u;
+        unsigned mask = 0u;  // by the signs of v - bound
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) mask |= (v[i] >= bound ? 1u : 0u) << i;
+        for (int i = EPL - 1; i >= 0; --i) mask = __funnelshift_l(__float_as_uint(v[i] - bound), mask, 1);
+        mask = ~mask & (EPL == 32 ? ~0u : (1u << (EPL & 31)) - 1u);
         exact &= on;
         if (!kept || !on || exact) mask = 0u;
         // the candidates in the order of the experts
@@ -653,15 +656,17 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
         if (t < a.tokens && !exact) {
             for (int i = gl; i < k; i += L) {
                 int e = -1;
-                float gate = 0.f;
+                float gate = 0.f, x = 0.f;
                 if (i < n) {
                     const int place = first_at[i];
+                    x = score_of(place);
                     e = sh_base[place / EPL] + place % EPL;
                     gate = first[i] * factor;
                     atomicAdd(&sh_n[e], 1u);
                 }
                 chosen[t * k + i] = e;
                 gates[t * k + i] = gate;
+                if (a.picked) a.picked[t * k + i] = x;
             }
         }
         unsigned left = __ballot_sync(~0u, exact && gl == 0);
@@ -669,7 +674,7 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
         if (left) {
             for (; left; left &= left - 1u) {
                 const int64_t which = tile * TPW + (__ffs(left) - 1) / L;
-                choose_exact(a, base + which * a.stride, reinterpret_cast<double*>(stage), chosen + which * k, gates + which * k, sh_n);
+                choose_exact<T>(a, which, reinterpret_cast<double*>(stage), chosen, gates, sh_n);
             }
             fill(stage);
             __syncwarp();
@@ -691,13 +696,12 @@ route_kernel(RouteArgs a, RoutePlan pl, int64_t* counts, int32_t* chosen, float*
 // larger than its lanes'.
 template <class T>
 __global__ void __launch_bounds__(kRouteThreads)
-route_exact_kernel(RouteArgs a, int64_t* counts, int32_t* chosen, float* gates) {
+route_exact_kernel(const __grid_constant__ RouteArgs a, int64_t* counts, int32_t* chosen, float* gates) {
     extern __shared__ double values[];  // [kRouteWarps][experts]
     __shared__ uint32_t sh_n[ISO_MAX_EXPERTS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.experts;
     for (int e = threadIdx.x; e < E; e += kRouteThreads) sh_n[e] = 0u;
     __syncthreads();
-    const T* const base = static_cast<const T*>(a.x);
     for (int64_t t = (int64_t)blockIdx.x * kRouteWarps + warp; t < a.tokens; t += (int64_t)gridDim.x * kRouteWarps) {
         if (a.mask && !a.mask[t]) {
             if (lane < a.top_k) {
@@ -706,7 +710,7 @@ route_exact_kernel(RouteArgs a, int64_t* counts, int32_t* chosen, float* gates) 
             }
             continue;
         }
-        choose_exact(a, base + t * a.stride, values + warp * E, chosen + t * a.top_k, gates + t * a.top_k, sh_n);
+        choose_exact<T>(a, t, values + warp * E, chosen, gates, sh_n);
     }
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += kRouteThreads)
@@ -757,7 +761,7 @@ cudaError_t route_rows(const RouteArgs& a, int64_t* counts, int32_t* chosen, flo
     const int L = route_team(a, sizeof(T), &p);
     const int warps = L ? kTeamWarps : kRouteWarps;
     const int64_t tiles = L ? (a.tokens + 32 / L - 1) / (32 / L) : a.tokens;
-    const int64_t grid = std::min<int64_t>((tiles + warps - 1) / warps, 152 * (L ? team_ctas<T> : 4));
+    const int64_t grid = std::min<int64_t>((tiles + warps - 1) / warps, 152 * (L ? kTeamCtas : 4));
     p.counted = L && grid == 1;
     if (!p.counted) {
         const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)a.experts * sizeof(int64_t), st);

@@ -527,6 +527,8 @@ iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t toke
  *  chosen     [tokens, top_k] int32, written: the experts by decreasing c; -1 where no open
  *             expert is left or the token takes no part.
  *  gates      [tokens, top_k] float32, written: 0 where chosen is -1.
+ *  picked     [tokens, top_k] float32, written: the scores of the chosen, for the backward of score 1
+ *             (0 where chosen is -1); or NULL.
  *             With score 0, a NaN or +inf among the scores of a token makes its gates and its
  *             gradient NaN; its experts are then the open ones by bias and index (c = bias_e).
  *             With score 1 a NaN closes its own expert only.
@@ -535,6 +537,8 @@ iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t toke
  * bias carry none).
  *
  *  chosen, gates  as the forward wrote them for the same logits.
+ *  picked         as the forward wrote them, or NULL: score 1 then reads them from the logits (1 M places of
+ *                 a 134 MB batch took as long as writing the gradient); score 0 does not use them.
  *  grad_gates     [tokens, top_k] float32.
  *  dlogits        [tokens, experts] of dtype, row t at t * out_stride, written; it may be the
  *                 logits themselves (out_stride == stride).
@@ -545,11 +549,12 @@ iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t toke
 iso_status iso_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t stride,
                      int top_k, const uint8_t *mask, const float *bias, int score, int groups,
                      int top_groups, int group_best, int renormalize, float scale, int64_t *counts,
-                     int32_t *chosen, float *gates, void *stream);
+                     int32_t *chosen, float *gates, float *picked, void *stream);
 iso_status iso_route_backward(const void *logits, int dtype, int64_t tokens, int64_t experts,
                               int64_t stride, int top_k, int score, int renormalize, float scale,
-                              const int32_t *chosen, const float *gates, const float *grad_gates,
-                              void *dlogits, int64_t out_stride, void *stream);
+                              const int32_t *chosen, const float *gates, const float *picked,
+                              const float *grad_gates, void *dlogits, int64_t out_stride,
+                              void *stream);
 
 /*
  * iso_beam_choose -- a step of beam search: of all continuations of a batch item's beams, the

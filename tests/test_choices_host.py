@@ -15,7 +15,7 @@ BAD = chp.ISO_ERR_INVALID_ARG
 
 def route_args(**change):
     a = dict(logits=P, dtype=0, tokens=4, experts=16, stride=16, top_k=2, mask=None, bias=None, score=0, groups=1,
-             top_groups=1, group_best=2, renormalize=0, scale=1.0, counts=P, chosen=P, gates=P, stream=None)
+             top_groups=1, group_best=2, renormalize=0, scale=1.0, counts=P, chosen=P, gates=P, picked=None, stream=None)
     a.update(change)
     return list(a.values())
 
@@ -37,7 +37,7 @@ def test_route_refusals(change):
     dict(score=2), dict(renormalize=-1), dict(scale=0.0), dict(out_stride=15), dict(tokens=-3), dict(dtype=7)])
 def test_route_backward_refusals(change):
     a = dict(logits=P, dtype=0, tokens=4, experts=16, stride=16, top_k=2, score=0, renormalize=0, scale=1.0, chosen=P,
-             gates=P, grad=P, out=P, out_stride=16, stream=None)
+             gates=P, picked=None, grad=P, out=P, out_stride=16, stream=None)
     a.update(change)
     assert chp.load_library().iso_route_backward(*a.values()) == BAD
 
