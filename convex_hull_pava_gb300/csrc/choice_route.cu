@@ -103,9 +103,9 @@ route_sparse_backward_kernel(const __grid_constant__ RouteArgs a, int places, in
         const int at = slot;
         const float own = gate, of = g, own_x = x;
         fetch(first + step);
-        float dot = at >= 0 ? own * of : 0.f;
+        float dot = at >= 0 ? own / a.scale * of : 0.f;  // (of one alone the gradient itself)
         for (int o = places / 2; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        float put = own * (a.renormalize ? of - dot / a.scale : of);
+        float put = own * (a.renormalize ? __fsub_rn(of, dot) : of);
         if (sigmoid) put *= 1.f / (1.f + expf(own_x));  // 1 - s
         T* const row = reinterpret_cast<T*>(mine + tw * pitch);
         if (at >= 0) row[at] = from_f32<T>(put);

@@ -638,7 +638,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
 #pragma unroll
             for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
         }
-        float factor = a.scale, sum = 0.f;
+        float sum = 0.f;
         for (int i = gl; i < filled; i += L) {
             const float x = score_of(first_at[i]);
             const float s = a.score == ISO_ROUTE_SIGMOID ? rcp(1.f + ex2(x * -kLog2e))
@@ -650,7 +650,8 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
         if (a.renormalize) {
             sum = group_add<L>(sum);
             if (n > 0 && !(sum > 1e-30f)) exact = true;  // sigmoids that are 0 in float32
-            factor *= 1.f / sum;
+        } else {
+            sum = 1.f;
         }
         exact = (__ballot_sync(~0u, exact) & team) != 0u;
         if (t < a.tokens && !exact) {
@@ -661,7 +662,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
                     const int place = first_at[i];
                     x = score_of(place);
                     e = sh_base[place / EPL] + place % EPL;
-                    gate = first[i] * factor;
+                    gate = a.scale * (first[i] / sum);  // (of one alone the scale itself: its gradient is 0)
                     atomicAdd(&sh_n[e], 1u);
                 }
                 chosen[t * k + i] = e;

@@ -180,6 +180,22 @@ def test_route_closed_nan_and_infinite(cuda_ok, n, groups, dtype):
                             top_groups=max(1, groups - 1))
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_route_one_renormalised_gate(cuda_ok, dtype, score):
+    """The renormalised gate of one expert alone is the scale, whatever its score, and has no gradient at all."""
+    from convex_hull_pava_gb300 import choices
+    rng = np.random.default_rng(8)
+    for n, k, groups, scale in ((40, 1, 1, 2.5), (256, 1, 8, 0.3), (1000, 1, 1, 1.0), (90, 1, 9, 7.0), (8, 4, 1, 2.5)):
+        v = 2.0 * rng.standard_normal((500, n))
+        if k > 1:
+            v[:, 1:] = -np.inf   # more places than open experts
+        r = choices.iso_route(rows_of(v, dtype), k, score=score, groups=groups, renormalize=True, scale=scale)
+        assert (wide(r.gates)[:, 0] == np.float32(scale)).all() and (wide(r.gates)[:, 1:] == 0).all()
+        d = choices.iso_route_backward(put(rng.standard_normal((500, k))), rows_of(v, dtype), r)
+        assert (wide(d) == 0).all()
+
+
 def test_route_empty(cuda_ok):
     import torch
     from convex_hull_pava_gb300 import choices
