@@ -10,6 +10,7 @@ namespace {
 
 // Softmax without renormalisation: all elements have a gradient.  The gates' part of each is put together in
 // shared memory, a warp's tokens beside one another; the next tokens' scores are on their way meanwhile.
+// Bound by HBM: 131,072 x 256 float32 in 44.6 us (268 MB, 6.0 TB/s; a plain copy of them takes 41.2).
 template <class T, int G, int EPL>
 __global__ void __launch_bounds__(256)
 route_dense_backward_kernel(const __grid_constant__ RouteArgs a, int whole, const int32_t* chosen, const float* gates, const float* grad_gates,
@@ -66,6 +67,9 @@ route_dense_backward_kernel(const __grid_constant__ RouteArgs a, int whole, cons
 // places (`places` lanes a token, a power of two); their rows, zero but for the chosen, lie in shared memory
 // in the output's type and are stored from there, 16 bytes a lane.  The next tokens' choice is asked
 // for one turn ahead, and (where the forward has not kept them) its scores as soon as that is there.  `chunk`: bytes of a store.
+// Bound by HBM's writes: 131,072 x 256 float32 in 20.3 us (6.6 TB/s; zeroing them takes 19.4).  With the
+// chosen's scores gathered from the rows 43 us, with float32 rows in shared memory and a token a group of
+// lanes 53.
 template <class T>
 __global__ void __launch_bounds__(256)
 route_sparse_backward_kernel(const __grid_constant__ RouteArgs a, int places, int tokens, int chunk, const int32_t* chosen, const float* gates,
