@@ -242,19 +242,18 @@ def iso_beam_reorder(states, beams, *, stream=None):
     rows = batch * width
     if not all(issubclass(kind, torch.Tensor) for kind in set(map(type, states))):
         raise ValueError("states must be tensors")
-    # (states of one call mostly have one layout: it is looked at once)
-    kinds = [(x.shape, x.stride(), x.dtype, x.device, x.requires_grad) for x in states]
-    layouts = {}
-    for x, kind in zip(states, kinds):
-        if kind not in layouts:
-            if kind[3] != dev:
-                raise ValueError(f"states must be tensors on {dev}")
-            if kind[4] and torch.is_grad_enabled():
-                raise ValueError("states are moved in place: they may not require a gradient")
-            layouts[kind] = _described(x, rows, batch)
     words, bases = [], set()
-    for x, kind in zip(states, kinds):
-        got = layouts[kind]
+    layouts, last, got = {}, None, ()
+    for x in states:
+        kind = (x.shape, x.stride(), x.dtype, x.device, x.requires_grad)
+        if kind != last:   # (states of one call mostly have one layout)
+            got, last = layouts.get(kind), kind
+            if got is None:
+                if kind[3] != dev:
+                    raise ValueError(f"states must be tensors on {dev}")
+                if kind[4] and torch.is_grad_enabled():
+                    raise ValueError("states are moved in place: they may not require a gradient")
+                got = layouts[kind] = _described(x, rows, batch)
         if got:
             base = x.data_ptr()
             bases.add(base)

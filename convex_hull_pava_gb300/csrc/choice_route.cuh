@@ -242,7 +242,7 @@ constexpr int kTeamCtas = 4;  // an SM, by shared memory; 6 warps and 3 CTAs too
 // candidates are chosen by choose_exact.
 // Neighbouring experts to a lane, and not interleaved ones, so that a lane's are of one group and its
 // candidates in the experts' order; rows come through shared memory for that, one tile ahead of its turn.
-// Bound by instructions: 131,072 x 256 float32, sigmoid with 8 groups and k = 8, in 75 us (1.8 TB/s; 370
+// Bound by instructions: 131,072 x 256 float32, sigmoid with 8 groups and k = 8, in 75 us (1.8 TB/s; 356
 // instructions a token, two thirds of them minima, maxima and comparisons at half rate), without groups and
 // bias 50 us.  One warp a token in 64 bits throughout took 4.4 ms, 8 lanes a token without the packing of
 // sigmoids two to a quotient and with the group's maxima found apart 131.

@@ -1,7 +1,8 @@
 /*
  * iso.h -- C ABI of the GB300 (sm_103a) isotonic-regression library libiso.so,
  * and of the training objectives beside it (token log-probabilities, policy,
- * preference and balance losses; see "Training objectives" below).
+ * preference and balance losses; see "Training objectives" below) and the choices
+ * over rows of scores (a router's experts, beam search, the beams' states).
  *
  * The operation ("Merge Hulls Without Copying Vertices: GPU Isotonic Regression",
  * Section 2.1, eq. (1)): for every row y_1..y_n with weights w_i > 0, the unique
