@@ -231,8 +231,13 @@ __device__ __noinline__ double inverse_sum(const T* x, int count, float m) {
 }
 
 constexpr int kFound = 32;  // candidates of a token
-constexpr int kTeamWarps = 4, kTeamThreads = 32 * kTeamWarps;
-constexpr int kTeamCtas = 4;  // an SM, by shared memory; 6 warps and 3 CTAs took 81 us of the largest case and not 75, 3 and 6 83'
+// Warps of a CTA and CTAs an SM, by shared memory and registers.  float32: 4 and 4 (6 and 3 took 81 us of
+// 131,072 x 256 and not 75, 3 and 6 83); 16 bits: 8 and 2, whose fewer CTAs add up fewer counts (16,384 x 128
+// in 12.5 us, 4 and 4 14.5).
+template <class T>
+constexpr int team_warps = sizeof(T) == 4 ? 4 : 8;
+template <class T>
+constexpr int team_ctas = sizeof(T) == 4 ? 4 : 2;
 
 // Candidates: experts whose ranked value reaches a bound that top_k of them reach, the top_k-th largest of
 // the lanes' partial maxima (8 a lane), which the lanes sort and merge (LIST of them).  VALUES: what is
@@ -247,9 +252,10 @@ constexpr int kTeamCtas = 4;  // an SM, by shared memory; 6 warps and 3 CTAs too
 // bias 50 us.  One warp a token in 64 bits throughout took 4.4 ms, 8 lanes a token without the packing of
 // sigmoids two to a quotient and with the group's maxima found apart 131.
 template <class T, int L, int EPL, bool VALUES, int LIST>
-__global__ void __launch_bounds__(kTeamThreads, kTeamCtas)
+__global__ void __launch_bounds__(32 * team_warps<T>, team_ctas<T>)
 route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RoutePlan pl, int64_t* counts, int32_t* chosen, float* gates) {
     constexpr int N = 16 / (int)sizeof(T), TPW = 32 / L, WORDS = EPL / N, LANE = (WORDS | 1) * 16, BIAS = (EPL / 4 | 1) * 4;
+    constexpr int kTeamWarps = team_warps<T>, kTeamThreads = 32 * kTeamWarps;
     constexpr int PER = EPL / 8;  // experts of a partial maximum
     extern __shared__ __align__(16) char memory[];
     __shared__ uint32_t sh_n[L * EPL];
@@ -449,6 +455,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
             const float value = pairs && two > -INFINITY ? one + two : one;
             const int own = gl >> pl.shift;
             int rank = 0;
+#pragma unroll 1
             for (int g = 0; g < a.groups; ++g) {
                 const float other = __shfl_sync(~0u, value, g * pl.per_group, L);
                 rank += other > value || (other == value && g < own) ? 1 : 0;
@@ -547,7 +554,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
         mask = ~mask & (EPL == 32 ? ~0u : (1u << (EPL & 31)) - 1u);
         exact &= on;
         if (!kept || !on || exact) mask = 0u;
-        // the candidates in the order of the experts
+        // the candidates in the order of the experts (loops as short code: it runs from the instruction cache)
         int at = __popc(mask), n;
 #pragma unroll
         for (int o = 1; o < L; o <<= 1) {
@@ -563,6 +570,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
         }
         for (; mask; mask &= mask - 1u) found_at[at++] = (uint16_t)(gl * EPL + __ffs(mask) - 1);
         __syncwarp();
+#pragma unroll 1
         for (int j = gl; j < ((n + 3) & ~3); j += L) {
             float c = -INFINITY;
             if (j < n) {
@@ -574,9 +582,11 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
         }
         __syncwarp();
         int ranks = 0;
+#pragma unroll 1
         for (int j = gl; j < n; j += L) {
             const float c = found[j];
             int rank = -1;  // the value itself is counted too
+#pragma unroll 1
             for (int q = 0; q < n; q += 4) {
                 const float4 f = *reinterpret_cast<const float4*>(&found[q]);
                 rank += (f.x >= c) + (f.y >= c) + (f.z >= c) + (f.w >= c);
@@ -647,6 +657,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
             for (int o = L / 2; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
         }
         float sum = 0.f;
+#pragma unroll 1
         for (int i = gl; i < filled; i += L) {
             const float x = score_of(first_at[i]);
             const float s = a.score == ISO_ROUTE_SIGMOID ? rcp(1.f + ex2(x * -kLog2e))
@@ -663,6 +674,7 @@ route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ RouteP
         }
         exact = (__ballot_sync(~0u, exact) & team) != 0u;
         if (t < a.tokens && !exact) {
+#pragma unroll 1
             for (int i = gl; i < k; i += L) {
                 int e = -1;
                 float gate = 0.f, x = 0.f;
@@ -768,9 +780,10 @@ template <class T>
 cudaError_t route_rows(const RouteArgs& a, int64_t* counts, int32_t* chosen, float* gates, cudaStream_t st) {
     RoutePlan p{};
     const int L = route_team(a, sizeof(T), &p);
+    constexpr int kTeamWarps = team_warps<T>, kTeamThreads = 32 * kTeamWarps;
     const int warps = L ? kTeamWarps : kRouteWarps;
     const int64_t tiles = L ? (a.tokens + 32 / L - 1) / (32 / L) : a.tokens;
-    const int64_t grid = std::min<int64_t>((tiles + warps - 1) / warps, 152 * (L ? kTeamCtas : 4));
+    const int64_t grid = std::min<int64_t>((tiles + warps - 1) / warps, 152 * (L ? team_ctas<T> : 4));
     p.counted = L && grid == 1;
     if (!p.counted) {
         const cudaError_t e = cudaMemsetAsync(counts, 0, (size_t)a.experts * sizeof(int64_t), st);
