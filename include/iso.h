@@ -497,8 +497,9 @@ iso_status iso_balance_loss_backward(const void *logits, int dtype, int64_t toke
  * Conventions, beside those of the objectives (types, strides and limits of the
  * scores are theirs):
  *  - A choice is that of the exact values: where rounding could change an order,
- *    the values are formed again with about 2^-50 (route) or 2^-36 (beams) of
- *    relative error.  Equal values go to the lowest index (beam first, then token).
+ *    the values are formed again: scores to about 2^-50 of themselves, the sums of
+ *    exponentials that they are taken against to about 2^-36.  Equal values go to
+ *    the lowest index (beam first, then token).
  *  - A score of -inf is closed and never chosen, nor is a NaN.  Places for which
  *    nothing is left hold -1.
  *  - Results do not depend on timing: the same call gives the same bits.
